@@ -5,10 +5,21 @@ calls the ``ht_*`` entry points.  No arithmetic of the method happens here.
     pw  = pack(W, fmt)                 # PackedLinear (owns its buffer)
     y   = linear(pw, x_bf16)           # fp32 [M, N]
     y   = mlp([pw0, pw1, ...], x_bf16) # Linear + ReLU per layer
+
+and, between the q|k|v and the output linear of a transformer layer, over a
+paged cache of keys and values in 8 bits (formats and formulas in ht.h):
+
+    codes, scales = kv_cache(n_pages, n_kv_heads, head_dim, device)
+    step = kv_plan(q_len, kv_len, owned, table, free_pages, n_free, T)
+    q, k = qk_norm_rope(q, k, step.positions, inv_freq, q_weight=..., k_weight=...)
+    kv_write(k, v, step.slots, codes, scales)
+    o    = kv_attention(q, codes, scales, table, step.cu_q, step.kv_len, max_q)
 """
 from __future__ import annotations
 
+import math
 from dataclasses import dataclass
+from typing import NamedTuple
 
 import torch
 
@@ -171,3 +182,232 @@ def mlp(layers: list, x: torch.Tensor, dump: bool = False, out: torch.Tensor | N
             off += M * pw.N
         return y, slabs
     return y
+
+
+# -----------------------------------------------------------------------------
+# Attention beside the linears
+# -----------------------------------------------------------------------------
+def _need(t: torch.Tensor, name: str, dtype, shape) -> None:
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype or tuple(t.shape) != tuple(shape):
+        got = f"{t.dtype} {tuple(t.shape)}" if isinstance(t, torch.Tensor) else type(t).__name__
+        raise ValueError(f"{name}: expected {dtype} {tuple(shape)}, got {got}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous tensor")
+
+
+def _table(t: torch.Tensor, R: int) -> None:
+    if t.dim() != 2 or t.dtype != torch.int32 or t.shape[0] != R or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"table: expected int32 [{R}, pages] with dense rows, got {t.dtype} {tuple(t.shape)}")
+
+
+def _rows(t: torch.Tensor, name: str) -> torch.Tensor:
+    """[T, heads, D] fp32 or bf16 as the kernels read it: the last dim dense,
+    pointer and strides in whole 16-byte pieces (a copy where they are not)."""
+    if t.dim() != 3 or t.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError(f"{name}: expected fp32 or bf16 [rows, heads, dim], got {t.dtype} {tuple(t.shape)}")
+    size, (rs, hs, ds) = t.element_size(), t.stride()
+    T, H, D = t.shape
+    if (ds == 1 and (rs * size) % 16 == 0 and ((hs * size) % 16 == 0 or H == 1) and t.data_ptr() % 16 == 0
+            and rs >= D and (hs >= D or H == 1)):
+        return t
+    return t.clone(memory_format=torch.contiguous_format)
+
+
+def _out_rows(t: torch.Tensor, name: str, shape, dtype) -> torch.Tensor:
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or t.stride(2) != 1:
+        raise ValueError(f"{name}: expected {dtype} {tuple(shape)} with a dense last dim, got {t.dtype} {tuple(t.shape)}")
+    return t
+
+
+def kv_cache(n_pages: int, n_kv_heads: int, head_dim: int, device) -> tuple:
+    """(codes int8 [n_pages, n_kv_heads, 2, 64 * head_dim], scales fp32
+    [n_pages, n_kv_heads, 2]) of one layer's cache, zeroed."""
+    B.ht_kv_cache_bytes(n_pages, n_kv_heads, head_dim)   # refuses what the kernels do not take
+    return (torch.zeros(n_pages, n_kv_heads, 2, B.HT_KV_PAGE * head_dim, dtype=torch.int8, device=device),
+            torch.zeros(n_pages, n_kv_heads, 2, dtype=torch.float32, device=device))
+
+
+def _cache_desc(codes: torch.Tensor, scales: torch.Tensor) -> B.KVCacheDesc:
+    if codes.dim() != 4 or codes.dtype != torch.int8 or codes.shape[2] != 2 or codes.shape[3] % B.HT_KV_PAGE:
+        raise ValueError(f"codes: expected int8 [pages, heads, 2, 64 * dim], got {codes.dtype} {tuple(codes.shape)}")
+    if not codes.is_contiguous():
+        raise ValueError("codes: expected a contiguous tensor")
+    _need(scales, "scales", torch.float32, codes.shape[:3])
+    return B.kv_cache_desc(codes, scales)
+
+
+def kv_cache_values(codes: torch.Tensor, scales: torch.Tensor) -> tuple:
+    """The keys and values a cache (or a selection of its pages) stands for:
+    two fp32 tensors [pages, heads, 64, dim].  Plain indexing, for inspection
+    and for moving a prefix to another format."""
+    n, h, _, b = codes.shape
+    d = b // B.HT_KV_PAGE
+    k = codes[:, :, 0].reshape(n, h, 4, d // 64, 4, 16, 16).permute(0, 1, 2, 5, 3, 4, 6).reshape(n, h, 64, d)
+    v = codes[:, :, 1].reshape(n, h, d // 16, 4, 16, 4, 4).permute(0, 1, 5, 3, 6, 2, 4).reshape(n, h, 64, d)
+    return k.float() * scales[:, :, 0, None, None], v.float() * scales[:, :, 1, None, None]
+
+
+class KVStep(NamedTuple):
+    """What kv_plan gives for one step (all int32, on the device)."""
+    cu_q: torch.Tensor        # [R + 1] first row of each request
+    slots: torch.Tensor       # [T] 64 * page + offset, -1: not stored
+    positions: torch.Tensor   # [T]
+    kv_len: torch.Tensor      # [R] tokens in the cache after the step
+    owned: torch.Tensor       # [R] pages owned after the step
+    status: torch.Tensor      # [2] pages left free, requests refused
+
+
+def kv_step(R: int, T: int, device) -> KVStep:
+    """Buffers for kv_plan's outputs, for reuse from step to step."""
+    return KVStep(*(torch.empty(n, dtype=torch.int32, device=device) for n in (R + 1, T, T, R, R, 2)))
+
+
+def kv_plan(q_len: torch.Tensor, kv_len: torch.Tensor, owned: torch.Tensor, table: torch.Tensor,
+            free_pages: torch.Tensor, n_free: torch.Tensor, T: int, out=None, stream=None) -> KVStep:
+    """Page tables, slots and positions of one step (ht_kv_plan).  q_len,
+    kv_len, owned int32 [R]; table int32 [R, pages] gets the new pages in
+    place; free_pages int32 [n] with its first n_free[0] entries free; T the
+    sum of q_len.  Nothing else changes: the next step takes step.kv_len,
+    step.owned and step.status[:1] as kv_len, owned and n_free."""
+    i32, R = torch.int32, q_len.shape[0]
+    for t, name in ((q_len, "q_len"), (kv_len, "kv_len"), (owned, "owned")):
+        _need(t, name, i32, (R,))
+    _table(table, R)
+    _need(free_pages, "free_pages", i32, (free_pages.numel(),))
+    _need(n_free, "n_free", i32, (1,))
+    if out is None:
+        out = kv_step(R, T, q_len.device)
+    else:
+        out = KVStep(*out)
+        for t, name, n in zip(out, KVStep._fields, (R + 1, T, T, R, R, 2)):
+            _need(t, name, i32, (n,))
+    B.ht_kv_plan(q_len, kv_len, owned, table, free_pages, n_free, T, *out, stream=stream)
+    return out
+
+
+def kv_release(which: torch.Tensor, kv_len: torch.Tensor, owned: torch.Tensor, table: torch.Tensor,
+               free_pages: torch.Tensor, n_free: torch.Tensor, stream=None) -> None:
+    """Give back the pages of the requests with which[r] (bool or uint8 [R]);
+    kv_len, owned, free_pages and n_free change in place (ht_kv_release)."""
+    R = which.shape[0]
+    if which.dtype not in (torch.bool, torch.uint8) or not which.is_contiguous():
+        raise ValueError(f"which: expected contiguous bool or uint8 [{R}], got {which.dtype}")
+    for t, name, n in ((kv_len, "kv_len", R), (owned, "owned", R), (n_free, "n_free", 1)):
+        _need(t, name, torch.int32, (n,))
+    _need(free_pages, "free_pages", torch.int32, (free_pages.numel(),))
+    _table(table, R)
+    B.ht_kv_release(which, kv_len, owned, table, free_pages, n_free, stream=stream)
+
+
+def rope_inv_freq(rot: int, base: float = 10000.0, device=None) -> torch.Tensor:
+    """fp64 [rot / 2]: base^(-2 i / rot), the angle per position of each pair."""
+    i = torch.arange(rot // 2, dtype=torch.float64, device=device)
+    return base ** (-2.0 * i / rot)
+
+
+def _rope_args(q, k, positions, inv_freq, q_weight, k_weight):
+    T, _, D = q.shape
+    if k is not None and (k.dtype != q.dtype or k.shape[0] != T or k.shape[2] != D):
+        raise ValueError(f"k: expected {q.dtype} [{T}, heads, {D}], got {k.dtype} {tuple(k.shape)}")
+    _need(positions, "positions", torch.int32, (T,))
+    _need(inv_freq, "inv_freq", torch.float64, (inv_freq.numel(),))
+    if (q_weight is None) != (k_weight is None):
+        raise ValueError("q_weight and k_weight: both or neither")
+    if q_weight is not None:
+        _need(q_weight, "q_weight", torch.float32, (D,))
+        _need(k_weight, "k_weight", torch.float32, (D,))
+
+
+def qk_norm_rope(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tensor, inv_freq: torch.Tensor,
+                 q_weight: torch.Tensor | None = None, k_weight: torch.Tensor | None = None, eps: float = 1e-6,
+                 interleaved: bool = False, out_dtype=None, out=None, stream=None) -> tuple:
+    """Norm of every head (with weights given) and rotation by position of q
+    [T, n_q, D] and k [T, n_k, D] (or None) in one pass (ht_qk_norm_rope).
+    fp32 or bf16, any row and head strides; positions int32 [T]; inv_freq
+    fp64 [rot / 2].  Returns (q, k) in out_dtype (q's own by default)."""
+    q = _rows(q, "q")
+    k = _rows(k, "k") if k is not None else None
+    _rope_args(q, k, positions, inv_freq, q_weight, k_weight)
+    dt = q.dtype if out_dtype is None else out_dtype
+    if dt not in (torch.float32, torch.bfloat16):
+        raise ValueError(f"out_dtype: expected fp32 or bf16, got {dt}")
+    if out is None:
+        yq = torch.empty(q.shape, dtype=dt, device=q.device)
+        yk = torch.empty(k.shape, dtype=dt, device=q.device) if k is not None else None
+    else:
+        yq = _out_rows(out[0], "out[0]", q.shape, dt)
+        yk = _out_rows(out[1], "out[1]", k.shape, dt) if k is not None else None
+    B.ht_qk_norm_rope(q, k, positions, inv_freq, q_weight, k_weight, eps, interleaved, yq, yk, stream=stream)
+    return yq, yk
+
+
+def qk_norm_rope_backward(dq: torch.Tensor, dk: torch.Tensor | None, q: torch.Tensor, k: torch.Tensor | None,
+                          positions: torch.Tensor, inv_freq: torch.Tensor, q_weight: torch.Tensor | None = None,
+                          k_weight: torch.Tensor | None = None, eps: float = 1e-6, interleaved: bool = False,
+                          out=None, ws: torch.Tensor | None = None, stream=None) -> tuple:
+    """Gradients of qk_norm_rope: (dq, dk) of its inputs, in their type, and
+    fp32 (dq_weight, dk_weight) (None without weights)."""
+    q, dq = _rows(q, "q"), _rows(dq, "dq")
+    k, dk = (_rows(k, "k"), _rows(dk, "dk")) if k is not None else (None, None)
+    _rope_args(q, k, positions, inv_freq, q_weight, k_weight)
+    if dq.shape != q.shape or (k is not None and (dk.shape != k.shape or dk.dtype != dq.dtype)):
+        raise ValueError("dq, dk: expected the shapes of q and k, one type")
+    if out is None:
+        xq, xk = torch.empty(q.shape, dtype=q.dtype, device=q.device), None
+        if k is not None:
+            xk = torch.empty(k.shape, dtype=k.dtype, device=q.device)
+    else:
+        xq = _out_rows(out[0], "out[0]", q.shape, q.dtype)
+        xk = _out_rows(out[1], "out[1]", k.shape, k.dtype) if k is not None else None
+    dwq = dwk = None
+    if q_weight is not None:
+        dwq, dwk = torch.empty_like(q_weight), torch.empty_like(k_weight)
+        if ws is None:
+            n_k = k.shape[1] if k is not None else 0
+            ws = workspace(B.ht_qk_norm_rope_workspace(q.shape[0], q.shape[1], n_k, q.shape[2], True), q.device)
+    B.ht_qk_norm_rope_backward(dq, dk, q, k, positions, inv_freq, q_weight, k_weight, eps, interleaved, xq, xk, dwq,
+                               dwk, ws=ws, stream=stream)
+    return xq, xk, dwq, dwk
+
+
+def kv_write(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor,
+             stream=None) -> None:
+    """Quantise keys and values [T, heads, D] (fp32 or bf16, each its own
+    type) into the cache at slots int32 [T] (ht_kv_write), in place."""
+    desc = _cache_desc(codes, scales)
+    k, v = _rows(k, "k"), _rows(v, "v")
+    shape = (slots.shape[0], codes.shape[1], codes.shape[3] // B.HT_KV_PAGE)
+    if tuple(k.shape) != shape or tuple(v.shape) != shape:
+        raise ValueError(f"k, v: expected {shape}, got {tuple(k.shape)} and {tuple(v.shape)}")
+    _need(slots, "slots", torch.int32, shape[:1])
+    B.ht_kv_write(k, v, slots, desc, stream=stream)
+
+
+def kv_attention(q: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, table: torch.Tensor, cu_q: torch.Tensor,
+                 kv_len: torch.Tensor, max_q: int, max_kv: int | None = None, scale: float | None = None,
+                 causal: bool = True, window: int = 0, out: torch.Tensor | None = None,
+                 ws: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Attention of the rows q bf16 [T, n_q, D] over the cache
+    (ht_kv_attention): bf16 [T, n_q, D].  max_q and max_kv (default: what the
+    table can hold) are the largest lengths the caller knows of; scale is
+    1 / sqrt(D) by default; window > 0 keeps each row to its last `window`
+    tokens."""
+    desc = _cache_desc(codes, scales)
+    if q.dtype != torch.bfloat16:
+        raise ValueError(f"q: expected bf16 [rows, heads, dim], got {q.dtype}")
+    q = _rows(q, "q")
+    T, n_q, D = q.shape
+    if D != codes.shape[3] // B.HT_KV_PAGE:
+        raise ValueError(f"q: expected head dim {codes.shape[3] // B.HT_KV_PAGE}, got {D}")
+    R = kv_len.shape[0]
+    _table(table, R)
+    _need(cu_q, "cu_q", torch.int32, (R + 1,))
+    _need(kv_len, "kv_len", torch.int32, (R,))
+    if max_kv is None:
+        max_kv = table.shape[1] * B.HT_KV_PAGE
+    out = torch.empty(q.shape, dtype=q.dtype, device=q.device) if out is None else _out_rows(out, "out", q.shape, q.dtype)
+    if ws is None:
+        ws = workspace(B.ht_kv_attention_workspace(desc, T, R, n_q, max_q, max_kv), q.device)
+    B.ht_kv_attention(q, desc, table, cu_q, kv_len, max_q, max_kv, 1.0 / math.sqrt(D) if scale is None else scale,
+                      causal, window, out, ws=ws, stream=stream)
+    return out

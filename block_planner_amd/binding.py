@@ -23,6 +23,7 @@ HT_INT4, HT_INT8, HT_BF16, HT_FP16, HT_FP32 = range(5)
 HT_ACT_NONE, HT_ACT_RELU = 0, 1
 HT_PATH_AUTO, HT_PATH_GEMV, HT_PATH_FUSED, HT_PATH_GEMM, HT_PATH_GEMV_MFMA, HT_PATH_GEMM_I8, HT_PATH_W8A8 = 0, 1, 2, 3, 4, 5, 6
 HT_LAYOUT_VERSION = 1
+HT_KV_PAGE, HT_KV_MIN_EXP = 64, -60
 STATUS = {0: "HT_OK", 1: "HT_EINVAL", 2: "HT_ESHAPE", 3: "HT_EALIGN", 4: "HT_ESMALL", 5: "HT_EHIP"}
 
 # Every symbol include/ht.h declares.
@@ -31,7 +32,9 @@ EXPORTS = ("ht_status_string", "ht_plan_params_default", "ht_plan", "ht_plan_cou
            "ht_linear_workspace", "ht_linear_forward",
            "ht_linear_forward_noalloc",
            "ht_linear_backward_workspace", "ht_linear_backward_data", "ht_linear_backward_weight",
-           "ht_mlp_workspace", "ht_workspace_init", "ht_mlp_forward")
+           "ht_mlp_workspace", "ht_workspace_init", "ht_mlp_forward",
+           "ht_kv_cache_bytes", "ht_kv_plan", "ht_kv_release", "ht_qk_norm_rope", "ht_qk_norm_rope_workspace",
+           "ht_qk_norm_rope_backward", "ht_kv_write", "ht_kv_attention_workspace", "ht_kv_attention")
 
 
 class HTError(RuntimeError):
@@ -53,6 +56,12 @@ class PackedWeight(ctypes.Structure):
                 ("off_scale", ctypes.c_uint64 * 2), ("off_payload", ctypes.c_uint64 * 5),
                 ("bytes", ctypes.c_uint64), ("layout_version", ctypes.c_int32),
                 ("reserved", ctypes.c_int32), ("base", ctypes.c_void_p)]
+
+
+class KVCacheDesc(ctypes.Structure):
+    """ht_kv_cache."""
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("n_pages", ctypes.c_int64),
+                ("n_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32)]
 
 
 _lib = None
@@ -121,6 +130,30 @@ def load() -> ctypes.CDLL:
     lib.ht_mlp_forward.restype = St
     lib.ht_mlp_forward.argtypes = [ctypes.POINTER(ctypes.POINTER(PackedWeight)), I32, P, I64, I64, P, I64, P, I32,
                                    P, ctypes.c_size_t, P]
+    F, Sz = ctypes.c_float, ctypes.c_size_t
+    PC, PSz = ctypes.POINTER(KVCacheDesc), ctypes.POINTER(ctypes.c_size_t)
+    lib.ht_kv_cache_bytes.restype = St
+    lib.ht_kv_cache_bytes.argtypes = [I64, I32, I32, PSz, PSz]
+    lib.ht_kv_plan.restype = St
+    lib.ht_kv_plan.argtypes = [P, P, P, I64, P, I64, I64, P, I64, P, I64, P, P, P, P, P, P, P]
+    lib.ht_kv_release.restype = St
+    lib.ht_kv_release.argtypes = [P, I64, P, P, P, I64, I64, P, I64, P, P]
+    lib.ht_qk_norm_rope.restype = St
+    lib.ht_qk_norm_rope.argtypes = [P, I64, I64, P, I64, I64, I32, I64, I32, I32, I32, I32, I32, P, P, P, P, F,
+                                    P, I64, I64, P, I64, I64, I32, P]
+    lib.ht_qk_norm_rope_workspace.restype = St
+    lib.ht_qk_norm_rope_workspace.argtypes = [I64, I32, I32, I32, I32, PSz]
+    lib.ht_qk_norm_rope_backward.restype = St
+    lib.ht_qk_norm_rope_backward.argtypes = [P, I64, I64, P, I64, I64, I32, P, I64, I64, P, I64, I64, I32, I64, I32,
+                                             I32, I32, I32, I32, P, P, P, P, F, P, I64, I64, P, I64, I64, P, P, P, Sz,
+                                             P]
+    lib.ht_kv_write.restype = St
+    lib.ht_kv_write.argtypes = [P, I64, I64, I32, P, I64, I64, I32, I64, P, PC, P]
+    lib.ht_kv_attention_workspace.restype = St
+    lib.ht_kv_attention_workspace.argtypes = [PC, I64, I64, I32, I64, I64, PSz]
+    lib.ht_kv_attention.restype = St
+    lib.ht_kv_attention.argtypes = [P, I64, I64, I64, I32, PC, P, I64, I64, P, P, I64, I64, I64, F, I32, I64, P, I64,
+                                    I64, P, Sz, P]
     _lib = lib
     return lib
 
@@ -307,3 +340,95 @@ def ht_mlp_forward(descs, x, y, act_dump=None, path: int = HT_PATH_AUTO, ws=None
     arr = _desc_array(descs) if desc_array is None else desc_array
     _check("ht_mlp_forward", load().ht_mlp_forward(arr, len(descs), _ptr(x), M, ldx, _ptr(y), ldy,
                                                    _ptr(act_dump), path, _ptr(ws), wsb, _stream(stream)))
+
+
+# -----------------------------------------------------------------------------
+# Attention beside the linears
+# -----------------------------------------------------------------------------
+def _act(t) -> int:
+    """HT_FP32 or HT_BF16 of a tensor."""
+    import torch
+    return HT_BF16 if t.dtype == torch.bfloat16 else HT_FP32
+
+
+def _ld(t) -> int:
+    """Row stride of a matrix (the stride of a single row may be anything)."""
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def ht_kv_cache_bytes(n_pages: int, n_heads: int, head_dim: int) -> tuple:
+    """(bytes of the codes, bytes of the scales)."""
+    c, s = ctypes.c_size_t(0), ctypes.c_size_t(0)
+    _check("ht_kv_cache_bytes", load().ht_kv_cache_bytes(n_pages, n_heads, head_dim, ctypes.byref(c), ctypes.byref(s)))
+    return c.value, s.value
+
+
+def ht_kv_plan(q_len, kv_len, owned, table, free_pages, n_free, T: int, cu_q, slots, positions, kv_out, owned_out,
+               status, stream=None) -> None:
+    _check("ht_kv_plan", load().ht_kv_plan(
+        _ptr(q_len), _ptr(kv_len), _ptr(owned), q_len.shape[0], _ptr(table), table.shape[1], _ld(table),
+        _ptr(free_pages), free_pages.shape[0], _ptr(n_free), T, _ptr(cu_q), _ptr(slots), _ptr(positions),
+        _ptr(kv_out), _ptr(owned_out), _ptr(status), _stream(stream)))
+
+
+def ht_kv_release(which, kv_len, owned, table, free_pages, n_free, stream=None) -> None:
+    _check("ht_kv_release", load().ht_kv_release(
+        _ptr(which), which.shape[0], _ptr(kv_len), _ptr(owned), _ptr(table), table.shape[1], _ld(table),
+        _ptr(free_pages), free_pages.shape[0], _ptr(n_free), _stream(stream)))
+
+
+def ht_qk_norm_rope(q, k, positions, inv_freq, wq, wk, eps: float, interleaved: bool, yq, yk, stream=None) -> None:
+    """q, yq [T, n_q, D]; k, yk [T, n_k, D] or None."""
+    T, n_q, D = q.shape
+    n_k, ldk, hsk, ldyk, hsyk = (k.shape[1], *k.stride()[:2], *yk.stride()[:2]) if k is not None else (0, 0, 0, 0, 0)
+    _check("ht_qk_norm_rope", load().ht_qk_norm_rope(
+        _ptr(q), q.stride(0), q.stride(1), _ptr(k), ldk, hsk, _act(q), T, n_q, n_k, D, 2 * inv_freq.shape[0],
+        int(interleaved), _ptr(positions), _ptr(inv_freq), _ptr(wq), _ptr(wk), eps, _ptr(yq), yq.stride(0),
+        yq.stride(1), _ptr(yk), ldyk, hsyk, _act(yq), _stream(stream)))
+
+
+def ht_qk_norm_rope_workspace(T: int, n_q: int, n_k: int, D: int, norm: bool) -> int:
+    out = ctypes.c_size_t(0)
+    _check("ht_qk_norm_rope_workspace", load().ht_qk_norm_rope_workspace(T, n_q, n_k, D, int(norm), ctypes.byref(out)))
+    return out.value
+
+
+def ht_qk_norm_rope_backward(dq, dk, q, k, positions, inv_freq, wq, wk, eps: float, interleaved: bool, dxq, dxk,
+                             dwq=None, dwk=None, ws=None, stream=None) -> None:
+    T, n_q, D = dq.shape
+    n_k, lddk, hsdk, ldk, hsk, lddxk, hsdxk = \
+        (k.shape[1], *dk.stride()[:2], *k.stride()[:2], *dxk.stride()[:2]) if k is not None else (0,) * 7
+    wsb = ws.numel() * ws.element_size() if ws is not None else 0
+    _check("ht_qk_norm_rope_backward", load().ht_qk_norm_rope_backward(
+        _ptr(dq), dq.stride(0), dq.stride(1), _ptr(dk), lddk, hsdk, _act(dq), _ptr(q), q.stride(0), q.stride(1),
+        _ptr(k), ldk, hsk, _act(q), T, n_q, n_k, D, 2 * inv_freq.shape[0], int(interleaved), _ptr(positions),
+        _ptr(inv_freq), _ptr(wq), _ptr(wk), eps, _ptr(dxq), dxq.stride(0), dxq.stride(1), _ptr(dxk), lddxk, hsdxk,
+        _ptr(dwq), _ptr(dwk), _ptr(ws), wsb, _stream(stream)))
+
+
+def kv_cache_desc(codes, scales) -> KVCacheDesc:
+    """Descriptor of codes int8 [pages, heads, 2, 64 * D] and scales fp32 [pages, heads, 2]."""
+    return KVCacheDesc(codes.data_ptr(), scales.data_ptr(), codes.shape[0], codes.shape[1],
+                       codes.shape[3] // HT_KV_PAGE)
+
+
+def ht_kv_write(k, v, slots, desc: KVCacheDesc, stream=None) -> None:
+    _check("ht_kv_write", load().ht_kv_write(_ptr(k), k.stride(0), k.stride(1), _act(k), _ptr(v), v.stride(0),
+                                             v.stride(1), _act(v), k.shape[0], _ptr(slots), ctypes.byref(desc),
+                                             _stream(stream)))
+
+
+def ht_kv_attention_workspace(desc: KVCacheDesc, T: int, R: int, n_q: int, max_q: int, max_kv: int) -> int:
+    out = ctypes.c_size_t(0)
+    _check("ht_kv_attention_workspace", load().ht_kv_attention_workspace(ctypes.byref(desc), T, R, n_q, max_q, max_kv,
+                                                                         ctypes.byref(out)))
+    return out.value
+
+
+def ht_kv_attention(q, desc: KVCacheDesc, table, cu_q, kv_len, max_q: int, max_kv: int, scale: float, causal: bool,
+                    window: int, out, ws=None, stream=None) -> None:
+    wsb = ws.numel() * ws.element_size() if ws is not None else 0
+    _check("ht_kv_attention", load().ht_kv_attention(
+        _ptr(q), q.stride(0), q.stride(1), q.shape[0], q.shape[1], ctypes.byref(desc), _ptr(table), table.shape[1],
+        _ld(table), _ptr(cu_q), _ptr(kv_len), kv_len.shape[0], max_q, max_kv, scale, int(causal), window,
+        _ptr(out), out.stride(0), out.stride(1), _ptr(ws), wsb, _stream(stream)))

@@ -429,6 +429,164 @@ ht_status ht_mlp_forward(const ht_packed_weight *const *layers, int32_t n_layers
                          uint16_t *act_dump, int32_t path, void *ws, size_t ws_bytes,
                          ht_stream stream);
 
+/* ---------------------------------------------------------------------------
+ * Attention beside the linears: a paged cache of keys and values held in 8
+ * bits, the step plan that places a batch's rows in it, the per-head norm and
+ * position rotation of q and k, and the attention that reads the cache.
+ * ("Key Features" names a HyperAttention module and fixes nothing of it; the
+ * formats, the layout and the formulas are this library's.)
+ *
+ * Conventions of these calls, beside the ones at the top of this file:
+ *   - A batch has R requests and T rows; request r owns rows
+ *     [cu_q[r], cu_q[r+1]), its newest tokens, in order.
+ *   - int32 arrays need 4-byte alignment, everything else 16 bytes, and row
+ *     and head strides (in elements) a multiple of 16 bytes.
+ *   - Values the device holds (lengths, tables, slots, free lists) cannot be
+ *     checked on the host.  The kernels clamp or skip what points outside the
+ *     arrays they were given, so wrong values there give wrong results and no
+ *     access out of range.
+ *   - `dtype` arguments are HT_FP32 or HT_BF16.
+ * ------------------------------------------------------------------------- */
+#define HT_KV_PAGE 64            /* tokens per page */
+#define HT_KV_MIN_EXP (-60)      /* smallest exponent E of a page's largest magnitude */
+
+/* The cache of one layer.  Each (page, KV head, K or V) is a block of 64 x D
+ * int8 codes with one fp32 scale, a power of two: value = code * scale.
+ *   codes   int8 [n_pages][n_heads][2][64 * D] (index 0: K, 1: V); within a block, token t, dim d:
+ *             K  t = 16 a + r, d = 64 c + 16 g + b:  at [a][c][g][r][b] of (4, D/64, 4, 16, 16)
+ *             V  t = 16 b + 4 g + i, d = 16 e + m:   at [e][g][m][b][i] of (D/16, 4, 16, 4, 4)
+ *           (the orders in which the matrix cores take their operands);
+ *   scales  fp32 [n_pages][n_heads][2].
+ * With 2^(E-1) <= max |x| < 2^E over the block's finite entries (E = HT_KV_MIN_EXP
+ * at least) the scale is 2^(E-7) and code = clamp(rne(x 2^(7-E)), -127, 127);
+ * +-Inf becomes +-127, NaN becomes 0.  Rows appended to a page that holds some
+ * raise E when they need to: older codes become rne(code 2^(E_old - E_new)),
+ * so an entry is off by less than one scale (half for its own rounding and
+ * half at most for all later halvings together), or by one where clamped.
+ * Scales must be initialised (zeros will do). */
+typedef struct {
+    int8_t *codes;               /* 16-byte aligned */
+    float *scales;
+    int64_t n_pages;             /* n_pages * 64 < 2^31 */
+    int32_t n_heads;             /* KV heads */
+    int32_t head_dim;            /* D: 64, 128, 192 or 256 */
+} ht_kv_cache;
+
+/* ht_kv_cache_bytes -- sizes of a cache's two arrays (host only). */
+ht_status ht_kv_cache_bytes(int64_t n_pages, int32_t n_heads, int32_t head_dim, size_t *codes, size_t *scales);
+
+/* ht_kv_plan -- page tables, slots and positions of one step, from the
+ * requests' lengths alone, on the device (no host round trip).
+ *   q_len     int32 [R]: new rows of each request (negative counts as 0);
+ *   kv_len    int32 [R]: tokens the cache holds of it before the step;
+ *   owned     int32 [R]: pages it owns (the valid entries of its table row);
+ *   table     int32 [R][ldt], P <= ldt entries used per row, in and out: only
+ *             entries of pages added by this call are written;
+ *   free_pages int32 [free_cap]: page numbers, of which the first *n_free are
+ *             free (n_free int32 [1], device); the i-th page this step adds, in
+ *             request order, is free_pages[*n_free - 1 - i];
+ *   T         rows of the batch (the caller's sum of q_len).
+ * Request r needs max(0, ceil((kv_len + q_len) / 64) - owned) pages more.  It
+ * is refused, and gets none, when its table row is too short or the pages
+ * asked for by requests up to it (those with too short a row left out) exceed
+ * *n_free; a request that needs none is never refused for want of pages.
+ *   cu_q      int32 [R + 1] out: exclusive prefix sums of q_len;
+ *   slots     int32 [T] out: 64 * page + offset of each row's token, -1 for a
+ *             refused request's rows and rows past cu_q[R];
+ *   positions int32 [T] out: kv_len[r] + row - cu_q[r] (0 past cu_q[R]);
+ *   kv_out    int32 [R] out: kv_len + q_len (kv_len if refused);
+ *   owned_out int32 [R] out;
+ *   status    int32 [2] out: pages left free (the next step's *n_free), requests refused.
+ * No output may overlap an input (HT_EINVAL for equal pointers). */
+ht_status ht_kv_plan(const int32_t *q_len, const int32_t *kv_len, const int32_t *owned, int64_t R,
+                     int32_t *table, int64_t P, int64_t ldt, const int32_t *free_pages, int64_t free_cap,
+                     const int32_t *n_free, int64_t T, int32_t *cu_q, int32_t *slots, int32_t *positions,
+                     int32_t *kv_out, int32_t *owned_out, int32_t *status, ht_stream stream);
+
+/* ht_kv_release -- give back the pages of the requests with which[r] != 0
+ * (uint8 [R]): pushed on the free list in request order, each row's pages last
+ * to first; their owned and kv_len become 0.  Everything in place; a page that
+ * does not fit in free_cap entries is dropped. */
+ht_status ht_kv_release(const uint8_t *which, int64_t R, int32_t *kv_len, int32_t *owned, const int32_t *table,
+                        int64_t P, int64_t ldt, int32_t *free_pages, int64_t free_cap, int32_t *n_free,
+                        ht_stream stream);
+
+/* ht_qk_norm_rope -- the norm of every head of q and k and the rotation by
+ * position in one pass: n = x / sqrt(mean(x^2) + eps) * w (skipped when both
+ * weights are NULL), then for each pair i < rot / 2 with the angle
+ * a = position * inv_freq[i]:  y_i = n_i cos a - n_j sin a,
+ * y_j = n_j cos a + n_i sin a.  Pairs are (i, i + rot/2), or (2i, 2i+1) when
+ * interleaved; dims from rot on are only normed.
+ *   q, k       [T][heads][D] of dtype xt, rows ldq / ldk and heads hsq / hsk
+ *              elements apart;  D % 8 == 0, D <= 256; rot % 8 == 0, rot <= D;
+ *              n_q >= 1, n_k >= 0 (k may be NULL with n_k = 0);
+ *   positions  int32 [T];  inv_freq  fp64 [rot / 2] (the angle is reduced in
+ *              fp64, so far positions keep their phase);
+ *   wq, wk     fp32 [D] both, or both NULL;
+ *   yq, yk     [T][heads][D] of dtype yt; may be q and k themselves when type
+ *              and strides are the same.
+ * Sums and products in fp32, one rounding at the end. */
+ht_status ht_qk_norm_rope(const void *q, int64_t ldq, int64_t hsq, const void *k, int64_t ldk, int64_t hsk,
+                          int32_t xt, int64_t T, int32_t n_q, int32_t n_k, int32_t D, int32_t rot,
+                          int32_t interleaved, const int32_t *positions, const double *inv_freq, const float *wq,
+                          const float *wk, float eps, void *yq, int64_t ldyq, int64_t hsyq, void *yk, int64_t ldyk,
+                          int64_t hsyk, int32_t yt, ht_stream stream);
+
+/* ht_qk_norm_rope_backward -- its gradients: with g the gradient dy rotated
+ * back and r = 1 / sqrt(mean(x^2) + eps):
+ *   dx = r (w g) - x r^3 / D * sum(w g x),   dw = sum over rows and heads of g x r.
+ *   dq, dk     gradients of yq, yk, dtype yt;  q, k: the forward's inputs,
+ *              dtype xt (not read when both weights are NULL: dx = g);
+ *   dxq, dxk   out, dtype xt;  dwq, dwk  fp32 [D] out (NULL with no weights).
+ *   ws         ht_qk_norm_rope_workspace bytes (0 without weights): partial
+ *              sums of dw, added in a fixed order (bitwise reproducible). */
+ht_status ht_qk_norm_rope_workspace(int64_t T, int32_t n_q, int32_t n_k, int32_t D, int32_t norm, size_t *bytes);
+ht_status ht_qk_norm_rope_backward(const void *dq, int64_t lddq, int64_t hsdq, const void *dk, int64_t lddk,
+                                   int64_t hsdk, int32_t yt, const void *q, int64_t ldq, int64_t hsq, const void *k,
+                                   int64_t ldk, int64_t hsk, int32_t xt, int64_t T, int32_t n_q, int32_t n_k,
+                                   int32_t D, int32_t rot, int32_t interleaved, const int32_t *positions,
+                                   const double *inv_freq, const float *wq, const float *wk, float eps, void *dxq,
+                                   int64_t lddxq, int64_t hsdxq, void *dxk, int64_t lddxk, int64_t hsdxk, float *dwq,
+                                   float *dwk, void *ws, size_t ws_bytes, ht_stream stream);
+
+/* ht_kv_write -- quantise rows of keys and values into the cache.
+ *   k, v      [T][n_heads][D], dtypes kt and vt, rows ldk / ldv and heads hsk /
+ *             hsv elements apart;
+ *   slots     int32 [T] (ht_kv_plan's): rows with a slot outside the cache
+ *             (-1) are skipped.  The rows of one page must follow each other,
+ *             in the order of their slots; the first one at offset 0 starts
+ *             the page afresh (what it held does not count for the scale).
+ * Reproducible bit for bit; writing the same rows again changes nothing. */
+ht_status ht_kv_write(const void *k, int64_t ldk, int64_t hsk, int32_t kt, const void *v, int64_t ldv, int64_t hsv,
+                      int32_t vt, int64_t T, const int32_t *slots, const ht_kv_cache *cache, ht_stream stream);
+
+/* ht_kv_attention -- attention of a batch's rows over the cache:
+ *   out[t, a] = sum_j softmax_j(scale * q[t, a] . K_j) V_j
+ * over the tokens j of row t's request with j < kv_len, j <= pos (when causal)
+ * and j > pos - window (when window > 0), pos = kv_len - q_len + (row in its
+ * request); a row that sees no token gives zeros.  Query head a reads KV head
+ * a / (n_q / n_heads).  A table entry outside the cache hides its page.
+ *   q         bf16 [T][n_q][D], rows ldq and heads hsq elements apart;
+ *   table, P, ldt, cu_q, kv_len   as ht_kv_plan gives them (kv_out), lengths
+ *             including this step's rows;
+ *   max_q, max_kv   the largest q_len and kv_len as far as the caller knows:
+ *             they size the launch, results do not depend on them beyond
+ *             the order of fp32 sums;
+ *   out       bf16 [T][n_q][D], rows ldo and heads hso elements apart.
+ * q.K runs on the int8 matrix cores with each row of q as (256 hi + lo)
+ * 2^(E-14), 2^(E-1) <= max |q| < 2^E, int8 planes hi and lo (off by at most
+ * 2^-15 of the row's largest entry) and exact int32 sums; the weights go to V
+ * as fp16 relative to the row's largest contribution; sums in fp32.  A row of q
+ * holding Inf or NaN gives NaN.  Bitwise reproducible.
+ *   ws        ht_kv_attention_workspace bytes: partial results of split rows. */
+ht_status ht_kv_attention_workspace(const ht_kv_cache *cache, int64_t T, int64_t R, int32_t n_q, int64_t max_q,
+                                    int64_t max_kv, size_t *bytes);
+ht_status ht_kv_attention(const uint16_t *q, int64_t ldq, int64_t hsq, int64_t T, int32_t n_q,
+                          const ht_kv_cache *cache, const int32_t *table, int64_t P, int64_t ldt, const int32_t *cu_q,
+                          const int32_t *kv_len, int64_t R, int64_t max_q, int64_t max_kv, float scale, int32_t causal,
+                          int64_t window, uint16_t *out, int64_t ldo, int64_t hso, void *ws, size_t ws_bytes,
+                          ht_stream stream);
+
 #ifdef __cplusplus
 }
 #endif
