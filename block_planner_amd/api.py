@@ -187,10 +187,9 @@ def mlp(layers: list, x: torch.Tensor, dump: bool = False, out: torch.Tensor | N
 # -----------------------------------------------------------------------------
 # Attention beside the linears
 # -----------------------------------------------------------------------------
-def _need(t: torch.Tensor, name: str, dtype, shape) -> None:
-    if not isinstance(t, torch.Tensor) or t.dtype != dtype or tuple(t.shape) != tuple(shape):
-        got = f"{t.dtype} {tuple(t.shape)}" if isinstance(t, torch.Tensor) else type(t).__name__
-        raise ValueError(f"{name}: expected {dtype} {tuple(shape)}, got {got}")
+def _need(t: torch.Tensor, name: str, dtype, shape: tuple) -> None:
+    if t.dtype is not dtype or t.shape != shape:
+        raise ValueError(f"{name}: expected {dtype} {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name}: expected a contiguous tensor")
 

@@ -8,9 +8,11 @@ namespace {
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 constexpr int kAttnThreads = 256;
 constexpr int kWaves = kAttnThreads / 64;
+constexpr int kMaxSplits = 64;   // one per lane of the kernel that joins them
 constexpr float kLog2e = 1.44269504088896341f;
 // The largest weight handed to V is 2^14: fp16 keeps 11 bits down to 2^-28 of it.
 constexpr float kTopLog2 = 14.f;
@@ -24,15 +26,25 @@ struct AttnArgs {
     float *part;        // [splits][T][n_q][D], normalised
     float *lse;         // [splits][T][n_q], log2 of the weights' sum
     int64_t ldq, hsq, ldo, hso, ldt, P;
-    int32_t T, n_q, n_heads, group, n_pages, causal, splits, split_pages;
+    int32_t T, n_q, n_heads, group, n_pages, causal;
+    int32_t splits, split_pages;     // of the decode kernel's requests
+    int32_t psplits, psplit_pages;   // of the prompt kernel's
+    int32_t prompt_from;             // columns from which a request is the prompt kernel's
     int64_t window;
-    float scale_log2;   // scale * log2(e)
+    float scale_log2;   // |scale| * log2(e)
+    float sign;         // of scale
 };
 
 // One request as the kernels see it: lengths clamped to the arrays.
 struct Request {
-    int32_t row0, rows, kv, p0, p1, splits;   // pages [p0, p1) hold every token its rows may see
+    int32_t row0, rows, kv, p0, p1;   // pages [p0, p1) hold every token its rows may see
+    int32_t splits, split_pages;
+    bool prompt;                      // the prompt kernel's
 };
+
+// Columns (rows x heads of a group) of a request up to which the decode kernel
+// takes it, where both kernels run.
+constexpr int kDecodeCols = 32;
 
 __device__ __forceinline__ Request load_request(const AttnArgs &a, int r) {
     Request q;
@@ -42,7 +54,9 @@ __device__ __forceinline__ Request load_request(const AttnArgs &a, int r) {
     q.p1 = (q.kv + kPage - 1) / kPage;
     const int64_t first = a.window > 0 ? int64_t(q.kv) - q.rows + 1 - a.window : 0;   // first row's first token
     q.p0 = first > 0 ? min(int32_t(min(first / kPage, int64_t(q.p1))), q.p1) : 0;
-    q.splits = min(max((q.p1 - q.p0 + a.split_pages - 1) / a.split_pages, 1), a.splits);
+    q.prompt = int64_t(q.rows) * a.group >= a.prompt_from;
+    q.split_pages = q.prompt ? a.psplit_pages : a.split_pages;
+    q.splits = min(max((q.p1 - q.p0 + q.split_pages - 1) / q.split_pages, 1), q.prompt ? a.psplits : a.splits);
     return q;
 }
 
@@ -96,9 +110,9 @@ __global__ __launch_bounds__(kAttnThreads) void attn_decode_kernel(AttnArgs a) {
     const int r = int(blockIdx.x) / a.n_heads, head = int(blockIdx.x) % a.n_heads;
     const Request rq = load_request(a, r);
     const int split = int(blockIdx.y);
-    if (rq.rows == 0 || split >= rq.splits) return;
-    const int pa = rq.p0 + split * a.split_pages;
-    const int pb = split == rq.splits - 1 ? rq.p1 : min(rq.p1, pa + a.split_pages);
+    if (rq.rows == 0 || rq.prompt || split >= rq.splits) return;
+    const int pa = rq.p0 + split * rq.split_pages;
+    const int pb = split == rq.splits - 1 ? rq.p1 : min(rq.p1, pa + rq.split_pages);
     const int n_cols = rq.rows * a.group;
     const int32_t *row_of_table = a.table + int64_t(r) * a.ldt;
 
@@ -128,7 +142,7 @@ __global__ __launch_bounds__(kAttnThreads) void attn_decode_kernel(AttnArgs a) {
             top = max(top, uint32_t(__shfl_xor(int(top), 32)));
             const bool bad = top >= 0x7F80u;
             const int e = max(int(top >> 7) - 126, -100);
-            const float f = bad ? 0.f : pow2f(14 - e);
+            const float f = bad ? 0.f : pow2f(14 - e) * a.sign;
 #pragma unroll
             for (int j = 0; j < DC; ++j) {
                 if (bad) {
@@ -261,55 +275,296 @@ __global__ __launch_bounds__(kAttnThreads) void attn_decode_kernel(AttnArgs a) {
     }
 }
 
-// Joins the splits of one request's rows, in their order: a wavefront per row and head.
+// Prompts: tiles of 128 columns, 32 per wavefront, over all pages of a split.
+//
+// A page's codes are turned into fp16 (exactly) once per workgroup and put in
+// LDS in the order in which the 32x32x16 fp16 MFMAs take them, K as their A
+// operand of S^T = K Q^T, V as that of O^T += V^T P^T.  The accumulator of S^T
+// holds, per lane, 4 + 4 tokens of a 16-token stretch of one column; V's
+// operand takes its tokens in that same order, so the weights go from one
+// product to the next in registers.  The next page is loaded into registers
+// while this one is multiplied, and converted into the other LDS buffer after.
+template <int DC>
+__global__ __launch_bounds__(kAttnThreads, DC <= 2 ? 2 : 1) void attn_prompt_kernel(AttnArgs a) {
+    constexpr int D = 64 * DC, KS = D / 16, DB = D / 32, kHalf = 64 * D * 2 / 16;   // 16-byte pieces of K's half
+    __shared__ f16x8 lds[2][2 * kHalf];
+    const int tid = threadIdx.x, lane = tid & 63, wv = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int col = lane & 31, h = lane >> 5;
+    const int r = int(blockIdx.x) / a.n_heads, head = int(blockIdx.x) % a.n_heads;
+    const Request rq = load_request(a, r);
+    const int split = int(blockIdx.y);
+    if (rq.rows == 0 || !rq.prompt || split >= rq.splits) return;
+    const int pa = rq.p0 + split * rq.split_pages;
+    const int pb = split == rq.splits - 1 ? rq.p1 : min(rq.p1, pa + rq.split_pages);
+    const int n_cols = rq.rows * a.group, n_tiles = (n_cols + 127) / 128;
+    const int32_t *row_of_table = a.table + int64_t(r) * a.ldt;
+
+    // the last tiles first: under a causal mask they see the most
+    for (int tile = n_tiles - 1 - int(blockIdx.z); tile >= 0; tile -= int(gridDim.z)) {
+        const int c0 = tile * 128, c = c0 + wv * 32 + col;
+        const bool live = c < n_cols;
+        const int qi = (live ? c : c0) / a.group, gh = (live ? c : c0) - qi * a.group;
+        const int t = rq.row0 + qi, hq = head * a.group + gh;
+        int lo, hi;
+        row_range(a, rq, qi, lo, hi);
+        if (!live) hi = lo = 0;
+        // ranges of the tile and of this wavefront's columns (lo and hi never fall from row to row)
+        int t_lo, t_hi, w_lo_max, w_hi_min, unused;
+        row_range(a, rq, c0 / a.group, t_lo, unused);
+        row_range(a, rq, (min(c0 + 128, n_cols) - 1) / a.group, unused, t_hi);
+        const int w_first = min(c0 + wv * 32, n_cols - 1), w_last = min(c0 + wv * 32 + 31, n_cols - 1);
+        row_range(a, rq, w_first / a.group, unused, w_hi_min);
+        row_range(a, rq, w_last / a.group, w_lo_max, unused);
+        const int p_first = max(pa, t_lo / kPage), p_last = min(pb, (t_hi + kPage - 1) / kPage);
+
+        // q's row as fp16, scaled by a power of two into fp16's normal range (exact but for
+        // entries 2^-28 of the row's largest)
+        f16x8 q[KS];
+        float qs;
+        {
+            const uint16_t *qp = a.q + int64_t(t) * a.ldq + int64_t(hq) * a.hsq + h * 8;
+            union { uint4 u; uint16_t x[8]; } x[KS];
+            uint32_t top = 0;
+#pragma unroll
+            for (int k = 0; k < KS; ++k) {
+                x[k].u = *reinterpret_cast<const uint4 *>(qp + 16 * k);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) top = max(top, uint32_t(x[k].x[i]) & 0x7FFFu);
+            }
+            top = max(top, uint32_t(__shfl_xor(int(top), 32)));
+            const bool bad = top >= 0x7F80u;
+            const int e = max(int(top >> 7) - 126, -100);
+            const float f = pow2f(14 - e) * a.sign;
+#pragma unroll
+            for (int k = 0; k < KS; ++k)
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    q[k][i] = bad ? _Float16(0.f) : _Float16(__uint_as_float(uint32_t(x[k].x[i]) << 16) * f);
+            qs = bad ? __uint_as_float(0x7FC00000u) : pow2f(e - 14) * a.scale_log2;
+        }
+
+        u32x4 kr[DC];
+        uint2 vr[DC][2];
+        float ks, vs;
+        bool there;
+        const auto load_page = [&](int p) {
+            int32_t page = p < pb ? __builtin_amdgcn_readfirstlane(row_of_table[p]) : -1;
+            there = page >= 0 && page < a.n_pages;
+            if (!there) page = 0;
+            const int64_t blk = (int64_t(page) * a.n_heads + head) * 2;
+            const int8_t *kp = a.codes + blk * (kPage * D), *vp = kp + kPage * D;
+            ks = a.scales[blk];
+            vs = a.scales[blk + 1];
+#pragma unroll
+            for (int j = 0; j < DC; ++j) {
+                kr[j] = *reinterpret_cast<const u32x4 *>(kp + (j * kAttnThreads + tid) * 16);
+                // two token groups g and g + 2 of a dim, half of their 16 tokens
+                const int u = j * kAttnThreads + tid, m = u & 15, g = (u >> 4) & 1, half = (u >> 5) & 1, e = u >> 6;
+                const int8_t *v = vp + ((e * 4 + g) * 16 + m) * 16 + half * 8;
+                vr[j][0] = *reinterpret_cast<const uint2 *>(v);
+                vr[j][1] = *reinterpret_cast<const uint2 *>(v + 512);
+            }
+        };
+        const auto store_page = [&](f16x8 *b) {
+#pragma unroll
+            for (int j = 0; j < DC; ++j) {
+                const int u = j * kAttnThreads + tid;
+                {   // 16 dims of a token: both halves of the lanes of one K operand
+                    const int rr = u & 15, g = (u >> 4) & 3, cc = (u >> 6) % DC, aa = (u >> 6) / DC;
+                    f16x8 *d = b + ((aa >> 1) * KS + cc * 4 + g) * 64 + (aa & 1) * 16 + rr;
+                    d[0] = codes_to_f16(kr[j].x, kr[j].y);
+                    d[32] = codes_to_f16(kr[j].z, kr[j].w);
+                }
+                const int m = u & 15, g = (u >> 4) & 1, half = (u >> 5) & 1, e = u >> 6;
+                f16x8 *d = b + kHalf + ((e >> 1) * 4 + half * 2) * 64 + g * 32 + (e & 1) * 16 + m;
+                d[0] = codes_to_f16(vr[j][0].x, vr[j][1].x);
+                d[64] = codes_to_f16(vr[j][0].y, vr[j][1].y);
+            }
+        };
+
+        f32x16 o[DB];
+#pragma unroll
+        for (int d = 0; d < DB; ++d)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) o[d][i] = 0.f;
+        float m_run = -INFINITY, l_run = 0.f;
+        if (p_first < p_last) {
+            load_page(p_first);
+            __syncthreads();   // the tile before has been read
+            store_page(lds[0]);
+        }
+        for (int p = p_first, cur = 0; p < p_last; ++p, cur ^= 1) {
+            const float f = qs * ks, ef = float(exp_of_scale(vs) - 7);
+            const float l_unit = pow2f(7 - exp_of_scale(vs));
+            const bool shown = there;
+            __syncthreads();   // this page is in LDS; the other buffer has been read
+            if (p + 1 < p_last) load_page(p + 1);
+            if (shown) {
+                const f16x8 *kb = lds[cur], *vb = lds[cur] + kHalf;
+                f32x16 s[2];
+#pragma unroll
+                for (int b = 0; b < 2; ++b)
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) s[b][i] = 0.f;
+#pragma unroll
+                for (int k = 0; k < KS; ++k)
+#pragma unroll
+                    for (int b = 0; b < 2; ++b)
+                        s[b] = __builtin_amdgcn_mfma_f32_32x32x16_f16(kb[(b * KS + k) * 64 + lane], q[k], s[b], 0, 0, 0);
+                const int j0 = p * kPage;
+                const bool edge = j0 < w_lo_max || j0 + kPage > w_hi_min;
+                if (edge) {
+#pragma unroll
+                    for (int b = 0; b < 2; ++b)
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            const int j = j0 + b * 32 + 8 * (i >> 2) + 4 * h + (i & 3);
+                            if (j < lo || j >= hi) s[b][i] = -INFINITY;
+                        }
+                }
+                float top = s[0][0];
+#pragma unroll
+                for (int b = 0; b < 2; ++b)
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) top = fmaxf(top, s[b][i]);
+                top = top == -INFINITY ? -INFINITY : top * f + ef;   // f >= 0
+                top = fmaxf(top, __shfl_xor(top, 32));
+                const float m_new = fmaxf(m_run, top);
+                if (__any(m_new > m_run)) {
+                    const float alpha = m_run == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m_run - m_new);
+                    l_run *= alpha;
+#pragma unroll
+                    for (int d = 0; d < DB; ++d) o[d] *= alpha;
+                    m_run = m_new;
+                }
+                const float shift = ef - (m_run == -INFINITY ? 0.f : m_run - kTopLog2);
+                float sum = 0.f;
+                f16x8 w[4];
+#pragma unroll
+                for (int b = 0; b < 2; ++b)
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        float x = __builtin_amdgcn_exp2f(s[b][i] * f + shift);
+                        if (edge && s[b][i] == -INFINITY) x = 0.f;   // f may be 0
+                        sum += x;
+                        w[2 * b + (i >> 3)][i & 7] = _Float16(x);
+                    }
+                l_run += sum * l_unit;
+#pragma unroll
+                for (int b = 0; b < 4; ++b)
+#pragma unroll
+                    for (int d = 0; d < DB; ++d)
+                        o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vb[(d * 4 + b) * 64 + lane], w[b], o[d], 0, 0, 0);
+            }
+            if (p + 1 < p_last) store_page(lds[cur ^ 1]);
+        }
+        const float l = l_run + __shfl_xor(l_run, 32);
+        if (live) {
+            const float inv = l == 0.f ? 0.f : 1.0f / l;
+            const int64_t at = (int64_t(split) * a.T + t) * a.n_q + hq;
+#pragma unroll
+            for (int d = 0; d < DB; ++d)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const f32x4 v = {o[d][4 * i] * inv, o[d][4 * i + 1] * inv, o[d][4 * i + 2] * inv, o[d][4 * i + 3] * inv};
+                    const int dim = d * 32 + 8 * i + 4 * h;
+                    if (rq.splits == 1) {
+                        uint2 u;
+                        u.x = uint32_t(f32_to_bf16_rne(v.x)) | (uint32_t(f32_to_bf16_rne(v.y)) << 16);
+                        u.y = uint32_t(f32_to_bf16_rne(v.z)) | (uint32_t(f32_to_bf16_rne(v.w)) << 16);
+                        *reinterpret_cast<uint2 *>(a.out + int64_t(t) * a.ldo + int64_t(hq) * a.hso + dim) = u;
+                    } else {
+                        *reinterpret_cast<f32x4 *>(a.part + at * D + dim) = v;
+                    }
+                }
+            if (rq.splits > 1 && h == 0)
+                a.lse[at] = l == 0.f ? -INFINITY : (m_run == -INFINITY ? 0.f : m_run) + log2f(l);
+        }
+    }
+}
+
+// Joins the splits of one request's rows, a workgroup per row and head: a
+// result row is D / 4 lanes wide, so 4096 / D splits are read at once; each
+// lane sums its splits in their order, then the groups are added in theirs.
 template <int DC>
 __global__ __launch_bounds__(kAttnThreads) void attn_join_kernel(AttnArgs a) {
-    constexpr int D = 64 * DC;
-    const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
+    constexpr int D = 64 * DC, kLanes = D / 4, kGroups = kAttnThreads / kLanes;
+    __shared__ float s_w[kMaxSplits];
+    __shared__ f32x4 s_v[kGroups][kLanes];
+    const int tid = threadIdx.x, lane = tid & 63, grp = tid / kLanes, d = tid % kLanes;
     const Request rq = load_request(a, int(blockIdx.x));
     if (rq.splits <= 1) return;
-    const int64_t n = int64_t(rq.rows) * a.n_q;
-    for (int64_t i = int64_t(blockIdx.y) * kWaves + wv; i < n; i += int64_t(gridDim.y) * kWaves) {
-        const int64_t at = int64_t(rq.row0) * a.n_q + i, step = int64_t(a.T) * a.n_q;
-        float m = -INFINITY;
-        for (int s = 0; s < rq.splits; ++s) m = fmaxf(m, a.lse[at + s * step]);
-        float l = 0.f, v[DC];
+    const int64_t n = int64_t(rq.rows) * a.n_q, step = int64_t(a.T) * a.n_q;
+    for (int64_t i = blockIdx.y; i < n; i += gridDim.y) {
+        const int64_t at = int64_t(rq.row0) * a.n_q + i;
+        // weights of the splits (at most 64: one per lane), the same in every wavefront
+        const float e = lane < rq.splits ? a.lse[at + lane * step] : -INFINITY;
+        float m = e;
 #pragma unroll
-        for (int j = 0; j < DC; ++j) v[j] = 0.f;
-        for (int s = 0; s < rq.splits; ++s) {
-            const float e = a.lse[at + s * step];
-            if (e == -INFINITY) continue;
-            const float w = __builtin_amdgcn_exp2f(e - m);
-            l += w;
+        for (int k = 1; k < 64; k <<= 1) m = fmaxf(m, __shfl_xor(m, k));
+        const float w = e == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(e - m);
+        float l = w;
 #pragma unroll
-            for (int j = 0; j < DC; ++j) v[j] += w * a.part[(at + s * step) * D + j * 64 + lane];
+        for (int k = 1; k < 64; k <<= 1) l += __shfl_xor(l, k);
+        if (tid < 64) s_w[tid] = l == 0.f ? 0.f : w / l;
+        __syncthreads();
+        f32x4 v = {0.f, 0.f, 0.f, 0.f};
+        if (grp < kGroups) {
+            const f32x4 *p = reinterpret_cast<const f32x4 *>(a.part + at * D) + d;
+#pragma unroll 4
+            for (int s = grp; s < rq.splits; s += kGroups) {
+                const float ws = s_w[s];
+                const f32x4 x = p[s * step * (D / 4)];
+                if (ws != 0.f) v += x * ws;   // what an empty split left there is not looked at (a NaN weight is)
+            }
+            s_v[grp][d] = v;
         }
-        const float inv = l == 0.f ? 0.f : 1.0f / l;
-        const int64_t t = rq.row0 + i / a.n_q, h = i % a.n_q;
+        __syncthreads();
+        if (grp == 0) {
 #pragma unroll
-        for (int j = 0; j < DC; ++j)
-            a.out[t * a.ldo + h * a.hso + j * 64 + lane] = f32_to_bf16_rne(v[j] * inv);
+            for (int k = 1; k < kGroups; ++k) v += s_v[k][d];
+            uint2 u;
+            u.x = uint32_t(f32_to_bf16_rne(v.x)) | (uint32_t(f32_to_bf16_rne(v.y)) << 16);
+            u.y = uint32_t(f32_to_bf16_rne(v.z)) | (uint32_t(f32_to_bf16_rne(v.w)) << 16);
+            const int64_t t = rq.row0 + i / a.n_q, h = i % a.n_q;
+            *reinterpret_cast<uint2 *>(a.out + t * a.ldo + h * a.hso + 4 * d) = u;
+        }
+        __syncthreads();
     }
 }
 
 struct AttnShape {
-    int32_t splits, split_pages;
+    int32_t splits, split_pages, psplits, psplit_pages;
+    bool decode, prompt;   // kernels to run; one that runs alone takes every request
 };
 
-// Splits of the cached tokens: enough workgroups to fill the card a few times
-// over, each with a few pages at least.
+// Pages per split and splits, for `items` workgroups' worth of rows and heads:
+// `want` workgroups in all, at least `least` pages each.
+void split_pages_of(int64_t pages, int64_t items, int64_t want, int64_t least, int32_t &splits, int32_t &per_split) {
+    splits = 1;
+    per_split = int32_t(pages > 0 ? pages : 1);
+    const int64_t n = (want + items - 1) / items;
+    int64_t per = (pages + n - 1) / n;
+    if (per < least) per = least;
+    if (per * kMaxSplits < pages) per = (pages + kMaxSplits - 1) / kMaxSplits;
+    if (per < pages) {
+        splits = int32_t((pages + per - 1) / per);
+        per_split = int32_t(per);
+    }
+}
+
 AttnShape attn_shape(int64_t T, int64_t R, int32_t n_heads, int32_t n_q, int64_t max_q, int64_t max_kv) {
-    const int64_t pages = (max_kv + kPage - 1) / kPage;
-    const int64_t tiles = max_q > 0 ? (max_q * (n_q / n_heads) + 15) / 16 : 1;
-    const int64_t items = R * n_heads * tiles;
-    AttnShape s{1, int32_t(pages > 0 ? pages : 1)};
-    const int64_t want = (2048 + items - 1) / items;
-    int64_t per = (pages + want - 1) / want;
-    if (per < 4) per = 4;
-    int64_t n = (pages + per - 1) / per;
-    if (n > 64) { n = 64; per = (pages + n - 1) / n; n = (pages + per - 1) / per; }
-    if (n > 1) { s.splits = int32_t(n); s.split_pages = int32_t(per); }
-    (void)T;
+    const int64_t pages = (max_kv + kPage - 1) / kPage, group = n_q / n_heads;
+    AttnShape s{};
+    s.prompt = max_q * group > kDecodeCols;
+    s.decode = !s.prompt || R > 1;
+    const int64_t tiles = s.prompt ? (kDecodeCols + 15) / 16 : max_q > 0 ? (max_q * group + 15) / 16 : 1;
+    split_pages_of(pages, R * n_heads * tiles, 2048, 4, s.splits, s.split_pages);
+    // a prompt's partial results cost as much as its output sixteen times over: split only what leaves the card empty
+    const int64_t ptiles = (T * group + 127) / 128 + (R - 1);
+    split_pages_of(pages, ptiles * n_heads, 512, 8, s.psplits, s.psplit_pages);
+    if (!s.prompt) s.psplits = 1;
+    if (!s.decode) s.splits = 1;
     return s;
 }
 
@@ -330,17 +585,31 @@ ht_status check_attn(const ht_kv_cache *c, int64_t T, int64_t R, int32_t n_q, in
 }
 
 template <int DC>
-ht_status run_attn(const AttnArgs &a, int64_t R, int64_t max_q, hipStream_t s) {
-    const int64_t tiles = (max_q * a.group + 15) / 16;
-    const dim3 grid(uint32_t(R * a.n_heads), uint32_t(a.splits), uint32_t(tiles < 1 ? 1 : tiles > 4096 ? 4096 : tiles));
-    attn_decode_kernel<DC><<<grid, kAttnThreads, 0, s>>>(a);
-    HT_LAUNCH_CHECK();
-    if (a.splits > 1) {
-        int64_t y = (max_q * a.n_q + kWaves - 1) / kWaves;
-        attn_join_kernel<DC><<<dim3(uint32_t(R), uint32_t(y < 1 ? 1 : y > 1024 ? 1024 : y)), kAttnThreads, 0, s>>>(a);
+ht_status run_attn(const AttnArgs &a, const AttnShape &sh, int64_t R, int64_t max_q, hipStream_t s) {
+    const uint32_t x = uint32_t(R * a.n_heads);
+    if (sh.prompt) {
+        const int64_t tiles = (max_q * a.group + 127) / 128;
+        const dim3 grid(x, uint32_t(sh.psplits), uint32_t(tiles > 8192 ? 8192 : tiles));
+        attn_prompt_kernel<DC><<<grid, kAttnThreads, 0, s>>>(a);
+        HT_LAUNCH_CHECK();
+    }
+    if (sh.decode) {
+        const int64_t cols = sh.prompt ? kDecodeCols : max_q * a.group, tiles = cols > 16 ? (cols + 15) / 16 : 1;
+        attn_decode_kernel<DC><<<dim3(x, uint32_t(sh.splits), uint32_t(tiles)), kAttnThreads, 0, s>>>(a);
+        HT_LAUNCH_CHECK();
+    }
+    if (sh.splits > 1 || sh.psplits > 1) {
+        const int64_t y = (sh.psplits > 1 || !sh.prompt ? max_q : kDecodeCols / a.group) * a.n_q;
+        attn_join_kernel<DC><<<dim3(uint32_t(R), uint32_t(y < 1 ? 1 : y > 4096 ? 4096 : y)), kAttnThreads, 0, s>>>(a);
         HT_LAUNCH_CHECK();
     }
     return HT_OK;
+}
+
+// Splits that partial results are kept for.
+size_t partial_rows(const AttnShape &sh, int64_t T, int32_t n_q) {
+    const int32_t n = sh.splits > sh.psplits ? sh.splits : sh.psplits;
+    return n > 1 ? size_t(n) * size_t(T) * size_t(n_q) : 0;
 }
 
 }  // namespace
@@ -351,8 +620,8 @@ extern "C" ht_status ht_kv_attention_workspace(const ht_kv_cache *cache, int64_t
     const ht_status st = check_attn(cache, T, R, n_q, max_q, max_kv);
     if (st != HT_OK) return st;
     const AttnShape sh = attn_shape(T, R, cache->n_heads, n_q, max_q, max_kv);
-    const size_t rows = size_t(sh.splits) * size_t(T) * size_t(n_q);
-    *bytes = sh.splits > 1 ? size_t(align256(rows * 4u)) + rows * size_t(cache->head_dim) * 4u : 0;
+    const size_t rows = partial_rows(sh, T, n_q);
+    *bytes = size_t(align256(rows * 4u)) + rows * size_t(cache->head_dim) * 4u;
     return HT_OK;
 }
 
@@ -383,8 +652,7 @@ extern "C" ht_status ht_kv_attention(const uint16_t *q, int64_t ldq, int64_t hsq
     a.kv_len = kv_len;
     a.out = out;
     a.lse = static_cast<float *>(ws);
-    a.part = sh.splits > 1 ? static_cast<float *>(ws) + align256(size_t(sh.splits) * size_t(T) * size_t(n_q) * 4u) / 4
-                           : nullptr;
+    a.part = a.lse ? a.lse + align256(partial_rows(sh, T, n_q) * 4u) / 4 : nullptr;
     a.ldq = ldq; a.hsq = hsq; a.ldo = ldo; a.hso = hso; a.ldt = ldt; a.P = P;
     a.T = int32_t(T);
     a.n_q = n_q;
@@ -395,12 +663,16 @@ extern "C" ht_status ht_kv_attention(const uint16_t *q, int64_t ldq, int64_t hsq
     a.splits = sh.splits;
     a.split_pages = sh.split_pages;
     a.window = window;
-    a.scale_log2 = scale * kLog2e;
+    a.prompt_from = !sh.prompt ? INT32_MAX : sh.decode ? kDecodeCols + 1 : 0;
+    a.psplits = sh.psplits;
+    a.psplit_pages = sh.psplit_pages;
+    a.scale_log2 = (scale < 0.f ? -scale : scale) * kLog2e;
+    a.sign = scale < 0.f ? -1.f : 1.f;
     hipStream_t s = hipStream_t(stream);
     switch (cache->head_dim) {
-    case 64: return run_attn<1>(a, R, max_q, s);
-    case 128: return run_attn<2>(a, R, max_q, s);
-    case 192: return run_attn<3>(a, R, max_q, s);
-    default: return run_attn<4>(a, R, max_q, s);
+    case 64: return run_attn<1>(a, sh, R, max_q, s);
+    case 128: return run_attn<2>(a, sh, R, max_q, s);
+    case 192: return run_attn<3>(a, sh, R, max_q, s);
+    default: return run_attn<4>(a, sh, R, max_q, s);
     }
 }

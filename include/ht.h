@@ -554,8 +554,8 @@ ht_status ht_qk_norm_rope_backward(const void *dq, int64_t lddq, int64_t hsdq, c
  *             hsv elements apart;
  *   slots     int32 [T] (ht_kv_plan's): rows with a slot outside the cache
  *             (-1) are skipped.  The rows of one page must follow each other,
- *             in the order of their slots; the first one at offset 0 starts
- *             the page afresh (what it held does not count for the scale).
+ *             at consecutive slots; a row at offset 0 starts its page afresh
+ *             (what it held does not count for the scale).
  * Reproducible bit for bit; writing the same rows again changes nothing. */
 ht_status ht_kv_write(const void *k, int64_t ldk, int64_t hsk, int32_t kt, const void *v, int64_t ldv, int64_t hsv,
                       int32_t vt, int64_t T, const int32_t *slots, const ht_kv_cache *cache, ht_stream stream);
