@@ -81,6 +81,12 @@ __device__ __forceinline__ f16x8 codes_to_f16(uint32_t w0, uint32_t w1) {
     return r.v;
 }
 
+// Larger of lane i's and lane i + 32's (i - 32's) value.
+__device__ __forceinline__ float max_halves(float v) {
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+
 // 16 elements of a row of q as int8 planes hi, lo with n = rne(x 2^(14-E)) = 256 hi + lo.
 __device__ __forceinline__ void encode16(const uint16_t *x, float f, i32x4 &hi, i32x4 &lo) {
 #pragma unroll
@@ -394,7 +400,8 @@ __global__ __launch_bounds__(kAttnThreads, DC <= 2 ? 2 : 1) void attn_prompt_ker
             store_page(lds[0]);
         }
         for (int p = p_first, cur = 0; p < p_last; ++p, cur ^= 1) {
-            const float f = qs * ks, ef = float(exp_of_scale(vs) - 7);
+            // above 0 (or NaN), so that a masked score, -inf, stays one
+            const float f = qs * ks == 0.f ? 0x1p-120f : qs * ks, ef = float(exp_of_scale(vs) - 7);
             const float l_unit = pow2f(7 - exp_of_scale(vs));
             const bool shown = there;
             __syncthreads();   // this page is in LDS; the other buffer has been read
@@ -427,8 +434,7 @@ __global__ __launch_bounds__(kAttnThreads, DC <= 2 ? 2 : 1) void attn_prompt_ker
                 for (int b = 0; b < 2; ++b)
 #pragma unroll
                     for (int i = 0; i < 16; ++i) top = fmaxf(top, s[b][i]);
-                top = top == -INFINITY ? -INFINITY : top * f + ef;   // f >= 0
-                top = fmaxf(top, __shfl_xor(top, 32));
+                top = max_halves(top * f + ef);
                 const float m_new = fmaxf(m_run, top);
                 if (__any(m_new > m_run)) {
                     const float alpha = m_run == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m_run - m_new);
@@ -444,8 +450,7 @@ __global__ __launch_bounds__(kAttnThreads, DC <= 2 ? 2 : 1) void attn_prompt_ker
                 for (int b = 0; b < 2; ++b)
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
-                        float x = __builtin_amdgcn_exp2f(s[b][i] * f + shift);
-                        if (edge && s[b][i] == -INFINITY) x = 0.f;   // f may be 0
+                        const float x = __builtin_amdgcn_exp2f(s[b][i] * f + shift);
                         sum += x;
                         w[2 * b + (i >> 3)][i & 7] = _Float16(x);
                     }
@@ -460,13 +465,15 @@ __global__ __launch_bounds__(kAttnThreads, DC <= 2 ? 2 : 1) void attn_prompt_ker
         }
         const float l = l_run + __shfl_xor(l_run, 32);
         if (live) {
-            const float inv = l == 0.f ? 0.f : 1.0f / l;
+            const bool none = l == 0.f || hi <= lo;
+            const float inv = 1.0f / l;
             const int64_t at = (int64_t(split) * a.T + t) * a.n_q + hq;
 #pragma unroll
             for (int d = 0; d < DB; ++d)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const f32x4 v = {o[d][4 * i] * inv, o[d][4 * i + 1] * inv, o[d][4 * i + 2] * inv, o[d][4 * i + 3] * inv};
+                    f32x4 v = {o[d][4 * i] * inv, o[d][4 * i + 1] * inv, o[d][4 * i + 2] * inv, o[d][4 * i + 3] * inv};
+                    if (none) v = f32x4{0.f, 0.f, 0.f, 0.f};
                     const int dim = d * 32 + 8 * i + 4 * h;
                     if (rq.splits == 1) {
                         uint2 u;
@@ -478,7 +485,7 @@ __global__ __launch_bounds__(kAttnThreads, DC <= 2 ? 2 : 1) void attn_prompt_ker
                     }
                 }
             if (rq.splits > 1 && h == 0)
-                a.lse[at] = l == 0.f ? -INFINITY : (m_run == -INFINITY ? 0.f : m_run) + log2f(l);
+                a.lse[at] = none ? -INFINITY : (m_run == -INFINITY ? 0.f : m_run) + log2f(l);
         }
     }
 }
