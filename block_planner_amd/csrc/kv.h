@@ -44,7 +44,7 @@ inline ht_status check_cache(const ht_kv_cache *c) {
     if (!c || !c->codes || !c->scales) return HT_EINVAL;
     if (c->n_pages <= 0 || c->n_pages * kPage >= (int64_t(1) << 31) || c->n_heads <= 0 || c->n_heads > 1024) return HT_ESHAPE;
     if (c->head_dim <= 0 || c->head_dim % 64 || c->head_dim > 256) return HT_ESHAPE;
-    if (!al16p(c->codes) || !al4(c->scales)) return HT_EALIGN;
+    if (!al16p(c->codes) || !al16p(c->scales)) return HT_EALIGN;
     return HT_OK;
 }
 

@@ -281,7 +281,7 @@ __global__ __launch_bounds__(kAttnThreads) void attn_decode_kernel(AttnArgs a) {
     }
 }
 
-// Prompts: tiles of 128 columns, 32 per wavefront, over all pages of a split.
+// Prompts: tiles of 32 columns per wavefront, 4 or 8 wavefronts, over all pages of a split.
 //
 // A page's codes are turned into fp16 (exactly) once per workgroup and put in
 // LDS in the order in which the 32x32x16 fp16 MFMAs take them, K as their A
@@ -290,10 +290,11 @@ __global__ __launch_bounds__(kAttnThreads) void attn_decode_kernel(AttnArgs a) {
 // operand takes its tokens in that same order, so the weights go from one
 // product to the next in registers.  The next page is loaded into registers
 // while this one is multiplied, and converted into the other LDS buffer after.
-template <int DC>
-__global__ __launch_bounds__(kAttnThreads, DC <= 2 ? 2 : 1) void attn_prompt_kernel(AttnArgs a) {
-    constexpr int D = 64 * DC, KS = D / 16, DB = D / 32, kHalf = 64 * D * 2 / 16;   // 16-byte pieces of K's half
-    __shared__ f16x8 lds[2][2 * kHalf];
+template <int DC, int NW>
+__global__ __launch_bounds__(64 * NW, DC <= 2 ? 2 : 1) void attn_prompt_kernel(AttnArgs a) {
+    constexpr int D = 64 * DC, KS = D / 16, DB = D / 32, kCols = 32 * NW, kThr = 64 * NW;
+    constexpr int kPieces = 4 * D, kPer = (kPieces + kThr - 1) / kThr;   // 16-byte pieces of K (and of V), per thread
+    __shared__ f16x8 k_lds[2][kPage * D / 8], v_lds[2][kPage * D / 8];
     const int tid = threadIdx.x, lane = tid & 63, wv = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int col = lane & 31, h = lane >> 5;
     const int r = int(blockIdx.x) / a.n_heads, head = int(blockIdx.x) % a.n_heads;
@@ -302,12 +303,12 @@ __global__ __launch_bounds__(kAttnThreads, DC <= 2 ? 2 : 1) void attn_prompt_ker
     if (rq.rows == 0 || !rq.prompt || split >= rq.splits) return;
     const int pa = rq.p0 + split * rq.split_pages;
     const int pb = split == rq.splits - 1 ? rq.p1 : min(rq.p1, pa + rq.split_pages);
-    const int n_cols = rq.rows * a.group, n_tiles = (n_cols + 127) / 128;
+    const int n_cols = rq.rows * a.group, n_tiles = (n_cols + kCols - 1) / kCols;
     const int32_t *row_of_table = a.table + int64_t(r) * a.ldt;
 
     // the last tiles first: under a causal mask they see the most
     for (int tile = n_tiles - 1 - int(blockIdx.z); tile >= 0; tile -= int(gridDim.z)) {
-        const int c0 = tile * 128, c = c0 + wv * 32 + col;
+        const int c0 = tile * kCols, c = c0 + wv * 32 + col;
         const bool live = c < n_cols;
         const int qi = (live ? c : c0) / a.group, gh = (live ? c : c0) - qi * a.group;
         const int t = rq.row0 + qi, hq = head * a.group + gh;
@@ -317,7 +318,7 @@ __global__ __launch_bounds__(kAttnThreads, DC <= 2 ? 2 : 1) void attn_prompt_ker
         // ranges of the tile and of this wavefront's columns (lo and hi never fall from row to row)
         int t_lo, t_hi, w_lo_max, w_hi_min, unused;
         row_range(a, rq, c0 / a.group, t_lo, unused);
-        row_range(a, rq, (min(c0 + 128, n_cols) - 1) / a.group, unused, t_hi);
+        row_range(a, rq, (min(c0 + kCols, n_cols) - 1) / a.group, unused, t_hi);
         const int w_first = min(c0 + wv * 32, n_cols - 1), w_last = min(c0 + wv * 32 + 31, n_cols - 1);
         row_range(a, rq, w_first / a.group, unused, w_hi_min);
         row_range(a, rq, w_last / a.group, w_lo_max, unused);
@@ -349,43 +350,63 @@ __global__ __launch_bounds__(kAttnThreads, DC <= 2 ? 2 : 1) void attn_prompt_ker
             qs = bad ? __uint_as_float(0x7FC00000u) : pow2f(e - 14) * a.scale_log2;
         }
 
-        u32x4 kr[DC];
-        uint2 vr[DC][2];
-        float ks, vs;
-        bool there;
-        const auto load_page = [&](int p) {
-            int32_t page = p < pb ? __builtin_amdgcn_readfirstlane(row_of_table[p]) : -1;
-            there = page >= 0 && page < a.n_pages;
-            if (!there) page = 0;
-            const int64_t blk = (int64_t(page) * a.n_heads + head) * 2;
-            const int8_t *kp = a.codes + blk * (kPage * D), *vp = kp + kPage * D;
-            ks = a.scales[blk];
-            vs = a.scales[blk + 1];
+        u32x4 kr[kPer];
+        uint2 vr[kPer][2];
+        const auto id_of = [&](int p) {
+            const int32_t id = p < p_last ? row_of_table[p] : -1;
+            return __builtin_amdgcn_readfirstlane(id >= 0 && id < a.n_pages ? id : -1);
+        };
+        // a page that is not there reads page 0 and is masked
+        const auto block_of = [&](int id) { return (int64_t(id < 0 ? 0 : id) * a.n_heads + head) * 2; };
+        const auto load_k = [&](int id) {
+            const int8_t *kp = a.codes + block_of(id) * (kPage * D);
 #pragma unroll
-            for (int j = 0; j < DC; ++j) {
-                kr[j] = *reinterpret_cast<const u32x4 *>(kp + (j * kAttnThreads + tid) * 16);
+            for (int j = 0; j < kPer; ++j)
+                if (kPieces % kThr == 0 || j * kThr + tid < kPieces)
+                    kr[j] = *reinterpret_cast<const u32x4 *>(kp + (j * kThr + tid) * 16);
+        };
+        const auto load_v = [&](int id) {
+            const int8_t *vp = a.codes + (block_of(id) + 1) * (kPage * D);
+#pragma unroll
+            for (int j = 0; j < kPer; ++j) {
                 // two token groups g and g + 2 of a dim, half of their 16 tokens
-                const int u = j * kAttnThreads + tid, m = u & 15, g = (u >> 4) & 1, half = (u >> 5) & 1, e = u >> 6;
+                const int u = j * kThr + tid, m = u & 15, g = (u >> 4) & 1, half = (u >> 5) & 1, e = u >> 6;
+                if (kPieces % kThr != 0 && u >= kPieces) break;
                 const int8_t *v = vp + ((e * 4 + g) * 16 + m) * 16 + half * 8;
                 vr[j][0] = *reinterpret_cast<const uint2 *>(v);
                 vr[j][1] = *reinterpret_cast<const uint2 *>(v + 512);
             }
         };
-        const auto store_page = [&](f16x8 *b) {
+        const auto store_k = [&](f16x8 *b) {   // 16 dims of a token: both halves of the lanes of one operand
 #pragma unroll
-            for (int j = 0; j < DC; ++j) {
-                const int u = j * kAttnThreads + tid;
-                {   // 16 dims of a token: both halves of the lanes of one K operand
-                    const int rr = u & 15, g = (u >> 4) & 3, cc = (u >> 6) % DC, aa = (u >> 6) / DC;
-                    f16x8 *d = b + ((aa >> 1) * KS + cc * 4 + g) * 64 + (aa & 1) * 16 + rr;
-                    d[0] = codes_to_f16(kr[j].x, kr[j].y);
-                    d[32] = codes_to_f16(kr[j].z, kr[j].w);
-                }
-                const int m = u & 15, g = (u >> 4) & 1, half = (u >> 5) & 1, e = u >> 6;
-                f16x8 *d = b + kHalf + ((e >> 1) * 4 + half * 2) * 64 + g * 32 + (e & 1) * 16 + m;
+            for (int j = 0; j < kPer; ++j) {
+                const int u = j * kThr + tid, rr = u & 15, g = (u >> 4) & 3, cc = (u >> 6) % DC, aa = (u >> 6) / DC;
+                if (kPieces % kThr != 0 && u >= kPieces) break;
+                f16x8 *d = b + ((aa >> 1) * KS + cc * 4 + g) * 64 + (aa & 1) * 16 + rr;
+                d[0] = codes_to_f16(kr[j].x, kr[j].y);
+                d[32] = codes_to_f16(kr[j].z, kr[j].w);
+            }
+        };
+        const auto store_v = [&](f16x8 *b) {
+#pragma unroll
+            for (int j = 0; j < kPer; ++j) {
+                const int u = j * kThr + tid, m = u & 15, g = (u >> 4) & 1, half = (u >> 5) & 1, e = u >> 6;
+                if (kPieces % kThr != 0 && u >= kPieces) break;
+                f16x8 *d = b + ((e >> 1) * 4 + half * 2) * 64 + g * 32 + (e & 1) * 16 + m;
                 d[0] = codes_to_f16(vr[j][0].x, vr[j][1].x);
                 d[64] = codes_to_f16(vr[j][0].y, vr[j][1].y);
             }
+        };
+        const auto scores = [&](const f16x8 *kb, f32x16 *s) {
+#pragma unroll
+            for (int b = 0; b < 2; ++b)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) s[b][i] = 0.f;
+#pragma unroll
+            for (int k = 0; k < KS; ++k)
+#pragma unroll
+                for (int b = 0; b < 2; ++b)
+                    s[b] = __builtin_amdgcn_mfma_f32_32x32x16_f16(kb[(b * KS + k) * 64 + lane], q[k], s[b], 0, 0, 0);
         };
 
         f32x16 o[DB];
@@ -394,74 +415,86 @@ __global__ __launch_bounds__(kAttnThreads, DC <= 2 ? 2 : 1) void attn_prompt_ker
 #pragma unroll
             for (int i = 0; i < 16; ++i) o[d][i] = 0.f;
         float m_run = -INFINITY, l_run = 0.f;
-        if (p_first < p_last) {
-            load_page(p_first);
-            __syncthreads();   // the tile before has been read
-            store_page(lds[0]);
-        }
-        for (int p = p_first, cur = 0; p < p_last; ++p, cur ^= 1) {
+        int id0 = -1, id1 = -1, id2 = -1;   // pages p, p + 1, p + 2
+        float2 sc = {0.f, 0.f};             // scales of page p
+        f32x16 s0[2], s1[2];
+        // One page: its scores are in s; the next page's go to n while these
+        // are turned into weights.  K is one page ahead of V in LDS.
+        const auto page_step = [&](int p, f32x16 *s, f32x16 *n, int cur) {
+            __syncthreads();   // K of p + 1 and V of p are in LDS; K of p and V of p - 1 have been read
+            load_k(id2);
+            load_v(id1);
+            const float2 sc_next = *reinterpret_cast<const float2 *>(a.scales + block_of(id1));
+            const int id3 = id_of(p + 3);
+            const int ev = exp_of_scale(sc.y) - 7;
             // above 0 (or NaN), so that a masked score, -inf, stays one
-            const float f = qs * ks == 0.f ? 0x1p-120f : qs * ks, ef = float(exp_of_scale(vs) - 7);
-            const float l_unit = pow2f(7 - exp_of_scale(vs));
-            const bool shown = there;
-            __syncthreads();   // this page is in LDS; the other buffer has been read
-            if (p + 1 < p_last) load_page(p + 1);
-            if (shown) {
-                const f16x8 *kb = lds[cur], *vb = lds[cur] + kHalf;
-                f32x16 s[2];
-#pragma unroll
-                for (int b = 0; b < 2; ++b)
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) s[b][i] = 0.f;
-#pragma unroll
-                for (int k = 0; k < KS; ++k)
-#pragma unroll
-                    for (int b = 0; b < 2; ++b)
-                        s[b] = __builtin_amdgcn_mfma_f32_32x32x16_f16(kb[(b * KS + k) * 64 + lane], q[k], s[b], 0, 0, 0);
-                const int j0 = p * kPage;
-                const bool edge = j0 < w_lo_max || j0 + kPage > w_hi_min;
-                if (edge) {
-#pragma unroll
-                    for (int b = 0; b < 2; ++b)
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            const int j = j0 + b * 32 + 8 * (i >> 2) + 4 * h + (i & 3);
-                            if (j < lo || j >= hi) s[b][i] = -INFINITY;
-                        }
-                }
-                float top = s[0][0];
-#pragma unroll
-                for (int b = 0; b < 2; ++b)
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) top = fmaxf(top, s[b][i]);
-                top = max_halves(top * f + ef);
-                const float m_new = fmaxf(m_run, top);
-                if (__any(m_new > m_run)) {
-                    const float alpha = m_run == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m_run - m_new);
-                    l_run *= alpha;
-#pragma unroll
-                    for (int d = 0; d < DB; ++d) o[d] *= alpha;
-                    m_run = m_new;
-                }
-                const float shift = ef - (m_run == -INFINITY ? 0.f : m_run - kTopLog2);
-                float sum = 0.f;
-                f16x8 w[4];
+            const float f = qs * sc.x == 0.f ? 0x1p-120f : qs * sc.x, ef = float(ev);
+            const int j0 = p * kPage;
+            if (id0 < 0 || j0 < w_lo_max || j0 + kPage > w_hi_min) {
+                const int seen = id0 < 0 ? 0 : hi;
 #pragma unroll
                 for (int b = 0; b < 2; ++b)
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
-                        const float x = __builtin_amdgcn_exp2f(s[b][i] * f + shift);
-                        sum += x;
-                        w[2 * b + (i >> 3)][i & 7] = _Float16(x);
+                        const int j = j0 + b * 32 + 8 * (i >> 2) + 4 * h + (i & 3);
+                        if (j < lo || j >= seen) s[b][i] = -INFINITY;
                     }
-                l_run += sum * l_unit;
-#pragma unroll
-                for (int b = 0; b < 4; ++b)
-#pragma unroll
-                    for (int d = 0; d < DB; ++d)
-                        o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vb[(d * 4 + b) * 64 + lane], w[b], o[d], 0, 0, 0);
             }
-            if (p + 1 < p_last) store_page(lds[cur ^ 1]);
+            scores(k_lds[cur ^ 1], n);
+            float top = s[0][0];
+#pragma unroll
+            for (int b = 0; b < 2; ++b)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) top = fmaxf(top, s[b][i]);
+            const float m_new = fmaxf(m_run, max_halves(top * f + ef));
+            const float shift = ef - (m_new == -INFINITY ? 0.f : m_new - kTopLog2);
+            const float alpha = m_run == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m_run - m_new);
+            float sum = 0.f;
+            f16x8 w[4];
+#pragma unroll
+            for (int b = 0; b < 2; ++b)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const float x = __builtin_amdgcn_exp2f(s[b][i] * f + shift);
+                    sum += x;
+                    w[2 * b + (i >> 3)][i & 7] = _Float16(x);
+                }
+            l_run = l_run * alpha + sum * pow2f(-ev);
+            if (__any(m_new > m_run)) {
+#pragma unroll
+                for (int d = 0; d < DB; ++d) o[d] *= alpha;
+            }
+            m_run = m_new;
+#pragma unroll
+            for (int b = 0; b < 4; ++b)
+#pragma unroll
+                for (int d = 0; d < DB; ++d)
+                    o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v_lds[cur][(d * 4 + b) * 64 + lane], w[b], o[d], 0, 0, 0);
+            store_k(k_lds[cur]);
+            store_v(v_lds[cur ^ 1]);
+            id0 = id1;
+            id1 = id2;
+            id2 = id3;
+            sc = sc_next;
+        };
+        if (p_first < p_last) {
+            id0 = id_of(p_first);
+            id1 = id_of(p_first + 1);
+            id2 = id_of(p_first + 2);
+            sc = *reinterpret_cast<const float2 *>(a.scales + block_of(id0));
+            load_k(id0);
+            load_v(id0);
+            __syncthreads();   // the tile before has been read
+            store_k(k_lds[0]);
+            store_v(v_lds[0]);
+            load_k(id1);
+            store_k(k_lds[1]);
+            __syncthreads();
+            scores(k_lds[0], s0);
+            for (int p = p_first; p < p_last; p += 2) {
+                page_step(p, s0, s1, 0);
+                if (p + 1 < p_last) page_step(p + 1, s1, s0, 1);
+            }
         }
         const float l = l_run + __shfl_xor(l_run, 32);
         if (live) {
@@ -543,6 +576,7 @@ __global__ __launch_bounds__(kAttnThreads) void attn_join_kernel(AttnArgs a) {
 struct AttnShape {
     int32_t splits, split_pages, psplits, psplit_pages;
     bool decode, prompt;   // kernels to run; one that runs alone takes every request
+    int32_t waves;         // of the prompt kernel's workgroups
 };
 
 // Pages per split and splits, for `items` workgroups' worth of rows and heads:
@@ -560,7 +594,7 @@ void split_pages_of(int64_t pages, int64_t items, int64_t want, int64_t least, i
     }
 }
 
-AttnShape attn_shape(int64_t T, int64_t R, int32_t n_heads, int32_t n_q, int64_t max_q, int64_t max_kv) {
+AttnShape attn_shape(int64_t T, int64_t R, int32_t n_heads, int32_t D, int32_t n_q, int64_t max_q, int64_t max_kv) {
     const int64_t pages = (max_kv + kPage - 1) / kPage, group = n_q / n_heads;
     AttnShape s{};
     s.prompt = max_q * group > kDecodeCols;
@@ -568,7 +602,8 @@ AttnShape attn_shape(int64_t T, int64_t R, int32_t n_heads, int32_t n_q, int64_t
     const int64_t tiles = s.prompt ? (kDecodeCols + 15) / 16 : max_q > 0 ? (max_q * group + 15) / 16 : 1;
     split_pages_of(pages, R * n_heads * tiles, 2048, 4, s.splits, s.split_pages);
     // a prompt's partial results cost as much as its output sixteen times over: split only what leaves the card empty
-    const int64_t ptiles = (T * group + 127) / 128 + (R - 1);
+    s.waves = D <= 128 ? 8 : 4;
+    const int64_t cols = 32 * s.waves, ptiles = (T * group + cols - 1) / cols + (R - 1);
     split_pages_of(pages, ptiles * n_heads, 512, 8, s.psplits, s.psplit_pages);
     if (!s.prompt) s.psplits = 1;
     if (!s.decode) s.splits = 1;
@@ -595,9 +630,12 @@ template <int DC>
 ht_status run_attn(const AttnArgs &a, const AttnShape &sh, int64_t R, int64_t max_q, hipStream_t s) {
     const uint32_t x = uint32_t(R * a.n_heads);
     if (sh.prompt) {
-        const int64_t tiles = (max_q * a.group + 127) / 128;
+        const int64_t cols = 32 * sh.waves, tiles = (max_q * a.group + cols - 1) / cols;
         const dim3 grid(x, uint32_t(sh.psplits), uint32_t(tiles > 8192 ? 8192 : tiles));
-        attn_prompt_kernel<DC><<<grid, kAttnThreads, 0, s>>>(a);
+        if constexpr (DC <= 2) {
+            if (sh.waves == 8) attn_prompt_kernel<DC, 8><<<grid, 512, 0, s>>>(a);
+        }
+        if (sh.waves == 4) attn_prompt_kernel<DC, 4><<<grid, 256, 0, s>>>(a);
         HT_LAUNCH_CHECK();
     }
     if (sh.decode) {
@@ -626,7 +664,7 @@ extern "C" ht_status ht_kv_attention_workspace(const ht_kv_cache *cache, int64_t
     if (!bytes) return HT_EINVAL;
     const ht_status st = check_attn(cache, T, R, n_q, max_q, max_kv);
     if (st != HT_OK) return st;
-    const AttnShape sh = attn_shape(T, R, cache->n_heads, n_q, max_q, max_kv);
+    const AttnShape sh = attn_shape(T, R, cache->n_heads, cache->head_dim, n_q, max_q, max_kv);
     const size_t rows = partial_rows(sh, T, n_q);
     *bytes = size_t(align256(rows * 4u)) + rows * size_t(cache->head_dim) * 4u;
     return HT_OK;
@@ -649,7 +687,7 @@ extern "C" ht_status ht_kv_attention(const uint16_t *q, int64_t ldq, int64_t hsq
     size_t need = 0;
     if ((st = ht_kv_attention_workspace(cache, T, R, n_q, max_q, max_kv, &need)) != HT_OK) return st;
     if (need > 0 && (!ws || ws_bytes < need)) return HT_ESMALL;
-    const AttnShape sh = attn_shape(T, R, cache->n_heads, n_q, max_q, max_kv);
+    const AttnShape sh = attn_shape(T, R, cache->n_heads, cache->head_dim, n_q, max_q, max_kv);
     AttnArgs a{};
     a.q = q;
     a.codes = cache->codes;
