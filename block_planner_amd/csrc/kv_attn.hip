@@ -293,6 +293,7 @@ __global__ __launch_bounds__(kAttnThreads) void attn_decode_kernel(AttnArgs a) {
 template <int DC, int NW>
 __global__ __launch_bounds__(64 * NW, DC <= 2 ? 2 : 1) void attn_prompt_kernel(AttnArgs a) {
     constexpr int D = 64 * DC, KS = D / 16, DB = D / 32, kCols = 32 * NW, kThr = 64 * NW;
+    constexpr int kAhead = 4;                                            // operands read ahead of their product
     constexpr int kPieces = 4 * D, kPer = (kPieces + kThr - 1) / kThr;   // 16-byte pieces of K (and of V), per thread
     __shared__ f16x8 k_lds[2][kPage * D / 8], v_lds[2][kPage * D / 8];
     const int tid = threadIdx.x, lane = tid & 63, wv = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -352,9 +353,12 @@ __global__ __launch_bounds__(64 * NW, DC <= 2 ? 2 : 1) void attn_prompt_kernel(A
 
         u32x4 kr[kPer];
         uint2 vr[kPer][2];
-        const auto id_of = [&](int p) {
-            const int32_t id = p < p_last ? row_of_table[p] : -1;
-            return __builtin_amdgcn_readfirstlane(id >= 0 && id < a.n_pages ? id : -1);
+        // Table entries are loaded a step before they are looked at, ahead of that
+        // step's codes: waiting for an entry at once would wait for the codes too.
+        const auto entry = [&](int p) { return row_of_table[min(p, p_last - 1)]; };
+        const auto id_of = [&](int32_t e, int p) {
+            const int32_t id = __builtin_amdgcn_readfirstlane(e);
+            return p < p_last && id >= 0 && id < a.n_pages ? id : -1;
         };
         // a page that is not there reads page 0 and is masked
         const auto block_of = [&](int id) { return (int64_t(id < 0 ? 0 : id) * a.n_heads + head) * 2; };
@@ -415,17 +419,19 @@ __global__ __launch_bounds__(64 * NW, DC <= 2 ? 2 : 1) void attn_prompt_kernel(A
 #pragma unroll
             for (int i = 0; i < 16; ++i) o[d][i] = 0.f;
         float m_run = -INFINITY, l_run = 0.f;
-        int id0 = -1, id1 = -1, id2 = -1;   // pages p, p + 1, p + 2
+        int id0 = -1, id1 = -1;             // pages p, p + 1
+        int32_t e2 = -1;                    // table entry of p + 2
         float2 sc = {0.f, 0.f};             // scales of page p
         f32x16 s0[2], s1[2];
         // One page: its scores are in s; the next page's go to n while these
         // are turned into weights.  K is one page ahead of V in LDS.
         const auto page_step = [&](int p, f32x16 *s, f32x16 *n, int cur) {
             __syncthreads();   // K of p + 1 and V of p are in LDS; K of p and V of p - 1 have been read
+            const int id2 = id_of(e2, p + 2);
+            e2 = entry(p + 3);
             load_k(id2);
             load_v(id1);
             const float2 sc_next = *reinterpret_cast<const float2 *>(a.scales + block_of(id1));
-            const int id3 = id_of(p + 3);
             const int ev = exp_of_scale(sc.y) - 7;
             // above 0 (or NaN), so that a masked score, -inf, stays one
             const float f = qs * sc.x == 0.f ? 0x1p-120f : qs * sc.x, ef = float(ev);
@@ -440,47 +446,69 @@ __global__ __launch_bounds__(64 * NW, DC <= 2 ? 2 : 1) void attn_prompt_kernel(A
                         if (j < lo || j >= seen) s[b][i] = -INFINITY;
                     }
             }
-            scores(k_lds[cur ^ 1], n);
             float top = s[0][0];
 #pragma unroll
             for (int b = 0; b < 2; ++b)
 #pragma unroll
                 for (int i = 0; i < 16; ++i) top = fmaxf(top, s[b][i]);
             const float m_new = fmaxf(m_run, max_halves(top * f + ef));
-            const float shift = ef - (m_new == -INFINITY ? 0.f : m_new - kTopLog2);
-            const float alpha = m_run == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m_run - m_new);
+            if (__any(m_new > m_run)) {
+                const float alpha = m_run == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m_run - m_new);
+                l_run *= alpha;
+#pragma unroll
+                for (int d = 0; d < DB; ++d) o[d] *= alpha;
+                m_run = m_new;
+            }
+            const float shift = ef - (m_run == -INFINITY ? 0.f : m_run - kTopLog2);
+            // The next page's 2 KS products with this page's 32 weights between
+            // them, then this page's 4 DB products with the conversions of the
+            // pages behind: matrix and vector instructions side by side, operands
+            // read kAhead products early.  The order is fixed here step by step
+            // (left alone, the products come in one run and the rest after it).
+            const f16x8 *kb = k_lds[cur ^ 1] + lane, *vb = v_lds[cur] + lane;
+            f16x8 fr[kAhead];
             float sum = 0.f;
             f16x8 w[4];
 #pragma unroll
+            for (int i = 0; i < kAhead; ++i) fr[i] = kb[((i & 1) * KS + (i >> 1)) * 64];
+#pragma unroll
             for (int b = 0; b < 2; ++b)
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const float x = __builtin_amdgcn_exp2f(s[b][i] * f + shift);
+                for (int i = 0; i < 16; ++i) n[b][i] = 0.f;
+#pragma unroll
+            for (int i = 0; i < 2 * KS; ++i) {
+                __builtin_amdgcn_sched_barrier(0);
+                n[i & 1] = __builtin_amdgcn_mfma_f32_32x32x16_f16(fr[i % kAhead], q[i >> 1], n[i & 1], 0, 0, 0);
+                const int next = i + kAhead;
+                if (next < 2 * KS) fr[i % kAhead] = kb[((next & 1) * KS + (next >> 1)) * 64];
+                else fr[i % kAhead] = vb[((next - 2 * KS) % DB * 4 + (next - 2 * KS) / DB) * 64];
+#pragma unroll
+                for (int j = i * 32 / (2 * KS); j < (i + 1) * 32 / (2 * KS); ++j) {
+                    const float x = __builtin_amdgcn_exp2f(s[j >> 4][j & 15] * f + shift);
                     sum += x;
-                    w[2 * b + (i >> 3)][i & 7] = _Float16(x);
+                    w[j >> 3][j & 7] = _Float16(x);
                 }
-            l_run = l_run * alpha + sum * pow2f(-ev);
-            if (__any(m_new > m_run)) {
-#pragma unroll
-                for (int d = 0; d < DB; ++d) o[d] *= alpha;
             }
-            m_run = m_new;
+            l_run += sum * pow2f(-ev);
 #pragma unroll
-            for (int b = 0; b < 4; ++b)
-#pragma unroll
-                for (int d = 0; d < DB; ++d)
-                    o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v_lds[cur][(d * 4 + b) * 64 + lane], w[b], o[d], 0, 0, 0);
-            store_k(k_lds[cur]);
-            store_v(v_lds[cur ^ 1]);
+            for (int i = 0; i < 4 * DB; ++i) {
+                __builtin_amdgcn_sched_barrier(0);
+                const int at = (2 * KS + i) % kAhead, next = i + kAhead;
+                o[i % DB] = __builtin_amdgcn_mfma_f32_32x32x16_f16(fr[at], w[i / DB], o[i % DB], 0, 0, 0);
+                if (next < 4 * DB) fr[at] = vb[(next % DB * 4 + next / DB) * 64];
+                if (i == DB) store_k(k_lds[cur]);
+                if (i == 2 * DB) store_v(v_lds[cur ^ 1]);
+            }
+            __builtin_amdgcn_sched_barrier(0);
             id0 = id1;
             id1 = id2;
-            id2 = id3;
             sc = sc_next;
         };
         if (p_first < p_last) {
-            id0 = id_of(p_first);
-            id1 = id_of(p_first + 1);
-            id2 = id_of(p_first + 2);
+            const int32_t e0 = entry(p_first), e1 = entry(p_first + 1);
+            e2 = entry(p_first + 2);
+            id0 = id_of(e0, p_first);
+            id1 = id_of(e1, p_first + 1);
             sc = *reinterpret_cast<const float2 *>(a.scales + block_of(id0));
             load_k(id0);
             load_v(id0);
