@@ -202,20 +202,26 @@ def _table(t: torch.Tensor, R: int) -> None:
 def _rows(t: torch.Tensor, name: str) -> torch.Tensor:
     """[T, heads, D] fp32 or bf16 as the kernels read it: the last dim dense,
     pointer and strides in whole 16-byte pieces (a copy where they are not)."""
-    if t.dim() != 3 or t.dtype not in (torch.float32, torch.bfloat16):
-        raise ValueError(f"{name}: expected fp32 or bf16 [rows, heads, dim], got {t.dtype} {tuple(t.shape)}")
-    size, (rs, hs, ds) = t.element_size(), t.stride()
-    T, H, D = t.shape
-    if (ds == 1 and (rs * size) % 16 == 0 and ((hs * size) % 16 == 0 or H == 1) and t.data_ptr() % 16 == 0
-            and rs >= D and (hs >= D or H == 1)):
+    shape, dt = t.shape, t.dtype
+    if len(shape) != 3 or (dt is not torch.float32 and dt is not torch.bfloat16):
+        raise ValueError(f"{name}: expected fp32 or bf16 [rows, heads, dim], got {dt} {tuple(shape)}")
+    rs, hs, ds = t.stride()
+    D, piece = shape[2], 3 if dt is torch.float32 else 7      # strides in 16-byte pieces
+    if ds == 1 and rs >= D and not rs & piece and (shape[1] == 1 or (hs >= D and not hs & piece)) and not t.data_ptr() & 15:
         return t
     return t.clone(memory_format=torch.contiguous_format)
 
 
 def _out_rows(t: torch.Tensor, name: str, shape, dtype) -> torch.Tensor:
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or t.stride(2) != 1:
+    if t.dtype is not dtype or t.shape != shape or t.stride(2) != 1:
         raise ValueError(f"{name}: expected {dtype} {tuple(shape)} with a dense last dim, got {t.dtype} {tuple(t.shape)}")
     return t
+
+
+def _scratch(nbytes: int, device) -> torch.Tensor | None:
+    """Workspace of a call that needs 16-byte alignment (torch's allocator
+    gives 512)."""
+    return torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
 
 
 def kv_cache(n_pages: int, n_kv_heads: int, head_dim: int, device) -> tuple:
@@ -227,12 +233,13 @@ def kv_cache(n_pages: int, n_kv_heads: int, head_dim: int, device) -> tuple:
 
 
 def _cache_desc(codes: torch.Tensor, scales: torch.Tensor) -> B.KVCacheDesc:
-    if codes.dim() != 4 or codes.dtype != torch.int8 or codes.shape[2] != 2 or codes.shape[3] % B.HT_KV_PAGE:
-        raise ValueError(f"codes: expected int8 [pages, heads, 2, 64 * dim], got {codes.dtype} {tuple(codes.shape)}")
+    shape = codes.shape
+    if len(shape) != 4 or codes.dtype is not torch.int8 or shape[2] != 2 or shape[3] % B.HT_KV_PAGE:
+        raise ValueError(f"codes: expected int8 [pages, heads, 2, 64 * dim], got {codes.dtype} {tuple(shape)}")
     if not codes.is_contiguous():
         raise ValueError("codes: expected a contiguous tensor")
-    _need(scales, "scales", torch.float32, codes.shape[:3])
-    return B.kv_cache_desc(codes, scales)
+    _need(scales, "scales", torch.float32, shape[:3])
+    return B.KVCacheDesc(codes.data_ptr(), scales.data_ptr(), shape[0], shape[1], shape[3] // B.HT_KV_PAGE)
 
 
 def kv_cache_values(codes: torch.Tensor, scales: torch.Tensor) -> tuple:
@@ -277,9 +284,10 @@ def kv_plan(q_len: torch.Tensor, kv_len: torch.Tensor, owned: torch.Tensor, tabl
     if out is None:
         out = kv_step(R, T, q_len.device)
     else:
-        out = KVStep(*out)
         for t, name, n in zip(out, KVStep._fields, (R + 1, T, T, R, R, 2)):
             _need(t, name, i32, (n,))
+        if not isinstance(out, KVStep):
+            out = KVStep(*out)
     B.ht_kv_plan(q_len, kv_len, owned, table, free_pages, n_free, T, *out, stream=stream)
     return out
 
@@ -331,8 +339,9 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tenso
     if dt not in (torch.float32, torch.bfloat16):
         raise ValueError(f"out_dtype: expected fp32 or bf16, got {dt}")
     if out is None:
-        yq = torch.empty(q.shape, dtype=dt, device=q.device)
-        yk = torch.empty(k.shape, dtype=dt, device=q.device) if k is not None else None
+        # dense, whatever the strides of q and k
+        yq = torch.empty_like(q, dtype=dt, memory_format=torch.contiguous_format)
+        yk = torch.empty_like(k, dtype=dt, memory_format=torch.contiguous_format) if k is not None else None
     else:
         yq = _out_rows(out[0], "out[0]", q.shape, dt)
         yk = _out_rows(out[1], "out[1]", k.shape, dt) if k is not None else None
@@ -352,9 +361,8 @@ def qk_norm_rope_backward(dq: torch.Tensor, dk: torch.Tensor | None, q: torch.Te
     if dq.shape != q.shape or (k is not None and (dk.shape != k.shape or dk.dtype != dq.dtype)):
         raise ValueError("dq, dk: expected the shapes of q and k, one type")
     if out is None:
-        xq, xk = torch.empty(q.shape, dtype=q.dtype, device=q.device), None
-        if k is not None:
-            xk = torch.empty(k.shape, dtype=k.dtype, device=q.device)
+        xq = torch.empty_like(q, memory_format=torch.contiguous_format)
+        xk = torch.empty_like(k, memory_format=torch.contiguous_format) if k is not None else None
     else:
         xq = _out_rows(out[0], "out[0]", q.shape, q.dtype)
         xk = _out_rows(out[1], "out[1]", k.shape, k.dtype) if k is not None else None
@@ -363,7 +371,7 @@ def qk_norm_rope_backward(dq: torch.Tensor, dk: torch.Tensor | None, q: torch.Te
         dwq, dwk = torch.empty_like(q_weight), torch.empty_like(k_weight)
         if ws is None:
             n_k = k.shape[1] if k is not None else 0
-            ws = workspace(B.ht_qk_norm_rope_workspace(q.shape[0], q.shape[1], n_k, q.shape[2], True), q.device)
+            ws = _scratch(B.ht_qk_norm_rope_workspace(q.shape[0], q.shape[1], n_k, q.shape[2], True), q.device)
     B.ht_qk_norm_rope_backward(dq, dk, q, k, positions, inv_freq, q_weight, k_weight, eps, interleaved, xq, xk, dwq,
                                dwk, ws=ws, stream=stream)
     return xq, xk, dwq, dwk
@@ -404,9 +412,12 @@ def kv_attention(q: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, tab
     _need(kv_len, "kv_len", torch.int32, (R,))
     if max_kv is None:
         max_kv = table.shape[1] * B.HT_KV_PAGE
-    out = torch.empty(q.shape, dtype=q.dtype, device=q.device) if out is None else _out_rows(out, "out", q.shape, q.dtype)
+    if out is None:
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
+    else:
+        _out_rows(out, "out", q.shape, q.dtype)
     if ws is None:
-        ws = workspace(B.ht_kv_attention_workspace(desc, T, R, n_q, max_q, max_kv), q.device)
+        ws = _scratch(B.ht_kv_attention_workspace(desc, T, R, n_q, max_q, max_kv), q.device)
     B.ht_kv_attention(q, desc, table, cu_q, kv_len, max_q, max_kv, 1.0 / math.sqrt(D) if scale is None else scale,
                       causal, window, out, ws=ws, stream=stream)
     return out

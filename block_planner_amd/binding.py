@@ -169,7 +169,8 @@ def _ptr(t) -> int | None:
 def _stream(stream) -> int | None:
     if stream is None:
         import torch
-        return torch.cuda.current_stream().cuda_stream
+        # the handle of torch.cuda.current_stream(), without building its Python object (2 us a call)
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -348,7 +349,11 @@ def ht_mlp_forward(descs, x, y, act_dump=None, path: int = HT_PATH_AUTO, ws=None
 def _act(t) -> int:
     """HT_FP32 or HT_BF16 of a tensor."""
     import torch
-    return HT_BF16 if t.dtype == torch.bfloat16 else HT_FP32
+    if t.dtype is torch.bfloat16:
+        return HT_BF16
+    if t.dtype is not torch.float32:
+        raise ValueError(f"expected fp32 or bf16, got {t.dtype}")
+    return HT_FP32
 
 
 def _ld(t) -> int:
@@ -365,26 +370,35 @@ def ht_kv_cache_bytes(n_pages: int, n_heads: int, head_dim: int) -> tuple:
 
 def ht_kv_plan(q_len, kv_len, owned, table, free_pages, n_free, T: int, cu_q, slots, positions, kv_out, owned_out,
                status, stream=None) -> None:
+    R, P = table.shape
     _check("ht_kv_plan", load().ht_kv_plan(
-        _ptr(q_len), _ptr(kv_len), _ptr(owned), q_len.shape[0], _ptr(table), table.shape[1], _ld(table),
-        _ptr(free_pages), free_pages.shape[0], _ptr(n_free), T, _ptr(cu_q), _ptr(slots), _ptr(positions),
-        _ptr(kv_out), _ptr(owned_out), _ptr(status), _stream(stream)))
+        q_len.data_ptr(), kv_len.data_ptr(), owned.data_ptr(), R, table.data_ptr(), P, _ld(table),
+        free_pages.data_ptr(), free_pages.shape[0], n_free.data_ptr(), T, cu_q.data_ptr(), slots.data_ptr(),
+        positions.data_ptr(), kv_out.data_ptr(), owned_out.data_ptr(), status.data_ptr(), _stream(stream)))
 
 
 def ht_kv_release(which, kv_len, owned, table, free_pages, n_free, stream=None) -> None:
+    R, P = table.shape
     _check("ht_kv_release", load().ht_kv_release(
-        _ptr(which), which.shape[0], _ptr(kv_len), _ptr(owned), _ptr(table), table.shape[1], _ld(table),
-        _ptr(free_pages), free_pages.shape[0], _ptr(n_free), _stream(stream)))
+        which.data_ptr(), R, kv_len.data_ptr(), owned.data_ptr(), table.data_ptr(), P, _ld(table),
+        free_pages.data_ptr(), free_pages.shape[0], n_free.data_ptr(), _stream(stream)))
+
+
+def _heads(t) -> tuple:
+    """(pointer, row stride, head stride) of [T, heads, D], zeros for None."""
+    if t is None:
+        return 0, 0, 0
+    st = t.stride()
+    return t.data_ptr(), st[0], st[1]
 
 
 def ht_qk_norm_rope(q, k, positions, inv_freq, wq, wk, eps: float, interleaved: bool, yq, yk, stream=None) -> None:
     """q, yq [T, n_q, D]; k, yk [T, n_k, D] or None."""
     T, n_q, D = q.shape
-    n_k, ldk, hsk, ldyk, hsyk = (k.shape[1], *k.stride()[:2], *yk.stride()[:2]) if k is not None else (0, 0, 0, 0, 0)
+    n_k = k.shape[1] if k is not None else 0
     _check("ht_qk_norm_rope", load().ht_qk_norm_rope(
-        _ptr(q), q.stride(0), q.stride(1), _ptr(k), ldk, hsk, _act(q), T, n_q, n_k, D, 2 * inv_freq.shape[0],
-        int(interleaved), _ptr(positions), _ptr(inv_freq), _ptr(wq), _ptr(wk), eps, _ptr(yq), yq.stride(0),
-        yq.stride(1), _ptr(yk), ldyk, hsyk, _act(yq), _stream(stream)))
+        *_heads(q), *_heads(k), _act(q), T, n_q, n_k, D, 2 * inv_freq.shape[0], interleaved, positions.data_ptr(),
+        inv_freq.data_ptr(), _ptr(wq), _ptr(wk), eps, *_heads(yq), *_heads(yk), _act(yq), _stream(stream)))
 
 
 def ht_qk_norm_rope_workspace(T: int, n_q: int, n_k: int, D: int, norm: bool) -> int:
@@ -396,26 +410,17 @@ def ht_qk_norm_rope_workspace(T: int, n_q: int, n_k: int, D: int, norm: bool) ->
 def ht_qk_norm_rope_backward(dq, dk, q, k, positions, inv_freq, wq, wk, eps: float, interleaved: bool, dxq, dxk,
                              dwq=None, dwk=None, ws=None, stream=None) -> None:
     T, n_q, D = dq.shape
-    n_k, lddk, hsdk, ldk, hsk, lddxk, hsdxk = \
-        (k.shape[1], *dk.stride()[:2], *k.stride()[:2], *dxk.stride()[:2]) if k is not None else (0,) * 7
+    n_k = k.shape[1] if k is not None else 0
     wsb = ws.numel() * ws.element_size() if ws is not None else 0
     _check("ht_qk_norm_rope_backward", load().ht_qk_norm_rope_backward(
-        _ptr(dq), dq.stride(0), dq.stride(1), _ptr(dk), lddk, hsdk, _act(dq), _ptr(q), q.stride(0), q.stride(1),
-        _ptr(k), ldk, hsk, _act(q), T, n_q, n_k, D, 2 * inv_freq.shape[0], int(interleaved), _ptr(positions),
-        _ptr(inv_freq), _ptr(wq), _ptr(wk), eps, _ptr(dxq), dxq.stride(0), dxq.stride(1), _ptr(dxk), lddxk, hsdxk,
+        *_heads(dq), *_heads(dk), _act(dq), *_heads(q), *_heads(k), _act(q), T, n_q, n_k, D, 2 * inv_freq.shape[0],
+        interleaved, positions.data_ptr(), inv_freq.data_ptr(), _ptr(wq), _ptr(wk), eps, *_heads(dxq), *_heads(dxk),
         _ptr(dwq), _ptr(dwk), _ptr(ws), wsb, _stream(stream)))
 
 
-def kv_cache_desc(codes, scales) -> KVCacheDesc:
-    """Descriptor of codes int8 [pages, heads, 2, 64 * D] and scales fp32 [pages, heads, 2]."""
-    return KVCacheDesc(codes.data_ptr(), scales.data_ptr(), codes.shape[0], codes.shape[1],
-                       codes.shape[3] // HT_KV_PAGE)
-
-
 def ht_kv_write(k, v, slots, desc: KVCacheDesc, stream=None) -> None:
-    _check("ht_kv_write", load().ht_kv_write(_ptr(k), k.stride(0), k.stride(1), _act(k), _ptr(v), v.stride(0),
-                                             v.stride(1), _act(v), k.shape[0], _ptr(slots), ctypes.byref(desc),
-                                             _stream(stream)))
+    _check("ht_kv_write", load().ht_kv_write(*_heads(k), _act(k), *_heads(v), _act(v), k.shape[0], slots.data_ptr(),
+                                             ctypes.byref(desc), _stream(stream)))
 
 
 def ht_kv_attention_workspace(desc: KVCacheDesc, T: int, R: int, n_q: int, max_q: int, max_kv: int) -> int:
@@ -427,8 +432,9 @@ def ht_kv_attention_workspace(desc: KVCacheDesc, T: int, R: int, n_q: int, max_q
 
 def ht_kv_attention(q, desc: KVCacheDesc, table, cu_q, kv_len, max_q: int, max_kv: int, scale: float, causal: bool,
                     window: int, out, ws=None, stream=None) -> None:
+    T, n_q, _ = q.shape
+    R, P = table.shape
     wsb = ws.numel() * ws.element_size() if ws is not None else 0
     _check("ht_kv_attention", load().ht_kv_attention(
-        _ptr(q), q.stride(0), q.stride(1), q.shape[0], q.shape[1], ctypes.byref(desc), _ptr(table), table.shape[1],
-        _ld(table), _ptr(cu_q), _ptr(kv_len), kv_len.shape[0], max_q, max_kv, scale, int(causal), window,
-        _ptr(out), out.stride(0), out.stride(1), _ptr(ws), wsb, _stream(stream)))
+        *_heads(q), T, n_q, ctypes.byref(desc), table.data_ptr(), P, _ld(table), cu_q.data_ptr(), kv_len.data_ptr(), R,
+        max_q, max_kv, scale, causal, window, *_heads(out), _ptr(ws), wsb, _stream(stream)))
