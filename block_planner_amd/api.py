@@ -417,7 +417,7 @@ def kv_attention(q: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, tab
     else:
         _out_rows(out, "out", q.shape, q.dtype)
     if ws is None:
-        ws = _scratch(B.ht_kv_attention_workspace(desc, T, R, n_q, max_q, max_kv), q.device)
+        ws = _scratch(B.ht_kv_attention_workspace(desc, T, R, n_q, max_q, max_kv, window), q.device)
     B.ht_kv_attention(q, desc, table, cu_q, kv_len, max_q, max_kv, 1.0 / math.sqrt(D) if scale is None else scale,
                       causal, window, out, ws=ws, stream=stream)
     return out

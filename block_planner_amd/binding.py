@@ -150,7 +150,7 @@ def load() -> ctypes.CDLL:
     lib.ht_kv_write.restype = St
     lib.ht_kv_write.argtypes = [P, I64, I64, I32, P, I64, I64, I32, I64, P, PC, P]
     lib.ht_kv_attention_workspace.restype = St
-    lib.ht_kv_attention_workspace.argtypes = [PC, I64, I64, I32, I64, I64, PSz]
+    lib.ht_kv_attention_workspace.argtypes = [PC, I64, I64, I32, I64, I64, I64, PSz]
     lib.ht_kv_attention.restype = St
     lib.ht_kv_attention.argtypes = [P, I64, I64, I64, I32, PC, P, I64, I64, P, P, I64, I64, I64, F, I32, I64, P, I64,
                                     I64, P, Sz, P]
@@ -423,10 +423,11 @@ def ht_kv_write(k, v, slots, desc: KVCacheDesc, stream=None) -> None:
                                              ctypes.byref(desc), _stream(stream)))
 
 
-def ht_kv_attention_workspace(desc: KVCacheDesc, T: int, R: int, n_q: int, max_q: int, max_kv: int) -> int:
+def ht_kv_attention_workspace(desc: KVCacheDesc, T: int, R: int, n_q: int, max_q: int, max_kv: int,
+                              window: int = 0) -> int:
     out = ctypes.c_size_t(0)
     _check("ht_kv_attention_workspace", load().ht_kv_attention_workspace(ctypes.byref(desc), T, R, n_q, max_q, max_kv,
-                                                                         ctypes.byref(out)))
+                                                                         window, ctypes.byref(out)))
     return out.value
 
 

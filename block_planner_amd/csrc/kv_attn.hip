@@ -12,6 +12,7 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 constexpr int kAttnThreads = 256;
 constexpr int kWaves = kAttnThreads / 64;
+constexpr int64_t kJoinPages = 2;
 constexpr int kMaxSplits = 64;   // one per lane of the kernel that joins them
 constexpr float kLog2e = 1.44269504088896341f;
 // The largest weight handed to V is 2^14: fp16 keeps 11 bits down to 2^-28 of it.
@@ -601,6 +602,42 @@ __global__ __launch_bounds__(kAttnThreads) void attn_join_kernel(AttnArgs a) {
     }
 }
 
+// The same for many rows: a group of D / 4 lanes per row and head, which goes
+// through the splits one after the other with a running maximum.  2300 rows of
+// 32 heads x 64 in 2 splits: 19 us where a workgroup per row and head takes 100.
+template <int DC>
+__global__ __launch_bounds__(kAttnThreads) void attn_join_rows_kernel(AttnArgs a) {
+    constexpr int D = 64 * DC, kLanes = D / 4, kGroups = kAttnThreads / kLanes;
+    const int grp = threadIdx.x / kLanes, d = threadIdx.x % kLanes;
+    const Request rq = load_request(a, int(blockIdx.x));
+    if (rq.splits <= 1 || grp >= kGroups) return;
+    const int64_t n = int64_t(rq.rows) * a.n_q, step = int64_t(a.T) * a.n_q;
+    for (int64_t i = int64_t(blockIdx.y) * kGroups + grp; i < n; i += int64_t(gridDim.y) * kGroups) {
+        const int64_t at = int64_t(rq.row0) * a.n_q + i;
+        const f32x4 *p = reinterpret_cast<const f32x4 *>(a.part + at * D) + d;
+        float m = -INFINITY, l = 0.f;
+        f32x4 v = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+        for (int s = 0; s < rq.splits; ++s) {
+            const float e = a.lse[at + s * step];
+            const f32x4 x = p[s * step * (D / 4)];
+            if (e == -INFINITY) continue;   // an empty split
+            const float top = fmaxf(m, e), old = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m - top);
+            const float w = __builtin_amdgcn_exp2f(e - top);   // NaN for a NaN row
+            v = v * old + x * w;
+            l = l * old + w;
+            m = top;
+        }
+        const float inv = l == 0.f ? 0.f : 1.0f / l;
+        v *= inv;
+        uint2 u;
+        u.x = uint32_t(f32_to_bf16_rne(v.x)) | (uint32_t(f32_to_bf16_rne(v.y)) << 16);
+        u.y = uint32_t(f32_to_bf16_rne(v.z)) | (uint32_t(f32_to_bf16_rne(v.w)) << 16);
+        const int64_t t = rq.row0 + i / a.n_q, h = i % a.n_q;
+        *reinterpret_cast<uint2 *>(a.out + t * a.ldo + h * a.hso + 4 * d) = u;
+    }
+}
+
 struct AttnShape {
     int32_t splits, split_pages, psplits, psplit_pages;
     bool decode, prompt;   // kernels to run; one that runs alone takes every request
@@ -622,17 +659,34 @@ void split_pages_of(int64_t pages, int64_t items, int64_t want, int64_t least, i
     }
 }
 
-AttnShape attn_shape(int64_t T, int64_t R, int32_t n_heads, int32_t D, int32_t n_q, int64_t max_q, int64_t max_kv) {
-    const int64_t pages = (max_kv + kPage - 1) / kPage, group = n_q / n_heads;
+AttnShape attn_shape(int64_t T, int64_t R, int32_t n_heads, int32_t D, int32_t n_q, int64_t max_q, int64_t max_kv,
+                     int64_t window) {
+    // pages a request's rows look at: a window's rows and the pages it cuts at both ends
+    int64_t pages = (max_kv + kPage - 1) / kPage;
+    if (window > 0 && (window + max_q) / kPage + 2 < pages) pages = (window + max_q) / kPage + 2;
+    const int64_t group = n_q / n_heads;
     AttnShape s{};
     s.prompt = max_q * group > kDecodeCols;
     s.decode = !s.prompt || R > 1;
     const int64_t tiles = s.prompt ? (kDecodeCols + 15) / 16 : max_q > 0 ? (max_q * group + 15) / 16 : 1;
     split_pages_of(pages, R * n_heads * tiles, 2048, 4, s.splits, s.split_pages);
-    // a prompt's partial results cost as much as its output sixteen times over: split only what leaves the card empty
-    s.waves = D <= 128 ? 8 : 4;
+    // 8 wavefronts share a page's conversion, 4 fill the card with fewer rows
+    // and run two workgroups per compute unit out of step.  D = 128: 566 us
+    // against 587 at 8192 rows; D = 64: 132 against 86 us a round of workgroups.
+    s.waves = D == 128 && (T * group + 255) / 256 * n_heads >= 1024 ? 8 : 4;
     const int64_t cols = 32 * s.waves, ptiles = (T * group + cols - 1) / cols + (R - 1);
-    split_pages_of(pages, ptiles * n_heads, 512, 8, s.psplits, s.psplit_pages);
+    // Splits of prompts: only into places for workgroups (two of 4 wavefronts or
+    // one of 8 on each of 256 compute units) that would stay empty, by the pages
+    // of each and kJoinPages a split for writing and joining its partial results.
+    // Splitting more than fills the card loses: 596 workgroups' worth of rows and
+    // heads with a window of 4096 took 130 us whole, 142 in 3 splits.
+    const int64_t items = ptiles * n_heads, slots = s.waves == 8 ? 256 : 512;
+    int64_t best = pages, want = 1;
+    for (int64_t n = 2; n <= kMaxSplits && n * items <= slots && n * 2 <= pages; ++n) {
+        const int64_t cost = (pages + n - 1) / n + kJoinPages * n;
+        if (cost < best) { best = cost; want = n; }
+    }
+    split_pages_of(pages, 1, want, 1, s.psplits, s.psplit_pages);
     if (!s.prompt) s.psplits = 1;
     if (!s.decode) s.splits = 1;
     return s;
@@ -660,7 +714,7 @@ ht_status run_attn(const AttnArgs &a, const AttnShape &sh, int64_t R, int64_t ma
     if (sh.prompt) {
         const int64_t cols = 32 * sh.waves, tiles = (max_q * a.group + cols - 1) / cols;
         const dim3 grid(x, uint32_t(sh.psplits), uint32_t(tiles > 8192 ? 8192 : tiles));
-        if constexpr (DC <= 2) {
+        if constexpr (DC == 2) {
             if (sh.waves == 8) attn_prompt_kernel<DC, 8><<<grid, 512, 0, s>>>(a);
         }
         if (sh.waves == 4) attn_prompt_kernel<DC, 4><<<grid, 256, 0, s>>>(a);
@@ -672,8 +726,13 @@ ht_status run_attn(const AttnArgs &a, const AttnShape &sh, int64_t R, int64_t ma
         HT_LAUNCH_CHECK();
     }
     if (sh.splits > 1 || sh.psplits > 1) {
-        const int64_t y = (sh.psplits > 1 || !sh.prompt ? max_q : kDecodeCols / a.group) * a.n_q;
-        attn_join_kernel<DC><<<dim3(uint32_t(R), uint32_t(y < 1 ? 1 : y > 4096 ? 4096 : y)), kAttnThreads, 0, s>>>(a);
+        const int64_t rows = (sh.psplits > 1 || !sh.prompt ? max_q : kDecodeCols / a.group) * a.n_q;
+        if (R * rows >= 4096) {   // more rows than the card takes workgroups at once
+            const int64_t per = kAttnThreads / (16 * DC), y = (rows + per - 1) / per;
+            attn_join_rows_kernel<DC><<<dim3(uint32_t(R), uint32_t(y < 4096 ? y : 4096)), kAttnThreads, 0, s>>>(a);
+        } else {
+            attn_join_kernel<DC><<<dim3(uint32_t(R), uint32_t(rows < 1 ? 1 : rows)), kAttnThreads, 0, s>>>(a);
+        }
         HT_LAUNCH_CHECK();
     }
     return HT_OK;
@@ -688,11 +747,12 @@ size_t partial_rows(const AttnShape &sh, int64_t T, int32_t n_q) {
 }  // namespace
 
 extern "C" ht_status ht_kv_attention_workspace(const ht_kv_cache *cache, int64_t T, int64_t R, int32_t n_q,
-                                               int64_t max_q, int64_t max_kv, size_t *bytes) {
+                                               int64_t max_q, int64_t max_kv, int64_t window, size_t *bytes) {
     if (!bytes) return HT_EINVAL;
     const ht_status st = check_attn(cache, T, R, n_q, max_q, max_kv);
     if (st != HT_OK) return st;
-    const AttnShape sh = attn_shape(T, R, cache->n_heads, cache->head_dim, n_q, max_q, max_kv);
+    if (window < 0) return HT_ESHAPE;
+    const AttnShape sh = attn_shape(T, R, cache->n_heads, cache->head_dim, n_q, max_q, max_kv, window);
     const size_t rows = partial_rows(sh, T, n_q);
     *bytes = size_t(align256(rows * 4u)) + rows * size_t(cache->head_dim) * 4u;
     return HT_OK;
@@ -713,9 +773,9 @@ extern "C" ht_status ht_kv_attention(const uint16_t *q, int64_t ldq, int64_t hsq
     if (!table || !cu_q || !kv_len) return HT_EINVAL;
     if (!al4(table) || !al4(cu_q) || !al4(kv_len) || !al16p(ws)) return HT_EALIGN;
     size_t need = 0;
-    if ((st = ht_kv_attention_workspace(cache, T, R, n_q, max_q, max_kv, &need)) != HT_OK) return st;
+    if ((st = ht_kv_attention_workspace(cache, T, R, n_q, max_q, max_kv, window, &need)) != HT_OK) return st;
     if (need > 0 && (!ws || ws_bytes < need)) return HT_ESMALL;
-    const AttnShape sh = attn_shape(T, R, cache->n_heads, cache->head_dim, n_q, max_q, max_kv);
+    const AttnShape sh = attn_shape(T, R, cache->n_heads, cache->head_dim, n_q, max_q, max_kv, window);
     AttnArgs a{};
     a.q = q;
     a.codes = cache->codes;

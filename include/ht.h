@@ -580,7 +580,7 @@ ht_status ht_kv_write(const void *k, int64_t ldk, int64_t hsk, int32_t kt, const
  * holding Inf or NaN gives NaN.  Bitwise reproducible.
  *   ws        ht_kv_attention_workspace bytes: partial results of split rows. */
 ht_status ht_kv_attention_workspace(const ht_kv_cache *cache, int64_t T, int64_t R, int32_t n_q, int64_t max_q,
-                                    int64_t max_kv, size_t *bytes);
+                                    int64_t max_kv, int64_t window, size_t *bytes);
 ht_status ht_kv_attention(const uint16_t *q, int64_t ldq, int64_t hsq, int64_t T, int32_t n_q,
                           const ht_kv_cache *cache, const int32_t *table, int64_t P, int64_t ldt, const int32_t *cu_q,
                           const int32_t *kv_len, int64_t R, int64_t max_q, int64_t max_kv, float scale, int32_t causal,
