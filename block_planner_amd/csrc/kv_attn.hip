@@ -12,7 +12,7 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 constexpr int kAttnThreads = 256;
 constexpr int kWaves = kAttnThreads / 64;
-constexpr int64_t kJoinPages = 2;
+constexpr int64_t kJoinPages = 2, kWholePages = 24;
 constexpr int kMaxSplits = 64;   // one per lane of the kernel that joins them
 constexpr float kLog2e = 1.44269504088896341f;
 // The largest weight handed to V is 2^14: fp16 keeps 11 bits down to 2^-28 of it.
@@ -82,6 +82,12 @@ __device__ __forceinline__ f16x8 codes_to_f16(uint32_t w0, uint32_t w1) {
     return r.v;
 }
 
+template <bool ONCE>
+__device__ __forceinline__ i32x4 load_codes(const int8_t *p) {
+    if constexpr (ONCE) return __builtin_nontemporal_load(reinterpret_cast<const i32x4 *>(p));
+    else return *reinterpret_cast<const i32x4 *>(p);
+}
+
 // Larger of lane i's and lane i + 32's (i - 32's) value.
 __device__ __forceinline__ float max_halves(float v) {
     const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
@@ -108,7 +114,12 @@ __device__ __forceinline__ void encode16(const uint16_t *x, float f, i32x4 &hi, 
 // Columns (row of the request, head of the group) in tiles of 16; a
 // workgroup's four wavefronts take the pages of its split in turn, each with
 // a running maximum and sum of its own, joined through LDS at the end.
-template <int DC>
+//
+// ONCE: every code is read by one workgroup (one tile of columns), so the loads
+// are hinted not to stay in the caches: 64 ragged requests of 32 x 128 heads 64
+// -> 57 us, 3 x 120k tokens 137 -> 126; with a second tile, which finds the
+// codes in the L2 without the hint, 16 x 7 rows over 3000 tokens 59 -> 65.
+template <int DC, bool ONCE>
 __global__ __launch_bounds__(kAttnThreads) void attn_decode_kernel(AttnArgs a) {
     constexpr int D = 64 * DC, NE = D / 16;
     __shared__ float s_o[kWaves][16][D + 4];
@@ -175,21 +186,43 @@ __global__ __launch_bounds__(kAttnThreads) void attn_decode_kernel(AttnArgs a) {
 #pragma unroll
         for (int e = 0; e < NE; ++e) o[e] = f32x4{0.f, 0.f, 0.f, 0.f};
         float m_run = -INFINITY, l_run = 0.f;
-        for (int p = p_first + wv; p < p_last; p += kWaves) {
-            const int32_t page = __builtin_amdgcn_readfirstlane(row_of_table[p]);
-            if (page < 0 || page >= a.n_pages) continue;
-            const int64_t blk = (int64_t(page) * a.n_heads + head) * 2;
-            const int8_t *kp = a.codes + blk * (kPage * D) + lane * 16, *vp = kp + kPage * D;
-            const float ks = a.scales[blk], vs = a.scales[blk + 1];
-            const int ev = exp_of_scale(vs) - 7;
-            i32x4 kf[4][DC];
+        // The wavefront's pages p_first + wv + 4 i: entry and scales of up to 64 of
+        // them by a lane each, the codes a page ahead: K of the next page is loaded
+        // when this page's scores are done, V when its values are added.
+        i32x4 kf[4][DC];
+        i32x4 vf[NE];
+        const auto codes_of = [&](int id) {   // a page that is not there reads page 0 and is masked
+            return a.codes + (int64_t(id < 0 ? 0 : id) * a.n_heads + head) * (2 * kPage * D) + lane * 16;
+        };
+        const auto load_k = [&](const int8_t *kp) {
 #pragma unroll
             for (int b = 0; b < 4; ++b)
 #pragma unroll
-                for (int j = 0; j < DC; ++j) kf[b][j] = *reinterpret_cast<const i32x4 *>(kp + (b * DC + j) * 1024);
-            u32x4 vf[NE];
+                for (int j = 0; j < DC; ++j) kf[b][j] = load_codes<ONCE>(kp + (b * DC + j) * 1024);
+        };
+        const auto load_v = [&](const int8_t *kp) {
 #pragma unroll
-            for (int e = 0; e < NE; ++e) vf[e] = *reinterpret_cast<const u32x4 *>(vp + e * 1024);
+            for (int e = 0; e < NE; ++e) vf[e] = load_codes<ONCE>(kp + kPage * D + e * 1024);
+        };
+        for (int p_at = p_first + wv; p_at < p_last; p_at += 64 * kWaves) {
+          const int mine = p_at + lane * kWaves, count = min(64, (p_last - p_at + kWaves - 1) / kWaves);
+          int32_t entry = row_of_table[min(mine, p_last - 1)];
+          if (entry < 0 || entry >= a.n_pages || mine >= p_last) entry = -1;
+          const float2 scale = *reinterpret_cast<const float2 *>(a.scales + (int64_t(max(entry, 0)) * a.n_heads + head) * 2);
+          int id = __builtin_amdgcn_readlane(entry, 0);
+          const int8_t *next = codes_of(id);
+          load_k(next);
+          load_v(next);
+          for (int at = 0; at < count; ++at) {
+            const int p = p_at + at * kWaves;
+            const bool there = id >= 0;
+            const float ks = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(scale.x), at));
+            const float vs = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(scale.y), at));
+            const int ev = exp_of_scale(vs) - 7;
+            if (at + 1 < count) {
+                id = __builtin_amdgcn_readlane(entry, at + 1);
+                next = codes_of(id);
+            }
             // scores of 16 tokens x 16 columns each, in the units of the codes
             const float f = qs * ks, ef = float(ev);
             float y[4][4];
@@ -205,14 +238,15 @@ __global__ __launch_bounds__(kAttnThreads) void attn_decode_kernel(AttnArgs a) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) y[b][i] = float(sh[i] * 256 + sl[i]) * f + ef;
             }
+            if (at + 1 < count) load_k(next);
             const int j0 = p * kPage;
-            if (j0 < lo_max || j0 + kPage > hi_min) {
+            if (!there || j0 < lo_max || j0 + kPage > hi_min) {
 #pragma unroll
                 for (int b = 0; b < 4; ++b)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const int j = j0 + b * 16 + g * 4 + i;
-                        if (j < lo || j >= hi) y[b][i] = -INFINITY;
+                        if (!there || j < lo || j >= hi) y[b][i] = -INFINITY;
                     }
             }
 #pragma unroll
@@ -238,9 +272,11 @@ __global__ __launch_bounds__(kAttnThreads) void attn_decode_kernel(AttnArgs a) {
 #pragma unroll
             for (int e = 0; e < NE; ++e) {
                 o[e] *= alpha;
-                o[e] = __builtin_amdgcn_mfma_f32_16x16x32_f16(codes_to_f16(vf[e].x, vf[e].y), pf[0], o[e], 0, 0, 0);
-                o[e] = __builtin_amdgcn_mfma_f32_16x16x32_f16(codes_to_f16(vf[e].z, vf[e].w), pf[1], o[e], 0, 0, 0);
+                o[e] = __builtin_amdgcn_mfma_f32_16x16x32_f16(codes_to_f16(uint32_t(vf[e].x), uint32_t(vf[e].y)), pf[0], o[e], 0, 0, 0);
+                o[e] = __builtin_amdgcn_mfma_f32_16x16x32_f16(codes_to_f16(uint32_t(vf[e].z), uint32_t(vf[e].w)), pf[1], o[e], 0, 0, 0);
             }
+            if (at + 1 < count) load_v(next);
+          }
         }
         // join: o[e][i] is dim 16 e + 4 g + i of column col
         l_run += __shfl_xor(l_run, 16);
@@ -644,19 +680,10 @@ struct AttnShape {
     int32_t waves;         // of the prompt kernel's workgroups
 };
 
-// Pages per split and splits, for `items` workgroups' worth of rows and heads:
-// `want` workgroups in all, at least `least` pages each.
-void split_pages_of(int64_t pages, int64_t items, int64_t want, int64_t least, int32_t &splits, int32_t &per_split) {
-    splits = 1;
-    per_split = int32_t(pages > 0 ? pages : 1);
-    const int64_t n = (want + items - 1) / items;
-    int64_t per = (pages + n - 1) / n;
-    if (per < least) per = least;
+void set_splits(int64_t pages, int64_t per, int32_t &splits, int32_t &per_split) {
     if (per * kMaxSplits < pages) per = (pages + kMaxSplits - 1) / kMaxSplits;
-    if (per < pages) {
-        splits = int32_t((pages + per - 1) / per);
-        per_split = int32_t(per);
-    }
+    splits = per < pages ? int32_t((pages + per - 1) / per) : 1;
+    per_split = int32_t(per > 0 ? per : 1);
 }
 
 AttnShape attn_shape(int64_t T, int64_t R, int32_t n_heads, int32_t D, int32_t n_q, int64_t max_q, int64_t max_kv,
@@ -669,7 +696,16 @@ AttnShape attn_shape(int64_t T, int64_t R, int32_t n_heads, int32_t D, int32_t n
     s.prompt = max_q * group > kDecodeCols;
     s.decode = !s.prompt || R > 1;
     const int64_t tiles = s.prompt ? (kDecodeCols + 15) / 16 : max_q > 0 ? (max_q * group + 15) / 16 : 1;
-    split_pages_of(pages, R * n_heads * tiles, 2048, 4, s.splits, s.split_pages);
+    // Splits of the decode kernel: none up to kWholePages pages (a second launch
+    // costs more than its four wavefronts' six pages each), else about 4096
+    // workgroups of 16 pages at least -- four per wavefront, which pay for the
+    // query's encoding before and the wavefronts' joining after (32 x 4000
+    // tokens of 2 heads x 256: 32 us, with four pages 53) -- or of down to four
+    // where that leaves compute units empty.
+    const int64_t ditems = R * n_heads * tiles, fill = pages * ditems / 256, least = fill < 4 ? 4 : fill < 16 ? fill : 16;
+    int64_t per = (pages * ditems + 4095) / 4096;
+    if (per < least) per = least;
+    set_splits(pages, pages <= kWholePages ? pages : per, s.splits, s.split_pages);
     // 8 wavefronts share a page's conversion, 4 fill the card with fewer rows
     // and run two workgroups per compute unit out of step.  D = 128: 566 us
     // against 587 at 8192 rows; D = 64: 132 against 86 us a round of workgroups.
@@ -686,7 +722,7 @@ AttnShape attn_shape(int64_t T, int64_t R, int32_t n_heads, int32_t D, int32_t n
         const int64_t cost = (pages + n - 1) / n + kJoinPages * n;
         if (cost < best) { best = cost; want = n; }
     }
-    split_pages_of(pages, 1, want, 1, s.psplits, s.psplit_pages);
+    set_splits(pages, (pages + want - 1) / want, s.psplits, s.psplit_pages);
     if (!s.prompt) s.psplits = 1;
     if (!s.decode) s.splits = 1;
     return s;
@@ -722,7 +758,9 @@ ht_status run_attn(const AttnArgs &a, const AttnShape &sh, int64_t R, int64_t ma
     }
     if (sh.decode) {
         const int64_t cols = sh.prompt ? kDecodeCols : max_q * a.group, tiles = cols > 16 ? (cols + 15) / 16 : 1;
-        attn_decode_kernel<DC><<<dim3(x, uint32_t(sh.splits), uint32_t(tiles)), kAttnThreads, 0, s>>>(a);
+        const dim3 grid(x, uint32_t(sh.splits), uint32_t(tiles));
+        if (tiles == 1) attn_decode_kernel<DC, true><<<grid, kAttnThreads, 0, s>>>(a);
+        else attn_decode_kernel<DC, false><<<grid, kAttnThreads, 0, s>>>(a);
         HT_LAUNCH_CHECK();
     }
     if (sh.splits > 1 || sh.psplits > 1) {

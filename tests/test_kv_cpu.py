@@ -127,7 +127,7 @@ def test_write_argument_checks(change, code):
     assert call("ht_kv_write", {**WRITE, "cache": cache()}, **change) == code
 
 
-ATTN = dict(q=A, ldq=1024, hsq=128, T=6, n_q=8, cache=None, table=A, P=8, ldt=8, cu=A, kv=A, R=3, max_q=2, max_kv=512,
+ATTN = dict(q=A, ldq=1024, hsq=128, T=6, n_q=8, cache=None, table=A, P=2000, ldt=2000, cu=A, kv=A, R=3, max_q=2, max_kv=100000,
             scale=0.1, causal=1, window=0, out=A, ldo=1024, hso=128, ws=A, ws_bytes=1 << 30, stream=None)
 
 
