@@ -1,5 +1,6 @@
 """PyTorch modules over the C ABI: HyperLinear, scan_model,
-wrap_model_with_hypertensor and save/load of packed models.
+wrap_model_with_hypertensor and save/load of packed models; HyperAttention
+over a paged 8-bit cache (KVPool); qk_norm_rope with its gradient.
 
 Follows the user calls of the HyperTensor 1.0.1 page ("Usage Example":
 HyperLinear layers with ReLU; "Convert model": scan_model, then
@@ -26,6 +27,10 @@ Scope, as built:
   * refresh_every > 0 with a master weight re-plans and re-packs every that
     many forward calls (the page's refresh cadence) with the fused single
     pass ht_refresh, into buffers allocated once.
+  * HyperAttention ("Key Features" names it and fixes nothing): the q|k|v
+    linear, per-head norm and rotation, the cache write and the attention, the
+    output linear, for serving (no backward pass through the cache).
+    qk_norm_rope is differentiable and serves training too.
 """
 from __future__ import annotations
 
@@ -187,6 +192,136 @@ class HyperLinear(torch.nn.Module):
             tot = sum(self.packed.counts) or 1
             mix = ", mix=" + "/".join(f"{c / tot:.3f}" for c in self.packed.counts)
         return f"in_features={self.in_features}, out_features={self.out_features}{mix}"
+
+
+# -----------------------------------------------------------------------------
+# Attention
+# -----------------------------------------------------------------------------
+class _QKNormRopeFn(torch.autograd.Function):
+    """api.qk_norm_rope with ht_qk_norm_rope_backward."""
+
+    @staticmethod
+    def forward(ctx, q, k, q_weight, k_weight, positions, inv_freq, eps, interleaved, out_dtype):
+        ctx.norm = q_weight is not None
+        ctx.args = (float(eps), bool(interleaved))
+        ctx.meta = (q.dtype, q.shape, None if k is None else k.shape)
+        # without the norm the gradient is the rotation back: the inputs are not needed
+        ctx.save_for_backward(positions, inv_freq, *((q, k, q_weight, k_weight) if ctx.norm else ()))
+        return api.qk_norm_rope(q, k, positions, inv_freq, q_weight, k_weight, eps, interleaved, out_dtype)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dyq, dyk):
+        positions, inv_freq, *saved = ctx.saved_tensors
+        dt, sq, sk = ctx.meta
+        eps, interleaved = ctx.args
+        if ctx.norm:
+            q, k, wq, wk = saved
+        else:
+            q = torch.empty(sq, dtype=dt, device=dyq.device)
+            k, wq, wk = None if sk is None else torch.empty(sk, dtype=dt, device=dyq.device), None, None
+        dq, dk, dwq, dwk = api.qk_norm_rope_backward(dyq, dyk if k is not None else None, q, k, positions, inv_freq, wq,
+                                                     wk, eps, interleaved)
+        return dq, dk, dwq, dwk, None, None, None, None, None
+
+
+def qk_norm_rope(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tensor, inv_freq: torch.Tensor,
+                 q_weight: torch.Tensor | None = None, k_weight: torch.Tensor | None = None, eps: float = 1e-6,
+                 interleaved: bool = False, out_dtype=None) -> tuple:
+    """Differentiable api.qk_norm_rope: gradients for q, k and the weights
+    (not for positions and frequencies)."""
+    return _QKNormRopeFn.apply(q, k, q_weight, k_weight, positions, inv_freq, eps, interleaved, out_dtype)
+
+
+class KVPool:
+    """A paged cache for every layer of a model and the state that places
+    requests in it: one page table, lengths and a free list for all layers.
+
+        pool = KVPool(layers, n_pages, n_kv_heads, head_dim, max_requests, max_pages, device)
+        step = pool.plan([17, 1, 0, 1])          # new rows of each request
+        ... HyperAttention(...)(x, pool, layer, step) for each layer ...
+        pool.release([False, False, True, False])
+
+    plan() advances the lengths; nothing is read back to the host.  A request
+    that finds no pages keeps its length and stores none of its new rows
+    (step.status[1] counts those): release others and plan its rows again."""
+
+    def __init__(self, layers: int, n_pages: int, n_kv_heads: int, head_dim: int, max_requests: int, max_pages: int,
+                 device):
+        self.caches = [api.kv_cache(n_pages, n_kv_heads, head_dim, device) for _ in range(layers)]
+        z = lambda *n: torch.zeros(*n, dtype=torch.int32, device=device)  # noqa: E731
+        self.device, self.max_requests = torch.device(device), int(max_requests)
+        self.table = torch.full((max_requests, max_pages), -1, dtype=torch.int32, device=device)
+        self.kv_len, self.owned = z(max_requests), z(max_requests)
+        self.free_pages = torch.arange(n_pages, dtype=torch.int32, device=device)
+        self.n_free = torch.full((1,), n_pages, dtype=torch.int32, device=device)
+        self.max_q = self.max_kv = 0     # of the last plan; max_kv: the table's width until told better
+
+    def plan(self, q_len, T: int | None = None, max_q: int | None = None, max_kv: int | None = None) -> api.KVStep:
+        """q_len: new rows of each request, a list (or an int32 tensor on the
+        device with T and max_q given).  max_kv: the longest request after the
+        step as far as the caller knows (default: what the table holds)."""
+        if not isinstance(q_len, torch.Tensor):
+            if len(q_len) != self.max_requests:
+                raise ValueError(f"q_len: expected {self.max_requests} lengths, got {len(q_len)}")
+            T, max_q = sum(q_len), max(q_len)
+            q_len = torch.tensor(q_len, dtype=torch.int32).to(self.device)
+        elif T is None or max_q is None:
+            raise ValueError("q_len on the device: T and max_q are needed")
+        step = api.kv_plan(q_len, self.kv_len, self.owned, self.table, self.free_pages, self.n_free, T)
+        self.kv_len, self.owned, self.n_free = step.kv_len, step.owned, step.status[:1]
+        self.max_q, self.max_kv = int(max_q), max_kv
+        return step
+
+    def release(self, which) -> None:
+        """Give back the pages of the requests with which[r]."""
+        if not isinstance(which, torch.Tensor):
+            which = torch.tensor(which, dtype=torch.bool).to(self.device)
+        self.kv_len, self.owned, self.n_free = self.kv_len.clone(), self.owned.clone(), self.n_free.clone()
+        api.kv_release(which, self.kv_len, self.owned, self.table, self.free_pages, self.n_free)
+
+
+class HyperAttention(torch.nn.Module):
+    """Attention of one layer for serving: x [T, hidden] -> fp32 [T, hidden]
+    over a KVPool's cache.
+
+    qkv and out are HyperLinear (or any linear giving fp32 or bf16): qkv maps
+    hidden to (n_heads + 2 n_kv_heads) * head_dim, out maps n_heads * head_dim
+    back.  With qk_norm each head of q and k is normed with a weight; base (or
+    inv_freq, fp64) sets the rotation; window > 0 limits every row to its last
+    `window` tokens."""
+
+    def __init__(self, qkv: torch.nn.Module, out: torch.nn.Module, n_heads: int, n_kv_heads: int, head_dim: int,
+                 base: float = 10000.0, inv_freq: torch.Tensor | None = None, qk_norm: bool = False, eps: float = 1e-6,
+                 interleaved: bool = False, window: int = 0, device=None):
+        super().__init__()
+        if n_heads % n_kv_heads:
+            raise ValueError("n_heads must be a multiple of n_kv_heads")
+        dev = torch.device(device) if device is not None else torch.device("cuda", torch.cuda.current_device())
+        self.qkv, self.out = qkv, out
+        self.n_heads, self.n_kv_heads, self.head_dim = int(n_heads), int(n_kv_heads), int(head_dim)
+        self.eps, self.interleaved, self.window = float(eps), bool(interleaved), int(window)
+        self.register_buffer("inv_freq", api.rope_inv_freq(head_dim, base, dev) if inv_freq is None else inv_freq)
+        one = lambda: torch.nn.Parameter(torch.ones(head_dim, device=dev)) if qk_norm else None  # noqa: E731
+        self.q_weight, self.k_weight = one(), one()
+
+    @torch.no_grad()
+    def forward(self, x: torch.Tensor, pool: KVPool, layer: int, step: api.KVStep) -> torch.Tensor:
+        y = self.qkv(x)
+        n, m, d = self.n_heads, self.n_kv_heads, self.head_dim
+        if y.dim() != 2 or y.shape[1] != (n + 2 * m) * d:
+            raise ValueError(f"qkv: expected [rows, {(n + 2 * m) * d}], got {tuple(y.shape)}")
+        y = y.unflatten(1, (n + 2 * m, d))
+        codes, scales = pool.caches[layer]
+        q, k = api.qk_norm_rope(y[:, :n], y[:, n:n + m], step.positions, self.inv_freq, self.q_weight, self.k_weight,
+                                self.eps, self.interleaved, out_dtype=torch.bfloat16)
+        api.kv_write(k, y[:, n + m:], step.slots, codes, scales)
+        o = api.kv_attention(q, codes, scales, pool.table, step.cu_q, step.kv_len, pool.max_q, max_kv=pool.max_kv,
+                             window=self.window)
+        return self.out(o.flatten(1))
+
+    def extra_repr(self) -> str:
+        return f"heads={self.n_heads}, kv_heads={self.n_kv_heads}, head_dim={self.head_dim}, window={self.window}"
 
 
 # -----------------------------------------------------------------------------
