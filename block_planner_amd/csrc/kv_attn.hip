@@ -15,8 +15,11 @@ constexpr int kWaves = kAttnThreads / 64;
 constexpr int64_t kJoinPages = 2, kWholePages = 24;
 constexpr int kMaxSplits = 64;   // one per lane of the kernel that joins them
 constexpr float kLog2e = 1.44269504088896341f;
-// The largest weight handed to V is 2^14: fp16 keeps 11 bits down to 2^-28 of it.
-constexpr float kTopLog2 = 14.f;
+// The weight of the running maximum, as handed to V: fp16 keeps 11 bits down to
+// 2^-26 of it and has 2^-36 as its last bit.  The prompt kernel moves its
+// maximum (and rescales its sums) only for a score kSlackLog2 above it: weights
+// stay under 2^15.5, below fp16's 65504.
+constexpr float kTopLog2 = 12.f, kSlackLog2 = 3.5f;
 
 struct AttnArgs {
     const uint16_t *q;
@@ -489,7 +492,7 @@ __global__ __launch_bounds__(64 * NW, DC <= 2 ? 2 : 1) void attn_prompt_kernel(A
 #pragma unroll
                 for (int i = 0; i < 16; ++i) top = fmaxf(top, s[b][i]);
             const float m_new = fmaxf(m_run, max_halves(top * f + ef));
-            if (__any(m_new > m_run)) {
+            if (__any(m_new > m_run + kSlackLog2)) {
                 const float alpha = m_run == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m_run - m_new);
                 l_run *= alpha;
 #pragma unroll
