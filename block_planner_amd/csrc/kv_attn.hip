@@ -402,6 +402,7 @@ __global__ __launch_bounds__(64 * NW, DC <= 2 ? 2 : 1) void attn_prompt_kernel(A
         };
         // a page that is not there reads page 0 and is masked
         const auto block_of = [&](int id) { return (int64_t(id < 0 ? 0 : id) * a.n_heads + head) * 2; };
+        const auto scales_of = [&](int id) { return *reinterpret_cast<const float2 *>(a.scales + block_of(id)); };
         const auto load_k = [&](int id) {
             const int8_t *kp = a.codes + block_of(id) * (kPage * D);
 #pragma unroll
@@ -459,19 +460,14 @@ __global__ __launch_bounds__(64 * NW, DC <= 2 ? 2 : 1) void attn_prompt_kernel(A
 #pragma unroll
             for (int i = 0; i < 16; ++i) o[d][i] = 0.f;
         float m_run = -INFINITY, l_run = 0.f;
-        int id0 = -1, id1 = -1;             // pages p, p + 1
-        int32_t e2 = -1;                    // table entry of p + 2
-        float2 sc = {0.f, 0.f};             // scales of page p
+        int id0 = -1, id1 = -1, id2 = -1;   // pages p, p + 1, p + 2
+        int32_t e3 = -1;                    // table entry of p + 3
+        float2 sc = {0.f, 0.f}, sc1 = sc;   // scales of pages p, p + 1
         f32x16 s0[2], s1[2];
         // One page: its scores are in s; the next page's go to n while these
         // are turned into weights.  K is one page ahead of V in LDS.
         const auto page_step = [&](int p, f32x16 *s, f32x16 *n, int cur) {
             __syncthreads();   // K of p + 1 and V of p are in LDS; K of p and V of p - 1 have been read
-            const int id2 = id_of(e2, p + 2);
-            e2 = entry(p + 3);
-            load_k(id2);
-            load_v(id1);
-            const float2 sc_next = *reinterpret_cast<const float2 *>(a.scales + block_of(id1));
             const int ev = exp_of_scale(sc.y) - 7;
             // above 0 (or NaN), so that a masked score, -inf, stays one
             const float f = qs * sc.x == 0.f ? 0x1p-120f : qs * sc.x, ef = float(ev);
@@ -540,16 +536,24 @@ __global__ __launch_bounds__(64 * NW, DC <= 2 ? 2 : 1) void attn_prompt_kernel(A
                 if (i == 2 * DB) store_v(v_lds[cur ^ 1]);
             }
             __builtin_amdgcn_sched_barrier(0);
+            // the next step's codes, now that the registers are free
             id0 = id1;
             id1 = id2;
-            sc = sc_next;
+            id2 = id_of(e3, p + 3);
+            e3 = entry(p + 4);
+            load_k(id2);
+            load_v(id1);
+            sc = sc1;
+            sc1 = scales_of(id1);
         };
         if (p_first < p_last) {
-            const int32_t e0 = entry(p_first), e1 = entry(p_first + 1);
-            e2 = entry(p_first + 2);
+            const int32_t e0 = entry(p_first), e1 = entry(p_first + 1), e2 = entry(p_first + 2);
+            e3 = entry(p_first + 3);
             id0 = id_of(e0, p_first);
             id1 = id_of(e1, p_first + 1);
-            sc = *reinterpret_cast<const float2 *>(a.scales + block_of(id0));
+            id2 = id_of(e2, p_first + 2);
+            sc = scales_of(id0);
+            sc1 = scales_of(id1);
             load_k(id0);
             load_v(id0);
             __syncthreads();   // the tile before has been read
@@ -557,6 +561,8 @@ __global__ __launch_bounds__(64 * NW, DC <= 2 ? 2 : 1) void attn_prompt_kernel(A
             store_v(v_lds[0]);
             load_k(id1);
             store_k(k_lds[1]);
+            load_k(id2);
+            load_v(id1);
             __syncthreads();
             scores(k_lds[0], s0);
             for (int p = p_first; p < p_last; p += 2) {
