@@ -194,6 +194,19 @@ def _need(t: torch.Tensor, name: str, dtype, shape: tuple) -> None:
         raise ValueError(f"{name}: expected a contiguous tensor")
 
 
+def _on_gpu(*tensors) -> None:
+    """The kernels get bare addresses: host memory never reaches them."""
+    for t in tensors:
+        if t is not None and not t.is_cuda:
+            raise ValueError("every tensor must be on the GPU")
+
+
+def _using(stream):
+    """Context in which a call given a stream allocates, copies and launches:
+    temporaries belong to that stream then."""
+    return torch.cuda.stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream)
+
+
 def _table(t: torch.Tensor, R: int) -> None:
     if t.dim() != 2 or t.dtype != torch.int32 or t.shape[0] != R or (t.shape[1] > 1 and t.stride(1) != 1):
         raise ValueError(f"table: expected int32 [{R}, pages] with dense rows, got {t.dtype} {tuple(t.shape)}")
@@ -275,6 +288,9 @@ def kv_plan(q_len: torch.Tensor, kv_len: torch.Tensor, owned: torch.Tensor, tabl
     place; free_pages int32 [n] with its first n_free[0] entries free; T the
     sum of q_len.  Nothing else changes: the next step takes step.kv_len,
     step.owned and step.status[:1] as kv_len, owned and n_free."""
+    if stream is not None:
+        with _using(stream):
+            return kv_plan(q_len, kv_len, owned, table, free_pages, n_free, T, out)
     i32, R = torch.int32, q_len.shape[0]
     for t, name in ((q_len, "q_len"), (kv_len, "kv_len"), (owned, "owned")):
         _need(t, name, i32, (R,))
@@ -288,7 +304,8 @@ def kv_plan(q_len: torch.Tensor, kv_len: torch.Tensor, owned: torch.Tensor, tabl
             _need(t, name, i32, (n,))
         if not isinstance(out, KVStep):
             out = KVStep(*out)
-    B.ht_kv_plan(q_len, kv_len, owned, table, free_pages, n_free, T, *out, stream=stream)
+    _on_gpu(q_len, kv_len, owned, table, free_pages, n_free, *out)
+    B.ht_kv_plan(q_len, kv_len, owned, table, free_pages, n_free, T, *out)
     return out
 
 
@@ -297,12 +314,13 @@ def kv_release(which: torch.Tensor, kv_len: torch.Tensor, owned: torch.Tensor, t
     """Give back the pages of the requests with which[r] (bool or uint8 [R]);
     kv_len, owned, free_pages and n_free change in place (ht_kv_release)."""
     R = which.shape[0]
-    if which.dtype not in (torch.bool, torch.uint8) or not which.is_contiguous():
-        raise ValueError(f"which: expected contiguous bool or uint8 [{R}], got {which.dtype}")
+    if which.dtype not in (torch.bool, torch.uint8) or which.dim() != 1 or not which.is_contiguous():
+        raise ValueError(f"which: expected contiguous bool or uint8 [requests], got {which.dtype} {tuple(which.shape)}")
     for t, name, n in ((kv_len, "kv_len", R), (owned, "owned", R), (n_free, "n_free", 1)):
         _need(t, name, torch.int32, (n,))
     _need(free_pages, "free_pages", torch.int32, (free_pages.numel(),))
     _table(table, R)
+    _on_gpu(which, kv_len, owned, table, free_pages, n_free)
     B.ht_kv_release(which, kv_len, owned, table, free_pages, n_free, stream=stream)
 
 
@@ -332,6 +350,9 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tenso
     [T, n_q, D] and k [T, n_k, D] (or None) in one pass (ht_qk_norm_rope).
     fp32 or bf16, any row and head strides; positions int32 [T]; inv_freq
     fp64 [rot / 2].  Returns (q, k) in out_dtype (q's own by default)."""
+    if stream is not None:
+        with _using(stream):
+            return qk_norm_rope(q, k, positions, inv_freq, q_weight, k_weight, eps, interleaved, out_dtype, out)
     q = _rows(q, "q")
     k = _rows(k, "k") if k is not None else None
     _rope_args(q, k, positions, inv_freq, q_weight, k_weight)
@@ -345,7 +366,8 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tenso
     else:
         yq = _out_rows(out[0], "out[0]", q.shape, dt)
         yk = _out_rows(out[1], "out[1]", k.shape, dt) if k is not None else None
-    B.ht_qk_norm_rope(q, k, positions, inv_freq, q_weight, k_weight, eps, interleaved, yq, yk, stream=stream)
+    _on_gpu(q, k, positions, inv_freq, q_weight, k_weight, yq, yk)
+    B.ht_qk_norm_rope(q, k, positions, inv_freq, q_weight, k_weight, eps, interleaved, yq, yk)
     return yq, yk
 
 
@@ -355,17 +377,22 @@ def qk_norm_rope_backward(dq: torch.Tensor, dk: torch.Tensor | None, q: torch.Te
                           out=None, ws: torch.Tensor | None = None, stream=None) -> tuple:
     """Gradients of qk_norm_rope: (dq, dk) of its inputs, in their type, and
     fp32 (dq_weight, dk_weight) (None without weights)."""
+    if stream is not None:
+        with _using(stream):
+            return qk_norm_rope_backward(dq, dk, q, k, positions, inv_freq, q_weight, k_weight, eps, interleaved, out, ws)
     q, dq = _rows(q, "q"), _rows(dq, "dq")
     k, dk = (_rows(k, "k"), _rows(dk, "dk")) if k is not None else (None, None)
     _rope_args(q, k, positions, inv_freq, q_weight, k_weight)
     if dq.shape != q.shape or (k is not None and (dk.shape != k.shape or dk.dtype != dq.dtype)):
         raise ValueError("dq, dk: expected the shapes of q and k, one type")
+    _on_gpu(dq, dk, q, k, positions, inv_freq, q_weight, k_weight, ws)
     if out is None:
         xq = torch.empty_like(q, memory_format=torch.contiguous_format)
         xk = torch.empty_like(k, memory_format=torch.contiguous_format) if k is not None else None
     else:
         xq = _out_rows(out[0], "out[0]", q.shape, q.dtype)
         xk = _out_rows(out[1], "out[1]", k.shape, k.dtype) if k is not None else None
+        _on_gpu(xq, xk)
     dwq = dwk = None
     if q_weight is not None:
         dwq, dwk = torch.empty_like(q_weight), torch.empty_like(k_weight)
@@ -373,7 +400,7 @@ def qk_norm_rope_backward(dq: torch.Tensor, dk: torch.Tensor | None, q: torch.Te
             n_k = k.shape[1] if k is not None else 0
             ws = _scratch(B.ht_qk_norm_rope_workspace(q.shape[0], q.shape[1], n_k, q.shape[2], True), q.device)
     B.ht_qk_norm_rope_backward(dq, dk, q, k, positions, inv_freq, q_weight, k_weight, eps, interleaved, xq, xk, dwq,
-                               dwk, ws=ws, stream=stream)
+                               dwk, ws=ws)
     return xq, xk, dwq, dwk
 
 
@@ -381,13 +408,17 @@ def kv_write(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, codes: torch
              stream=None) -> None:
     """Quantise keys and values [T, heads, D] (fp32 or bf16, each its own
     type) into the cache at slots int32 [T] (ht_kv_write), in place."""
+    if stream is not None:
+        with _using(stream):
+            return kv_write(k, v, slots, codes, scales)
     desc = _cache_desc(codes, scales)
     k, v = _rows(k, "k"), _rows(v, "v")
     shape = (slots.shape[0], codes.shape[1], codes.shape[3] // B.HT_KV_PAGE)
     if tuple(k.shape) != shape or tuple(v.shape) != shape:
         raise ValueError(f"k, v: expected {shape}, got {tuple(k.shape)} and {tuple(v.shape)}")
     _need(slots, "slots", torch.int32, shape[:1])
-    B.ht_kv_write(k, v, slots, desc, stream=stream)
+    _on_gpu(k, v, slots, codes, scales)
+    B.ht_kv_write(k, v, slots, desc)
 
 
 def kv_attention(q: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, table: torch.Tensor, cu_q: torch.Tensor,
@@ -399,6 +430,9 @@ def kv_attention(q: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, tab
     table can hold) are the largest lengths the caller knows of; scale is
     1 / sqrt(D) by default; window > 0 keeps each row to its last `window`
     tokens."""
+    if stream is not None:
+        with _using(stream):
+            return kv_attention(q, codes, scales, table, cu_q, kv_len, max_q, max_kv, scale, causal, window, out, ws)
     desc = _cache_desc(codes, scales)
     if q.dtype != torch.bfloat16:
         raise ValueError(f"q: expected bf16 [rows, heads, dim], got {q.dtype}")
@@ -410,14 +444,15 @@ def kv_attention(q: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, tab
     _table(table, R)
     _need(cu_q, "cu_q", torch.int32, (R + 1,))
     _need(kv_len, "kv_len", torch.int32, (R,))
+    if out is not None:
+        _out_rows(out, "out", q.shape, q.dtype)
+    _on_gpu(q, codes, scales, table, cu_q, kv_len, out, ws)
     if max_kv is None:
         max_kv = table.shape[1] * B.HT_KV_PAGE
     if out is None:
         out = torch.empty_like(q, memory_format=torch.contiguous_format)
-    else:
-        _out_rows(out, "out", q.shape, q.dtype)
     if ws is None:
         ws = _scratch(B.ht_kv_attention_workspace(desc, T, R, n_q, max_q, max_kv, window), q.device)
     B.ht_kv_attention(q, desc, table, cu_q, kv_len, max_q, max_kv, 1.0 / math.sqrt(D) if scale is None else scale,
-                      causal, window, out, ws=ws, stream=stream)
+                      causal, window, out, ws=ws)
     return out

@@ -27,8 +27,12 @@ struct AttnArgs {
     const float *scales;
     const int32_t *table, *cu_q, *kv_len;
     uint16_t *out;
-    float *part;        // [splits][T][n_q][D], normalised
-    float *lse;         // [splits][T][n_q], log2 of the weights' sum
+    // results of splits, normalised, and the log2 of their weights' sums:
+    // [splits][dec_rows][n_q] of the decode kernel's requests (rows by request,
+    // dec_per_request each, or by T where that is 0), then [psplits][T][n_q]
+    float *part, *lse;
+    int64_t dec_rows, prompt_at;
+    int32_t dec_per_request;
     int64_t ldq, hsq, ldo, hso, ldt, P;
     int32_t T, n_q, n_heads, group, n_pages, causal;
     int32_t splits, split_pages;     // of the decode kernel's requests
@@ -62,6 +66,13 @@ __device__ __forceinline__ Request load_request(const AttnArgs &a, int r) {
     q.split_pages = q.prompt ? a.psplit_pages : a.split_pages;
     q.splits = min(max((q.p1 - q.p0 + q.split_pages - 1) / q.split_pages, 1), q.prompt ? a.psplits : a.splits);
     return q;
+}
+
+// Partial result of split 0 of a request's first row, head 0, and the step to the next split.
+__device__ __forceinline__ int64_t partial_at(const AttnArgs &a, const Request &q, int r, int64_t &step) {
+    step = (q.prompt ? int64_t(a.T) : a.dec_rows) * a.n_q;
+    const int64_t row = q.prompt || a.dec_per_request == 0 ? q.row0 : int64_t(r) * a.dec_per_request;
+    return (q.prompt ? a.prompt_at : 0) + row * a.n_q;
 }
 
 // Tokens row i of a request sees: [lo, hi).
@@ -136,6 +147,8 @@ __global__ __launch_bounds__(kAttnThreads) void attn_decode_kernel(AttnArgs a) {
     const int pb = split == rq.splits - 1 ? rq.p1 : min(rq.p1, pa + rq.split_pages);
     const int n_cols = rq.rows * a.group;
     const int32_t *row_of_table = a.table + int64_t(r) * a.ldt;
+    int64_t part_step;
+    const int64_t part0 = partial_at(a, rq, r, part_step);
 
     for (int c0 = int(blockIdx.z) * 16; c0 < n_cols; c0 += int(gridDim.z) * 16) {
         const int c = c0 + col;
@@ -312,7 +325,7 @@ __global__ __launch_bounds__(kAttnThreads) void attn_decode_kernel(AttnArgs a) {
                 u.y = uint32_t(f32_to_bf16_rne(v.z)) | (uint32_t(f32_to_bf16_rne(v.w)) << 16);
                 *reinterpret_cast<uint2 *>(a.out + int64_t(tt) * a.ldo + int64_t(h) * a.hso + d) = u;
             } else {
-                const int64_t at = (int64_t(split) * a.T + tt) * a.n_q + h;
+                const int64_t at = part0 + split * part_step + int64_t((c0 + cc) / a.group) * a.n_q + h;
                 *reinterpret_cast<f32x4 *>(a.part + at * D + d) = v;
                 // kTopLog2 is in every l alike and cancels
                 if (d == 0) a.lse[at] = l == 0.f ? -INFINITY : (m == -INFINITY ? 0.f : m) + log2f(l);
@@ -346,6 +359,8 @@ __global__ __launch_bounds__(64 * NW, DC <= 2 ? 2 : 1) void attn_prompt_kernel(A
     const int pb = split == rq.splits - 1 ? rq.p1 : min(rq.p1, pa + rq.split_pages);
     const int n_cols = rq.rows * a.group, n_tiles = (n_cols + kCols - 1) / kCols;
     const int32_t *row_of_table = a.table + int64_t(r) * a.ldt;
+    int64_t part_step;
+    const int64_t part0 = partial_at(a, rq, r, part_step);
 
     // the last tiles first: under a causal mask they see the most
     for (int tile = n_tiles - 1 - int(blockIdx.z); tile >= 0; tile -= int(gridDim.z)) {
@@ -574,7 +589,7 @@ __global__ __launch_bounds__(64 * NW, DC <= 2 ? 2 : 1) void attn_prompt_kernel(A
         if (live) {
             const bool none = l == 0.f || hi <= lo;
             const float inv = 1.0f / l;
-            const int64_t at = (int64_t(split) * a.T + t) * a.n_q + hq;
+            const int64_t at = part0 + split * part_step + int64_t(qi) * a.n_q + hq;
 #pragma unroll
             for (int d = 0; d < DB; ++d)
 #pragma unroll
@@ -608,9 +623,11 @@ __global__ __launch_bounds__(kAttnThreads) void attn_join_kernel(AttnArgs a) {
     const int tid = threadIdx.x, lane = tid & 63, grp = tid / kLanes, d = tid % kLanes;
     const Request rq = load_request(a, int(blockIdx.x));
     if (rq.splits <= 1) return;
-    const int64_t n = int64_t(rq.rows) * a.n_q, step = int64_t(a.T) * a.n_q;
+    const int64_t n = int64_t(rq.rows) * a.n_q;
+    int64_t step;
+    const int64_t first = partial_at(a, rq, int(blockIdx.x), step);
     for (int64_t i = blockIdx.y; i < n; i += gridDim.y) {
-        const int64_t at = int64_t(rq.row0) * a.n_q + i;
+        const int64_t at = first + i;
         // weights of the splits (at most 64: one per lane), the same in every wavefront
         const float e = lane < rq.splits ? a.lse[at + lane * step] : -INFINITY;
         float m = e;
@@ -656,9 +673,11 @@ __global__ __launch_bounds__(kAttnThreads) void attn_join_rows_kernel(AttnArgs a
     const int grp = threadIdx.x / kLanes, d = threadIdx.x % kLanes;
     const Request rq = load_request(a, int(blockIdx.x));
     if (rq.splits <= 1 || grp >= kGroups) return;
-    const int64_t n = int64_t(rq.rows) * a.n_q, step = int64_t(a.T) * a.n_q;
+    const int64_t n = int64_t(rq.rows) * a.n_q;
+    int64_t step;
+    const int64_t first = partial_at(a, rq, int(blockIdx.x), step);
     for (int64_t i = int64_t(blockIdx.y) * kGroups + grp; i < n; i += int64_t(gridDim.y) * kGroups) {
-        const int64_t at = int64_t(rq.row0) * a.n_q + i;
+        const int64_t at = first + i;
         const f32x4 *p = reinterpret_cast<const f32x4 *>(a.part + at * D) + d;
         float m = -INFINITY, l = 0.f;
         f32x4 v = {0.f, 0.f, 0.f, 0.f};
@@ -747,8 +766,8 @@ namespace {
 ht_status check_attn(const ht_kv_cache *c, int64_t T, int64_t R, int32_t n_q, int64_t max_q, int64_t max_kv) {
     const ht_status st = check_cache(c);
     if (st != HT_OK) return st;
-    if (T < 0 || T > (int64_t(1) << 30) || R <= 0 || R > (int64_t(1) << 20) || n_q <= 0 || n_q > 4096 ||
-        n_q % c->n_heads || max_q < 0 || max_kv < 0 || max_q > (int64_t(1) << 30) || max_kv > (int64_t(1) << 30))
+    if (T < 0 || T > (int64_t(1) << 30) || R <= 0 || R * c->n_heads > (int64_t(1) << 22) || R > (int64_t(1) << 22) ||
+        n_q <= 0 || n_q > 4096 || n_q % c->n_heads || max_q < 0 || max_kv < 0 || max_q > (int64_t(1) << 30) || max_kv > (int64_t(1) << 30))
         return HT_ESHAPE;
     return HT_OK;
 }
@@ -785,10 +804,22 @@ ht_status run_attn(const AttnArgs &a, const AttnShape &sh, int64_t R, int64_t ma
     return HT_OK;
 }
 
-// Splits that partial results are kept for.
-size_t partial_rows(const AttnShape &sh, int64_t T, int32_t n_q) {
-    const int32_t n = sh.splits > sh.psplits ? sh.splits : sh.psplits;
-    return n > 1 ? size_t(n) * size_t(T) * size_t(n_q) : 0;
+// Where partial results of split rows go.  Where both kernels run, the decode
+// kernel's requests have at most kDecodeCols columns each and rows of their own
+// by request: T may be a prompt's thousands.
+struct PartialShape {
+    int64_t dec_rows, dec_total, total;   // rows per split; rows x heads x splits
+    int32_t dec_per_request;
+};
+
+PartialShape partial_shape(const AttnShape &sh, int64_t T, int64_t R, int32_t n_q, int32_t n_heads) {
+    PartialShape p{};
+    const int32_t group = n_q / n_heads;
+    p.dec_per_request = sh.prompt ? (kDecodeCols / group > 0 ? kDecodeCols / group : 1) : 0;
+    p.dec_rows = sh.prompt ? R * p.dec_per_request : T;
+    p.dec_total = sh.splits > 1 ? sh.splits * p.dec_rows * n_q : 0;
+    p.total = p.dec_total + (sh.psplits > 1 ? sh.psplits * T * n_q : 0);
+    return p;
 }
 
 }  // namespace
@@ -800,7 +831,7 @@ extern "C" ht_status ht_kv_attention_workspace(const ht_kv_cache *cache, int64_t
     if (st != HT_OK) return st;
     if (window < 0) return HT_ESHAPE;
     const AttnShape sh = attn_shape(T, R, cache->n_heads, cache->head_dim, n_q, max_q, max_kv, window);
-    const size_t rows = partial_rows(sh, T, n_q);
+    const size_t rows = size_t(partial_shape(sh, T, R, n_q, cache->n_heads).total);
     *bytes = size_t(align256(rows * 4u)) + rows * size_t(cache->head_dim) * 4u;
     return HT_OK;
 }
@@ -832,7 +863,11 @@ extern "C" ht_status ht_kv_attention(const uint16_t *q, int64_t ldq, int64_t hsq
     a.kv_len = kv_len;
     a.out = out;
     a.lse = static_cast<float *>(ws);
-    a.part = a.lse ? a.lse + align256(partial_rows(sh, T, n_q) * 4u) / 4 : nullptr;
+    const PartialShape ps = partial_shape(sh, T, R, n_q, cache->n_heads);
+    a.part = need > 0 ? a.lse + align256(size_t(ps.total) * 4u) / 4 : nullptr;
+    a.dec_rows = ps.dec_rows;
+    a.dec_per_request = ps.dec_per_request;
+    a.prompt_at = ps.dec_total;
     a.ldq = ldq; a.hsq = hsq; a.ldo = ldo; a.hso = hso; a.ldt = ldt; a.P = P;
     a.T = int32_t(T);
     a.n_q = n_q;

@@ -290,7 +290,7 @@ extern "C" ht_status ht_kv_write(const void *k, int64_t ldk, int64_t hsk, int32_
     ht_status st = check_cache(cache);
     if (st != HT_OK) return st;
     if (!act_size(kt) || !act_size(vt)) return HT_EINVAL;
-    if (T < 0 || T > (int64_t(1) << 30)) return HT_ESHAPE;
+    if (T < 0 || T > (int64_t(1) << 28)) return HT_ESHAPE;
     if (T == 0) return HT_OK;
     if ((st = check_rows(k, ldk, hsk, cache->n_heads, cache->head_dim, act_size(kt))) != HT_OK) return st;
     if ((st = check_rows(v, ldv, hsv, cache->n_heads, cache->head_dim, act_size(vt))) != HT_OK) return st;

@@ -286,6 +286,7 @@ RopeShape rope_shape(int64_t rows, int32_t H, int32_t D, int32_t half, bool bwd)
     const int64_t want = bwd ? 1024 : 4096;
     if (rows > want * step) per = (rows + want * step - 1) / (want * step) * step;
     if (!bwd && per > 4 * step) per = 4 * step;
+    while (rows / per >= (int64_t(1) << 22)) per *= 2;    // the launch's limit on threads
     int64_t tokens = (per + H - 2) / H + 1;               // most tokens a run of `per` rows touches
     const int64_t fit = (16 << 10) / (8 * half);          // 16 KiB of angles
     if (tokens > fit) tokens = fit;
@@ -294,7 +295,7 @@ RopeShape rope_shape(int64_t rows, int32_t H, int32_t D, int32_t half, bool bwd)
 
 ht_status check_rope(int64_t T, int32_t n_q, int32_t n_k, int32_t D, int32_t rot) {
     if (T < 0 || n_q <= 0 || n_k < 0 || n_q > 4096 || n_k > 4096 || D <= 0 || D % 8 || D > 256 || rot < 0 || rot % 8 ||
-        rot > D || T * (int64_t(n_q) + n_k) >= (int64_t(1) << 40))
+        rot > D || T > (int64_t(1) << 36) || T * (int64_t(n_q) + n_k) >= (int64_t(1) << 40))
         return HT_ESHAPE;
     return HT_OK;
 }

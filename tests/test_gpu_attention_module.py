@@ -104,6 +104,36 @@ def test_autograd(x, y, norm):
     assert torch.equal(one, flat)
 
 
+def test_calls_on_a_given_stream():
+    """stream= with inputs that are copied first (misaligned), while the
+    current stream reuses memory: the same bits as on the current stream."""
+    torch.manual_seed(4)
+    T, n, m, d = 300, 8, 2, 64
+    odd = lambda h: torch.randn(T * h * d + 1, device=dev())[1:].view(T, h, d)  # noqa: E731
+    q, k, v, dq, dk = odd(n), odd(m), odd(m), odd(n), odd(m)
+    w = [torch.randn(d, device=dev()) for _ in range(2)]
+    pos, inv = torch.arange(T, dtype=torch.int32, device=dev()), api.rope_inv_freq(d, device=dev())
+    ints = lambda a: torch.tensor(a, dtype=torch.int32, device=dev())  # noqa: E731
+    got = []
+    for side in (None, torch.cuda.Stream(), torch.cuda.Stream().cuda_stream):
+        codes, scales = api.kv_cache(12, m, d, dev())
+        table = torch.full((2, 6), -1, dtype=torch.int32, device=dev())
+        torch.cuda.synchronize()
+        step = api.kv_plan(ints([100, 200]), ints([0, 0]), ints([0, 0]), table, ints(list(range(12))), ints([12]), T,
+                           stream=side)
+        yq, yk = api.qk_norm_rope(q, k, pos, inv, *w, out_dtype=torch.bfloat16, stream=side)
+        api.kv_write(yk, v, step.slots, codes, scales, stream=side)
+        o = api.kv_attention(yq, codes, scales, table, step.cu_q, step.kv_len, 200, stream=side)
+        g = api.qk_norm_rope_backward(dq, dk, q, k, pos, inv, *w, stream=side)
+        junk = [torch.full((T, n, d), 9.0, device=dev()) for _ in range(8)]   # what the copies' memory would become
+        torch.cuda.synchronize()
+        del junk
+        got.append([t.clone() for t in (*step, table, yq, yk, codes, scales, o, *g)])
+    for other in got[1:]:
+        for a, b in zip(got[0], other):
+            assert torch.equal(a, b)
+
+
 def test_decode_step_in_a_graph():
     """Norm, write and attention of a decode step in one HIP graph, replayed
     with other inputs and lengths, against the same calls made eagerly; the

@@ -66,6 +66,14 @@ def test_prompts(n_q, H, D, q_len, kv_len):
     check(*make(D + sum(kv_len), q_len, kv_len, n_q, H, D)[1:])
 
 
+@pytest.mark.parametrize("n_q,H,D", [(4, 1, 64), (16, 2, 128), (12, 6, 256)])
+def test_answers_beside_prompts(n_q, H, D):
+    """Requests of both kernels in one batch, long enough that both split
+    their tokens; one request with a window over a long cache."""
+    check(*make(D, [130, 1, 2, 40, 0, 3], [2200, 5000, 1700, 40, 100, 64], n_q, H, D)[1:])
+    check(*make(D + 1, [1, 90], [9000, 3000], n_q, H, D)[1:], window=2500)
+
+
 @pytest.mark.parametrize("window", [1, 5, 64, 65, 100000])
 @pytest.mark.parametrize("q_len,kv_len", [([1, 1], [500, 3]), ([100, 3], [300, 64])])
 def test_window(window, q_len, kv_len):

@@ -121,7 +121,7 @@ WRITE = dict(k=A, ldk=256, hsk=128, kt=BF, v=A, ldv=1024, hsv=128, vt=F32, T=5, 
 @pytest.mark.parametrize("change,code", [
     *[({k: None}, EINVAL) for k in ("k", "v", "slots")], *[({k: A + 8}, EALIGN) for k in ("k", "v")],
     (dict(slots=A + 1), EALIGN), (dict(kt=0), EINVAL), (dict(vt=3), EINVAL), (dict(T=-1), ESHAPE),
-    (dict(T=1 << 31), ESHAPE), (dict(ldk=100), ESHAPE), (dict(hsv=64), ESHAPE), (dict(ldk=260), EALIGN),
+    (dict(T=(1 << 28) + 1), ESHAPE), (dict(ldk=100), ESHAPE), (dict(hsv=64), ESHAPE), (dict(ldk=260), EALIGN),
     (dict(ldv=1026), EALIGN)])
 def test_write_argument_checks(change, code):
     assert call("ht_kv_write", {**WRITE, "cache": cache()}, **change) == code
@@ -134,8 +134,8 @@ ATTN = dict(q=A, ldq=1024, hsq=128, T=6, n_q=8, cache=None, table=A, P=2000, ldt
 @pytest.mark.parametrize("change,code", [
     *[({k: None}, EINVAL) for k in ("q", "table", "cu", "kv", "out")],
     *[({k: A + 8}, EALIGN) for k in ("q", "out", "ws")], *[({k: A + 2}, EALIGN) for k in ("table", "cu", "kv")],
-    (dict(T=-1), ESHAPE), (dict(R=0), ESHAPE), (dict(n_q=0), ESHAPE), (dict(n_q=7), ESHAPE), (dict(P=0), ESHAPE),
-    (dict(ldt=7), ESHAPE), (dict(window=-1), ESHAPE), (dict(max_q=-1), ESHAPE), (dict(max_kv=-1), ESHAPE),
+    (dict(T=-1), ESHAPE), (dict(R=0), ESHAPE), (dict(R=1 << 22), ESHAPE), (dict(n_q=0), ESHAPE), (dict(n_q=7), ESHAPE),
+    (dict(P=0), ESHAPE), (dict(ldt=7), ESHAPE), (dict(window=-1), ESHAPE), (dict(max_q=-1), ESHAPE), (dict(max_kv=-1), ESHAPE),
     (dict(scale=float("nan")), EINVAL), (dict(scale=float("inf")), EINVAL), (dict(ldq=64), ESHAPE),
     (dict(hso=64), ESHAPE), (dict(ldo=1028), EALIGN), (dict(ws=None), ESMALL), (dict(ws_bytes=64), ESMALL)])
 def test_attention_argument_checks(change, code):
@@ -157,6 +157,8 @@ def test_attention_workspace_is_bounded():
     assert B.ht_kv_attention_workspace(d, 8192, 1, 32, 8192, 8192) == 0
     assert B.ht_kv_attention_workspace(d, 1, 1, 32, 1, 64) == 0
     assert B.ht_kv_attention_workspace(d, 1, 1, 32, 0, 0) == 0           # lengths not known
+    # answers beside a prompt of 8192 rows: partial results of the answers' rows, not of the prompt's
+    assert 0 < B.ht_kv_attention_workspace(d, 8208, 17, 32, 8192, 131072) <= 64 * 17 * 8 * 32 * 129 * 4 + 256
     assert 0 < B.ht_kv_attention_workspace(d, 1, 1, 32, 1, 100000) <= 64 * 32 * 129 * 4 + 256
 
 
@@ -176,7 +178,7 @@ def test_python_refusals():
                      ((q, k, pos, inv), dict(q_weight=t(64))), ((q, k, pos, inv), dict(q_weight=t(64), k_weight=t(63))),
                      ((q, k, pos, inv), dict(out_dtype=torch.float16)), ((q[0], k, pos, inv), {}),
                      ((q, k, pos, inv), dict(out=(t(3, 4, 32), k)))):
-        with pytest.raises(ValueError):
+        with pytest.raises(ValueError, match="expected|both or neither"):
             rope(*args, **kw)
     codes, scales = api.kv_cache(5, 2, 64, "cpu")
     assert codes.shape == (5, 2, 2, 4096) and scales.shape == (5, 2, 2) and not codes.any()
@@ -187,25 +189,32 @@ def test_python_refusals():
     for args in ((k, k, slots.long(), codes, scales), (k, k[:, :1], slots, codes, scales), (k[:2], k, slots, codes, scales),
                  (k, k, slots, codes.float(), scales), (k, k, slots, codes, scales[:4]), (k, k, slots, codes[:, :1], scales),
                  (k.half(), k, slots, codes, scales)):
-        with pytest.raises(ValueError):
+        with pytest.raises(ValueError, match="expected|both or neither"):
             api.kv_write(*args)
     qb, table, cu, kv = q.bfloat16(), t(1, 4, dtype=I32), t(2, dtype=I32), t(1, dtype=I32)
     for args, kw in (((q, codes, scales, table, cu, kv, 3), {}), ((qb[..., :32], codes, scales, table, cu, kv, 3), {}),
                      ((qb, codes, scales, table[0], cu, kv, 3), {}), ((qb, codes, scales, table, cu[:1], kv, 3), {}),
                      ((qb, codes, scales, table, cu, kv.long(), 3), {}), ((qb, codes, scales, table, cu, kv, 3), dict(out=q)),
                      ((qb, codes, scales, t(1, 8, dtype=I32)[:, ::2], cu, kv, 3), {})):
-        with pytest.raises(ValueError):
+        with pytest.raises(ValueError, match="expected|both or neither"):
             api.kv_attention(*args, **kw)
     lens, tab, free = t(2, dtype=I32), t(2, 4, dtype=I32), t(9, dtype=I32)
     for args, kw in (((lens.long(), lens, lens, tab, free, free[:1], 2), {}), ((lens, lens[:1], lens, tab, free, free[:1], 2), {}),
                      ((lens, lens, lens, tab[:1], free, free[:1], 2), {}), ((lens, lens, lens, tab, free, free[:2], 2), {}),
                      ((lens, lens, lens, tab, free, free[:1], 2), dict(out=[lens] * 6))):
-        with pytest.raises(ValueError):
+        with pytest.raises(ValueError, match="expected|both or neither"):
             api.kv_plan(*args, **kw)
-    with pytest.raises(ValueError):
+    with pytest.raises(ValueError, match="expected|both or neither"):
         api.kv_release(lens, lens, lens, tab, free, free[:1])
-    with pytest.raises(ValueError):
+    with pytest.raises(ValueError, match="expected|both or neither"):
         api.kv_release(t(2, dtype=torch.bool), lens, lens, tab.t(), free, free[:1])
+    # arguments that are right but not on a GPU: host pointers never reach a kernel
+    for f, args in ((rope, (q, k, pos, inv)), (api.kv_write, (k, k, slots, codes, scales)),
+                    (api.kv_attention, (qb, codes, scales, table, cu, kv, 3)),
+                    (api.kv_plan, (lens, lens, lens, tab, free, free[:1], 2)),
+                    (api.kv_release, (t(2, dtype=torch.bool), lens, lens, tab, free, free[:1]))):
+        with pytest.raises(ValueError, match="must be on the GPU"):
+            f(*args)
 
 
 # -- the host reference -------------------------------------------------------
