@@ -1,4 +1,25 @@
 // kv_attn.hip -- attention of a batch's query rows over the paged 8-bit cache.
+//
+//   o = sum_j w_j V_j / sum_j w_j,   w_j = 2^(x_j),   x_j = scale log2(e) q . K_j
+//
+// in one pass over the pages with a running maximum and sum.  A page's scales
+// are powers of two, 2^(k) for K and 2^(v) for V: with codes c, K = c 2^k is a
+// factor of the score and V = c 2^v an addend of the exponent, so that
+// w_j V_j = 2^(x_j + v) c_j.  The maximum is that of y_j = x_j + v, the size of
+// a token's contribution to o, and the weights go to the matrix cores as fp16
+// relative to it (round to nearest; 11 bits for anything within 2^-26 of the
+// largest contribution); the sum of the weights adds 2^(-v) times each page's.
+// A heavy token with small values therefore does not push the others out of
+// fp16's range.  Scores, maxima, sums and outputs are fp32.
+//
+// Rows of a request and the heads of a group that share a KV head are columns
+// of one product, S^T = K Q^T, O^T = V^T P^T, so every page is read once per
+// tile of columns.  Few columns (answers, drafts): attn_decode_kernel, bound by
+// HBM.  Many (prompts): attn_prompt_kernel, bound by the matrix and vector
+// units.  A batch with both runs both, each on its requests.  Pages of one
+// request are split over workgroups where that fills the card, and the
+// partial results joined in their order: the result depends on the launch's
+// hints by fp32 rounding only and is the same from run to run.
 #include "kv.h"
 
 namespace ht {
@@ -128,6 +149,16 @@ __device__ __forceinline__ void encode16(const uint16_t *x, float f, i32x4 &hi, 
 // Columns (row of the request, head of the group) in tiles of 16; a
 // workgroup's four wavefronts take the pages of its split in turn, each with
 // a running maximum and sum of its own, joined through LDS at the end.
+//
+// Codes go from HBM straight into the operands of the MFMAs, which is what the
+// cache's layout is for: K as int8 against q in two int8 planes (exact int32
+// sums; converting K to fp16 would cost 5 vector operations per 4 codes), V to
+// fp16 in registers.  The accumulator of S^T (16 tokens x 16 columns) holds 4
+// tokens of a column per lane, and V's order of tokens makes two such blocks
+// the B operand of P.V as they are.  Bound by HBM: 258 MB of 64 ragged requests
+// in 52 us + 5 us for the join (5.0 TB/s), 683 MB of 3 x 120k tokens in 119 + 8
+// (5.7 TB/s; a copy reaches 4.8).  A request of 17 pages takes 9 us, five page
+// round trips per wavefront.
 //
 // ONCE: every code is read by one workgroup (one tile of columns), so the loads
 // are hinted not to stay in the caches: 64 ragged requests of 32 x 128 heads 64
@@ -343,6 +374,13 @@ __global__ __launch_bounds__(kAttnThreads) void attn_decode_kernel(AttnArgs a) {
 // operand takes its tokens in that same order, so the weights go from one
 // product to the next in registers.  The next page is loaded into registers
 // while this one is multiplied, and converted into the other LDS buffer after.
+//
+// 8192 rows of 32 x 128 heads: 556 us, 989 TFLOP/s, where a large library
+// product reaches 1211 on this card.  The matrix units are busy 46% of the time
+// and the vector units 55%: a 32x32x16 product leaves room for about four vector
+// instructions, and a page has eight per product (two exponentials, their
+// sums, maxima and conversions).  At D = 64 the same vector work meets half the
+// products: six windowed chunks take 128 us, 490 TFLOP/s.
 template <int DC, int NW>
 __global__ __launch_bounds__(64 * NW, DC <= 2 ? 2 : 1) void attn_prompt_kernel(AttnArgs a) {
     constexpr int D = 64 * DC, KS = D / 16, DB = D / 32, kCols = 32 * NW, kThr = 64 * NW;
@@ -665,8 +703,9 @@ __global__ __launch_bounds__(kAttnThreads) void attn_join_kernel(AttnArgs a) {
 }
 
 // The same for many rows: a group of D / 4 lanes per row and head, which goes
-// through the splits one after the other with a running maximum.  2300 rows of
-// 32 heads x 64 in 2 splits: 19 us where a workgroup per row and head takes 100.
+// through the splits one after the other with a running maximum.  A prompt call
+// of 2300 rows of 32 heads x 64 in 2 splits: 158 us, with a workgroup per row and
+// head 248.
 template <int DC>
 __global__ __launch_bounds__(kAttnThreads) void attn_join_rows_kernel(AttnArgs a) {
     constexpr int D = 64 * DC, kLanes = D / 4, kGroups = kAttnThreads / kLanes;

@@ -8,7 +8,8 @@
 // and no exchange between workgroups.  Every workgroup computes the prefix
 // sums itself, 1024 requests at a time (12 bytes each, from the L2 after the
 // first reader), and then serves its own share of the rows and of the new
-// pages; nothing that one workgroup writes is read by another.
+// pages; nothing that one workgroup writes is read by another.  8 requests 4.1
+// us, 512 requests with 35k rows 8.0 us (a launch that does nothing: about 2).
 #include "kv.h"
 
 namespace ht {
