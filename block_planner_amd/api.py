@@ -194,6 +194,15 @@ def _need(t: torch.Tensor, name: str, dtype, shape: tuple) -> None:
         raise ValueError(f"{name}: expected a contiguous tensor")
 
 
+def _ints(*specs) -> None:
+    """Every (tensor, name, n): int32 [n], dense."""
+    i32 = torch.int32
+    for t, name, n in specs:
+        shape = t.shape
+        if t.dtype is not i32 or len(shape) != 1 or shape[0] != n or not t.is_contiguous():
+            _need(t, name, i32, (n,))
+
+
 def _on_gpu(*tensors) -> None:
     """The kernels get bare addresses: host memory never reaches them."""
     for t in tensors:
@@ -291,17 +300,14 @@ def kv_plan(q_len: torch.Tensor, kv_len: torch.Tensor, owned: torch.Tensor, tabl
     if stream is not None:
         with _using(stream):
             return kv_plan(q_len, kv_len, owned, table, free_pages, n_free, T, out)
-    i32, R = torch.int32, q_len.shape[0]
-    for t, name in ((q_len, "q_len"), (kv_len, "kv_len"), (owned, "owned")):
-        _need(t, name, i32, (R,))
+    R = q_len.shape[0]
+    _ints((q_len, "q_len", R), (kv_len, "kv_len", R), (owned, "owned", R), (n_free, "n_free", 1),
+          (free_pages, "free_pages", free_pages.numel()))
     _table(table, R)
-    _need(free_pages, "free_pages", i32, (free_pages.numel(),))
-    _need(n_free, "n_free", i32, (1,))
     if out is None:
         out = kv_step(R, T, q_len.device)
     else:
-        for t, name, n in zip(out, KVStep._fields, (R + 1, T, T, R, R, 2)):
-            _need(t, name, i32, (n,))
+        _ints(*zip(out, KVStep._fields, (R + 1, T, T, R, R, 2)))
         if not isinstance(out, KVStep):
             out = KVStep(*out)
     _on_gpu(q_len, kv_len, owned, table, free_pages, n_free, *out)
@@ -316,9 +322,8 @@ def kv_release(which: torch.Tensor, kv_len: torch.Tensor, owned: torch.Tensor, t
     R = which.shape[0]
     if which.dtype not in (torch.bool, torch.uint8) or which.dim() != 1 or not which.is_contiguous():
         raise ValueError(f"which: expected contiguous bool or uint8 [requests], got {which.dtype} {tuple(which.shape)}")
-    for t, name, n in ((kv_len, "kv_len", R), (owned, "owned", R), (n_free, "n_free", 1)):
-        _need(t, name, torch.int32, (n,))
-    _need(free_pages, "free_pages", torch.int32, (free_pages.numel(),))
+    _ints((kv_len, "kv_len", R), (owned, "owned", R), (n_free, "n_free", 1),
+          (free_pages, "free_pages", free_pages.numel()))
     _table(table, R)
     _on_gpu(which, kv_len, owned, table, free_pages, n_free)
     B.ht_kv_release(which, kv_len, owned, table, free_pages, n_free, stream=stream)
@@ -442,8 +447,7 @@ def kv_attention(q: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, tab
         raise ValueError(f"q: expected head dim {codes.shape[3] // B.HT_KV_PAGE}, got {D}")
     R = kv_len.shape[0]
     _table(table, R)
-    _need(cu_q, "cu_q", torch.int32, (R + 1,))
-    _need(kv_len, "kv_len", torch.int32, (R,))
+    _ints((cu_q, "cu_q", R + 1), (kv_len, "kv_len", R))
     if out is not None:
         _out_rows(out, "out", q.shape, q.dtype)
     _on_gpu(q, codes, scales, table, cu_q, kv_len, out, ws)
