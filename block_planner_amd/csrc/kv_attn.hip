@@ -252,78 +252,81 @@ __global__ __launch_bounds__(kAttnThreads) void attn_decode_kernel(AttnArgs a) {
             for (int e = 0; e < NE; ++e) vf[e] = load_codes<ONCE>(kp + kPage * D + e * 1024);
         };
         for (int p_at = p_first + wv; p_at < p_last; p_at += 64 * kWaves) {
-          const int mine = p_at + lane * kWaves, count = min(64, (p_last - p_at + kWaves - 1) / kWaves);
-          int32_t entry = row_of_table[min(mine, p_last - 1)];
-          if (entry < 0 || entry >= a.n_pages || mine >= p_last) entry = -1;
-          const float2 scale = *reinterpret_cast<const float2 *>(a.scales + (int64_t(max(entry, 0)) * a.n_heads + head) * 2);
-          int id = __builtin_amdgcn_readlane(entry, 0);
-          const int8_t *next = codes_of(id);
-          load_k(next);
-          load_v(next);
-          for (int at = 0; at < count; ++at) {
-            const int p = p_at + at * kWaves;
-            const bool there = id >= 0;
-            const float ks = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(scale.x), at));
-            const float vs = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(scale.y), at));
-            const int ev = exp_of_scale(vs) - 7;
-            if (at + 1 < count) {
-                id = __builtin_amdgcn_readlane(entry, at + 1);
-                next = codes_of(id);
-            }
-            // scores of 16 tokens x 16 columns each, in the units of the codes
-            const float f = qs * ks, ef = float(ev);
-            float y[4][4];
-            float top = -INFINITY;
+            const int mine = p_at + lane * kWaves, count = min(64, (p_last - p_at + kWaves - 1) / kWaves);
+            int32_t entry = row_of_table[min(mine, p_last - 1)];
+            if (entry < 0 || entry >= a.n_pages || mine >= p_last) entry = -1;
+            const int64_t blk = (int64_t(max(entry, 0)) * a.n_heads + head) * 2;
+            const float2 scale = *reinterpret_cast<const float2 *>(a.scales + blk);
+            int id = __builtin_amdgcn_readlane(entry, 0);
+            const int8_t *next = codes_of(id);
+            load_k(next);
+            load_v(next);
+            for (int at = 0; at < count; ++at) {
+                const int p = p_at + at * kWaves;
+                const bool there = id >= 0;
+                const float ks = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(scale.x), at));
+                const float vs = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(scale.y), at));
+                const int ev = exp_of_scale(vs) - 7;
+                if (at + 1 < count) {
+                    id = __builtin_amdgcn_readlane(entry, at + 1);
+                    next = codes_of(id);
+                }
+                // scores of 16 tokens x 16 columns each, in the units of the codes
+                const float f = qs * ks, ef = float(ev);
+                float y[4][4];
+                float top = -INFINITY;
 #pragma unroll
-            for (int b = 0; b < 4; ++b) {
-                i32x4 sh = {0, 0, 0, 0}, sl = {0, 0, 0, 0};
+                for (int b = 0; b < 4; ++b) {
+                    i32x4 sh = {0, 0, 0, 0}, sl = {0, 0, 0, 0};
 #pragma unroll
-                for (int j = 0; j < DC; ++j) {
-                    sh = __builtin_amdgcn_mfma_i32_16x16x64_i8(kf[b][j], qh[j], sh, 0, 0, 0);
-                    sl = __builtin_amdgcn_mfma_i32_16x16x64_i8(kf[b][j], ql[j], sl, 0, 0, 0);
+                    for (int j = 0; j < DC; ++j) {
+                        sh = __builtin_amdgcn_mfma_i32_16x16x64_i8(kf[b][j], qh[j], sh, 0, 0, 0);
+                        sl = __builtin_amdgcn_mfma_i32_16x16x64_i8(kf[b][j], ql[j], sl, 0, 0, 0);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) y[b][i] = float(sh[i] * 256 + sl[i]) * f + ef;
+                }
+                if (at + 1 < count) load_k(next);
+                const int j0 = p * kPage;
+                if (!there || j0 < lo_max || j0 + kPage > hi_min) {
+#pragma unroll
+                    for (int b = 0; b < 4; ++b)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int j = j0 + b * 16 + g * 4 + i;
+                            if (!there || j < lo || j >= hi) y[b][i] = -INFINITY;
+                        }
                 }
 #pragma unroll
-                for (int i = 0; i < 4; ++i) y[b][i] = float(sh[i] * 256 + sl[i]) * f + ef;
-            }
-            if (at + 1 < count) load_k(next);
-            const int j0 = p * kPage;
-            if (!there || j0 < lo_max || j0 + kPage > hi_min) {
+                for (int b = 0; b < 4; ++b)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) top = fmaxf(top, y[b][i]);
+                top = fmaxf(top, __shfl_xor(top, 16));
+                top = fmaxf(top, __shfl_xor(top, 32));
+                const float m_new = fmaxf(m_run, top), ref = m_new == -INFINITY ? 0.f : m_new - kTopLog2;
+                const float alpha = __builtin_amdgcn_exp2f(m_run == -INFINITY ? -INFINITY : m_run - m_new);
+                m_run = m_new;
+                float sum = 0.f;
+                f16x8 pf[2];
 #pragma unroll
                 for (int b = 0; b < 4; ++b)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const int j = j0 + b * 16 + g * 4 + i;
-                        if (!there || j < lo || j >= hi) y[b][i] = -INFINITY;
+                        const float w = __builtin_amdgcn_exp2f(y[b][i] - ref);
+                        sum += w;
+                        pf[b >> 1][(b & 1) * 4 + i] = _Float16(w);
                     }
-            }
+                l_run = l_run * alpha + sum * pow2f(-ev);
 #pragma unroll
-            for (int b = 0; b < 4; ++b)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) top = fmaxf(top, y[b][i]);
-            top = fmaxf(top, __shfl_xor(top, 16));
-            top = fmaxf(top, __shfl_xor(top, 32));
-            const float m_new = fmaxf(m_run, top), ref = m_new == -INFINITY ? 0.f : m_new - kTopLog2;
-            const float alpha = __builtin_amdgcn_exp2f(m_run == -INFINITY ? -INFINITY : m_run - m_new);
-            m_run = m_new;
-            float sum = 0.f;
-            f16x8 pf[2];
-#pragma unroll
-            for (int b = 0; b < 4; ++b)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float w = __builtin_amdgcn_exp2f(y[b][i] - ref);
-                    sum += w;
-                    pf[b >> 1][(b & 1) * 4 + i] = _Float16(w);
+                for (int e = 0; e < NE; ++e) {
+                    o[e] *= alpha;
+                    const f16x8 v0 = codes_to_f16(uint32_t(vf[e].x), uint32_t(vf[e].y));
+                    const f16x8 v1 = codes_to_f16(uint32_t(vf[e].z), uint32_t(vf[e].w));
+                    o[e] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v0, pf[0], o[e], 0, 0, 0);
+                    o[e] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v1, pf[1], o[e], 0, 0, 0);
                 }
-            l_run = l_run * alpha + sum * pow2f(-ev);
-#pragma unroll
-            for (int e = 0; e < NE; ++e) {
-                o[e] *= alpha;
-                o[e] = __builtin_amdgcn_mfma_f32_16x16x32_f16(codes_to_f16(uint32_t(vf[e].x), uint32_t(vf[e].y)), pf[0], o[e], 0, 0, 0);
-                o[e] = __builtin_amdgcn_mfma_f32_16x16x32_f16(codes_to_f16(uint32_t(vf[e].z), uint32_t(vf[e].w)), pf[1], o[e], 0, 0, 0);
+                if (at + 1 < count) load_v(next);
             }
-            if (at + 1 < count) load_v(next);
-          }
         }
         // join: o[e][i] is dim 16 e + 4 g + i of column col
         l_run += __shfl_xor(l_run, 16);
@@ -343,7 +346,9 @@ __global__ __launch_bounds__(kAttnThreads) void attn_decode_kernel(AttnArgs a) {
             f32x4 v = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int w = 0; w < kWaves; ++w) {
-                const float mw = s_m[w][cc], x = mw == -INFINITY && s_l[w][cc] == 0.f ? 0.f : __builtin_amdgcn_exp2f(mw == m ? 0.f : mw - m);
+                const float mw = s_m[w][cc];
+                const bool none = mw == -INFINITY && s_l[w][cc] == 0.f;
+                const float x = none ? 0.f : __builtin_amdgcn_exp2f(mw == m ? 0.f : mw - m);
                 l += s_l[w][cc] * x;
                 v += *reinterpret_cast<const f32x4 *>(&s_o[w][cc][d]) * x;
             }
@@ -806,7 +811,8 @@ ht_status check_attn(const ht_kv_cache *c, int64_t T, int64_t R, int32_t n_q, in
     const ht_status st = check_cache(c);
     if (st != HT_OK) return st;
     if (T < 0 || T > (int64_t(1) << 30) || R <= 0 || R * c->n_heads > (int64_t(1) << 22) || R > (int64_t(1) << 22) ||
-        n_q <= 0 || n_q > 4096 || n_q % c->n_heads || max_q < 0 || max_kv < 0 || max_q > (int64_t(1) << 30) || max_kv > (int64_t(1) << 30))
+        n_q <= 0 || n_q > 4096 || n_q % c->n_heads || T * (n_q / c->n_heads) > (int64_t(1) << 30) || max_q < 0 ||
+        max_kv < 0 || max_q > (int64_t(1) << 30) || max_kv > (int64_t(1) << 30))
         return HT_ESHAPE;
     return HT_OK;
 }

@@ -215,7 +215,7 @@ __device__ __forceinline__ void write_long(const WriteArgs &a, const Run &r, int
             mask[b] = m;
         }
         // piece of (token, dims) or (dim, tokens) in the block's order
-        u32x4 *p = out + (V ? ((4 * j + (lane >> 4)) * 4 + wv) * 16 + (lane & 15) : ((wv * DC + j) * 4 + (lane >> 4)) * 16 + (lane & 15));
+        u32x4 *p = out + (V ? (4 * j + (lane >> 4)) * 4 + wv : (wv * DC + j) * 4 + (lane >> 4)) * 16 + (lane & 15);
         const uint32_t all = mask.x & mask.y & mask.z & mask.w, any = mask.x | mask.y | mask.z | mask.w;
         if (all != 0xFFFFFFFFu) {
             if (any == 0 && down == 0) continue;

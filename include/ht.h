@@ -552,7 +552,7 @@ ht_status ht_qk_norm_rope_backward(const void *dq, int64_t lddq, int64_t hsdq, c
 /* ht_kv_write -- quantise rows of keys and values into the cache.
  *   k, v      [T][n_heads][D], dtypes kt and vt, rows ldk / ldv and heads hsk /
  *             hsv elements apart;
- *   slots     int32 [T] (ht_kv_plan's): rows with a slot outside the cache
+ *   slots     int32 [T] (T <= 2^28; ht_kv_plan's): rows with a slot outside the cache
  *             (-1) are skipped.  The rows of one page must follow each other,
  *             at consecutive slots; a row at offset 0 starts its page afresh
  *             (what it held does not count for the scale).
@@ -573,11 +573,14 @@ ht_status ht_kv_write(const void *k, int64_t ldk, int64_t hsk, int32_t kt, const
  *             they size the launch, results do not depend on them beyond
  *             the order of fp32 sums;
  *   out       bf16 [T][n_q][D], rows ldo and heads hso elements apart.
- * q.K runs on the int8 matrix cores with each row of q as (256 hi + lo)
- * 2^(E-14), 2^(E-1) <= max |q| < 2^E, int8 planes hi and lo (off by at most
- * 2^-15 of the row's largest entry) and exact int32 sums; the weights go to V
- * as fp16 relative to the row's largest contribution; sums in fp32.  A row of q
- * holding Inf or NaN gives NaN.  Bitwise reproducible.
+ * Requests of few columns (rows x heads per KV head: answers, drafts): q.K on
+ * the int8 matrix cores with each row of q as (256 hi + lo) 2^(E-14), 2^(E-1) <=
+ * max |q| < 2^E, int8 planes hi and lo (off by at most 2^-15 of the row's largest
+ * entry) and exact int32 sums.  Others: on the fp16 matrix cores with q 2^(14-E),
+ * exact but for entries under 2^-28 of the largest, and fp32 sums.  The weights
+ * go to V as fp16 relative to the row's largest contribution; sums in fp32.  A
+ * row of q holding Inf or NaN gives NaN.  Bitwise reproducible.  T times the heads
+ * per KV head is at most 2^30, R times n_heads 2^22.
  *   ws        ht_kv_attention_workspace bytes: partial results of split rows. */
 ht_status ht_kv_attention_workspace(const ht_kv_cache *cache, int64_t T, int64_t R, int32_t n_q, int64_t max_q,
                                     int64_t max_kv, int64_t window, size_t *bytes);

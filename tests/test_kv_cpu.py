@@ -134,7 +134,8 @@ ATTN = dict(q=A, ldq=1024, hsq=128, T=6, n_q=8, cache=None, table=A, P=2000, ldt
 @pytest.mark.parametrize("change,code", [
     *[({k: None}, EINVAL) for k in ("q", "table", "cu", "kv", "out")],
     *[({k: A + 8}, EALIGN) for k in ("q", "out", "ws")], *[({k: A + 2}, EALIGN) for k in ("table", "cu", "kv")],
-    (dict(T=-1), ESHAPE), (dict(R=0), ESHAPE), (dict(R=1 << 22), ESHAPE), (dict(n_q=0), ESHAPE), (dict(n_q=7), ESHAPE),
+    (dict(T=-1), ESHAPE), (dict(R=0), ESHAPE), (dict(R=1 << 22), ESHAPE), (dict(T=1 << 29), ESHAPE),
+    (dict(n_q=0), ESHAPE), (dict(n_q=7), ESHAPE),
     (dict(P=0), ESHAPE), (dict(ldt=7), ESHAPE), (dict(window=-1), ESHAPE), (dict(max_q=-1), ESHAPE), (dict(max_kv=-1), ESHAPE),
     (dict(scale=float("nan")), EINVAL), (dict(scale=float("inf")), EINVAL), (dict(ldq=64), ESHAPE),
     (dict(hso=64), ESHAPE), (dict(ldo=1028), EALIGN), (dict(ws=None), ESMALL), (dict(ws_bytes=64), ESMALL)])
