@@ -254,7 +254,8 @@ __global__ __launch_bounds__(1024) void rope_dw_kernel(const float *part, int n,
     const int col = threadIdx.x & 15, row = threadIdx.x >> 4;
     const int d = int(blockIdx.x) * 16 + col;
     float s = 0.f;
-    for (int i = row; i < n; i += 64) s += part[int64_t(i) * 2 * D + d];
+#pragma unroll 8
+    for (int i = row; i < n; i += 64) s += part[int64_t(i) * 2 * D + d];   // loads in flight together, added in order
     acc[row][col] = s;
     __syncthreads();
     for (int k = 32; k > 0; k >>= 1) {
@@ -285,7 +286,7 @@ RopeShape rope_shape(int64_t rows, int32_t H, int32_t D, int32_t half, bool bwd)
     // one step per workgroup until the card's 256 compute units hold 8
     // workgroups each, then longer runs, which share the angles of a token
     int64_t per = step;
-    const int64_t want = bwd ? 1024 : 4096;
+    const int64_t want = bwd ? 512 : 4096;
     if (rows > want * step) per = (rows + want * step - 1) / (want * step) * step;
     if (!bwd && per > 4 * step) per = 4 * step;
     while (rows / per >= (int64_t(1) << 22)) per *= 2;    // the launch's limit on threads
