@@ -8,7 +8,7 @@
 // Bound by HBM: x in, y out (backward: dy and x in, dx out), a few tens of
 // fp32 operations per 16 bytes.  8191 x 36 heads x 64, fp32 to bf16: 21 us, 5.3
 // TB/s (part of it from the Infinity Cache); backward of 8192 x 40 x 128 in fp32:
-// 104 us, 4.9 TB/s, + 7 us for the weights' partial sums; one token 3.3 us.
+// 89 us with the weights' partial sums, 5.6 TB/s; one token 3.3 us.
 //
 // A head's row is held by LPR lanes (8, 16 or 32 for D up to 64, 128, 256),
 // 8 elements each in two groups of four chosen so that a lane holds both
@@ -119,8 +119,17 @@ __device__ __forceinline__ void fill_angles(const RopeArgs &a, float *cs, int64_
     }
 }
 
+template <bool ONCE, typename T>
+__device__ __forceinline__ f32x4 load_row4(const T *p) {
+    if constexpr (ONCE) return ld_stream_f4(reinterpret_cast<const float *>(p));   // T is float
+    else return load4(p);
+}
+
 // BWD: 0 forward, 1 backward.  X: type of q, k (and dx); Y: type of y (and dy).
-template <int LPR, typename X, typename Y, bool NORM, bool BWD>
+// ONCE: fp32 rows of more data than the 256 MB Infinity Cache are read with the
+// hint not to keep them there: 503 MB forward 96 -> 81 us, backward 106 -> 90;
+// 63 MB forward takes 15.9 us without the hint and 17.5 with it.
+template <int LPR, typename X, typename Y, bool NORM, bool BWD, bool ONCE>
 __global__ __launch_bounds__(kRopeThreads) void rope_kernel(RopeArgs a) {
     extern __shared__ __align__(16) float cs[];
     constexpr int kRpw = 64 / LPR;                       // rows per wavefront
@@ -168,13 +177,13 @@ __global__ __launch_bounds__(kRopeThreads) void rope_kernel(RopeArgs a) {
             if (live) {
                 if (!BWD || NORM) {
                     const X *x = static_cast<const X *>(m.x) + t * m.ld + hh * m.hs;
-                    x0 = load4(x + o0);
-                    x1 = load4(x + o1);
+                    x0 = load_row4<ONCE>(x + o0);
+                    x1 = load_row4<ONCE>(x + o1);
                 }
                 if (BWD) {
                     const Y *dy = static_cast<const Y *>(m.dy) + t * m.ldd + hh * m.hsd;
-                    g0 = load4(dy + o0);
-                    g1 = load4(dy + o1);
+                    g0 = load_row4<ONCE && sizeof(Y) == 4>(dy + o0);
+                    g1 = load_row4<ONCE && sizeof(Y) == 4>(dy + o1);
                 }
             }
             float rn = 1.f;
@@ -266,11 +275,13 @@ __global__ __launch_bounds__(1024) void rope_dw_kernel(const float *part, int n,
 }
 
 template <int LPR, bool NORM, bool BWD>
-void launch_rope(const RopeArgs &a, uint32_t grid, size_t lds, bool xb, bool yb, hipStream_t s) {
-    if (xb && yb) rope_kernel<LPR, uint16_t, uint16_t, NORM, BWD><<<grid, kRopeThreads, lds, s>>>(a);
-    else if (xb) rope_kernel<LPR, uint16_t, float, NORM, BWD><<<grid, kRopeThreads, lds, s>>>(a);
-    else if (yb) rope_kernel<LPR, float, uint16_t, NORM, BWD><<<grid, kRopeThreads, lds, s>>>(a);
-    else rope_kernel<LPR, float, float, NORM, BWD><<<grid, kRopeThreads, lds, s>>>(a);
+void launch_rope(const RopeArgs &a, uint32_t grid, size_t lds, bool xb, bool yb, bool once, hipStream_t s) {
+    if (xb && yb) rope_kernel<LPR, uint16_t, uint16_t, NORM, BWD, false><<<grid, kRopeThreads, lds, s>>>(a);
+    else if (xb) rope_kernel<LPR, uint16_t, float, NORM, BWD, false><<<grid, kRopeThreads, lds, s>>>(a);
+    else if (yb && once) rope_kernel<LPR, float, uint16_t, NORM, BWD, true><<<grid, kRopeThreads, lds, s>>>(a);
+    else if (yb) rope_kernel<LPR, float, uint16_t, NORM, BWD, false><<<grid, kRopeThreads, lds, s>>>(a);
+    else if (once) rope_kernel<LPR, float, float, NORM, BWD, true><<<grid, kRopeThreads, lds, s>>>(a);
+    else rope_kernel<LPR, float, float, NORM, BWD, false><<<grid, kRopeThreads, lds, s>>>(a);
 }
 
 int lanes_per_row(int32_t D) { return D <= 64 ? 8 : D <= 128 ? 16 : 32; }
@@ -281,12 +292,15 @@ struct RopeShape {
     uint32_t grid;
 };
 
-RopeShape rope_shape(int64_t rows, int32_t H, int32_t D, int32_t half, bool bwd) {
+RopeShape rope_shape(int64_t rows, int32_t H, int32_t D, int32_t half, bool bwd, int size) {
     const int step = kRopeThreads / lanes_per_row(D);
-    // one step per workgroup until the card's 256 compute units hold 8
-    // workgroups each, then longer runs, which share the angles of a token
+    // One step per workgroup while that gives few workgroups, then longer runs,
+    // which share the angles of a token.  Backward, whose workgroups each leave a
+    // partial sum of dw: 512 for fp32 input (8192 x 40 x 128: 106 us, with 1024
+    // 109), 1024 for bf16, whose rows are half the bytes in flight (65 us, with
+    // 512 94, with 2048 68).
     int64_t per = step;
-    const int64_t want = bwd ? 512 : 4096;
+    const int64_t want = !bwd ? 4096 : size == 4 ? 512 : 1024;
     if (rows > want * step) per = (rows + want * step - 1) / (want * step) * step;
     if (!bwd && per > 4 * step) per = 4 * step;
     while (rows / per >= (int64_t(1) << 22)) per *= 2;    // the launch's limit on threads
@@ -313,21 +327,23 @@ ht_status run_rope(RopeArgs &a, int64_t T, int32_t n_q, int32_t n_k, int32_t D, 
     a.D = D;
     a.half = rot / 2;
     a.inv_d = 1.0f / float(D);
-    const RopeShape sh = rope_shape(a.rows, n_q + n_k, D, a.half > 0 ? a.half : 4, BWD);
+    const RopeShape sh = rope_shape(a.rows, n_q + n_k, D, a.half > 0 ? a.half : 4, BWD, act_size(xt));
     a.rows_per_wg = sh.rows_per_wg;
     a.tokens_lds = sh.tokens;
     size_t lds = size_t(sh.tokens) * 8 * size_t(a.half);
     if (BWD && norm) lds = lds > size_t(32) * D ? lds : size_t(32) * D;
     const bool xb = xt == HT_BF16, yb = yt == HT_BF16;
     const int lpr = lanes_per_row(D);
+    const int64_t moved = a.rows * D * (act_size(xt) * (BWD && norm ? 2 : 1) + act_size(yt));
+    const bool once = moved >= (int64_t(256) << 20);
     if (norm) {
-        if (lpr == 8) launch_rope<8, true, BWD>(a, sh.grid, lds, xb, yb, s);
-        else if (lpr == 16) launch_rope<16, true, BWD>(a, sh.grid, lds, xb, yb, s);
-        else launch_rope<32, true, BWD>(a, sh.grid, lds, xb, yb, s);
+        if (lpr == 8) launch_rope<8, true, BWD>(a, sh.grid, lds, xb, yb, once, s);
+        else if (lpr == 16) launch_rope<16, true, BWD>(a, sh.grid, lds, xb, yb, once, s);
+        else launch_rope<32, true, BWD>(a, sh.grid, lds, xb, yb, once, s);
     } else {
-        if (lpr == 8) launch_rope<8, false, BWD>(a, sh.grid, lds, xb, yb, s);
-        else if (lpr == 16) launch_rope<16, false, BWD>(a, sh.grid, lds, xb, yb, s);
-        else launch_rope<32, false, BWD>(a, sh.grid, lds, xb, yb, s);
+        if (lpr == 8) launch_rope<8, false, BWD>(a, sh.grid, lds, xb, yb, once, s);
+        else if (lpr == 16) launch_rope<16, false, BWD>(a, sh.grid, lds, xb, yb, once, s);
+        else launch_rope<32, false, BWD>(a, sh.grid, lds, xb, yb, once, s);
     }
     HT_LAUNCH_CHECK();
     if (BWD && norm && sh.grid > 1) {
@@ -381,7 +397,8 @@ extern "C" ht_status ht_qk_norm_rope_workspace(int64_t T, int32_t n_q, int32_t n
     HT_TRY(check_rope(T, n_q, n_k, D, 0));
     *bytes = 0;
     if (!norm || T == 0) return HT_OK;
-    const RopeShape sh = rope_shape(T * (int64_t(n_q) + n_k), n_q + n_k, D, 4, true);
+    // the more workgroups of the two types of input
+    const RopeShape sh = rope_shape(T * (int64_t(n_q) + n_k), n_q + n_k, D, 4, true, 2);
     if (sh.grid > 1) *bytes = size_t(sh.grid) * 2u * size_t(D) * sizeof(float);
     return HT_OK;
 }
