@@ -8,7 +8,7 @@
 // Bound by HBM: x in, y out (backward: dy and x in, dx out), a few tens of
 // fp32 operations per 16 bytes.  8191 x 36 heads x 64, fp32 to bf16: 21 us, 5.3
 // TB/s (part of it from the Infinity Cache); backward of 8192 x 40 x 128 in fp32:
-// 89 us with the weights' partial sums, 5.6 TB/s; one token 3.3 us.
+// 85 us, 5.9 TB/s, + 5 us for the weights' partial sums; one token 3.1 us.
 //
 // A head's row is held by LPR lanes (8, 16 or 32 for D up to 64, 128, 256),
 // 8 elements each in two groups of four chosen so that a lane holds both
