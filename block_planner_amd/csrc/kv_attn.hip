@@ -14,12 +14,13 @@
 //
 // Rows of a request and the heads of a group that share a KV head are columns
 // of one product, S^T = K Q^T, O^T = V^T P^T, so every page is read once per
-// tile of columns.  Few columns (answers, drafts): attn_decode_kernel, bound by
-// HBM.  Many (prompts): attn_prompt_kernel, bound by the matrix and vector
-// units.  A batch with both runs both, each on its requests.  Pages of one
+// tile of columns.  Few columns (answers, drafts) and short calls:
+// attn_decode_kernel, bound by HBM.  Many (prompts): attn_prompt_kernel, bound by
+// the matrix and vector units.  A batch with both runs both, each on its
+// requests.  Pages of one
 // request are split over workgroups where that fills the card, and the
 // partial results joined in their order: the result depends on the launch's
-// hints by fp32 rounding only and is the same from run to run.
+// hints by rounding only and is the same from run to run.
 #include "kv.h"
 
 namespace ht {
@@ -74,6 +75,8 @@ struct Request {
 // Columns (rows x heads of a group) of a request up to which the decode kernel
 // takes it, where both kernels run.
 constexpr int kDecodeCols = 32;
+// Tiles of 16 columns times pages of a call up to which it runs alone (D <= 128).
+constexpr int kDecodeVisits = 16384;
 
 __device__ __forceinline__ Request load_request(const AttnArgs &a, int r) {
     Request q;
@@ -765,7 +768,19 @@ AttnShape attn_shape(int64_t T, int64_t R, int32_t n_heads, int32_t D, int32_t n
     if (window > 0 && (window + max_q) / kPage + 2 < pages) pages = (window + max_q) / kPage + 2;
     const int64_t group = n_q / n_heads;
     AttnShape s{};
-    s.prompt = max_q * group > kDecodeCols;
+    // Up to kDecodeCols columns the decode kernel, and also for short prompts:
+    // its 16 columns convert no page and come in as many workgroups as its tiles,
+    // where the prompt kernel's few would walk the pages one after the other.
+    // What the decode kernel does is counted in tiles times pages.  Prompt kernel
+    // against decode kernel, us, one request of q rows unless said, heads / KV
+    // heads x dim: q 64 of 700, 4 times, 32 / 8 x 128 (5632) 27.3, 13.7; q 1024,
+    // 12 / 2 x 128 (12288) 29.7, 20.1; q 128 of 4000, 32 / 8 x 128 (16128) 36.3,
+    // 35.4; q 256 of 1000, 4 times, the same heads (32768) 35.6, 50.1.  At D = 256
+    // a tile's page takes twice as long: q 512, 8 / 1 (2048) 37.5, 13.9; q 1024
+    // (8192) 47.0, 28.7; q 512, 32 / 8 (8192) 39.2, 42.9; q 2048, 8 / 1 (32768)
+    // 89.6, 118.9.
+    const double visits = double((max_q * group + 15) / 16) * double(R * n_heads) * double(pages > 0 ? pages : 1);
+    s.prompt = max_q * group > kDecodeCols && visits * (D > 128 ? D : 128) > 128.0 * kDecodeVisits;
     s.decode = !s.prompt || R > 1;
     const int64_t tiles = s.prompt ? (kDecodeCols + 15) / 16 : max_q > 0 ? (max_q * group + 15) / 16 : 1;
     // Splits of the decode kernel: none up to kWholePages pages (a second launch

@@ -570,10 +570,11 @@ ht_status ht_kv_write(const void *k, int64_t ldk, int64_t hsk, int32_t kt, const
  *   table, P, ldt, cu_q, kv_len   as ht_kv_plan gives them (kv_out), lengths
  *             including this step's rows;
  *   max_q, max_kv   the largest q_len and kv_len as far as the caller knows:
- *             they size the launch, results do not depend on them beyond
- *             the order of fp32 sums;
+ *             they size the launch and choose its kernels; what is computed
+ *             does not depend on them, its rounding does (below);
  *   out       bf16 [T][n_q][D], rows ldo and heads hso elements apart.
- * Requests of few columns (rows x heads per KV head: answers, drafts): q.K on
+ * Requests of few columns (rows x heads per KV head: answers, drafts) and short
+ * calls (by R, max_q and max_kv): q.K on
  * the int8 matrix cores with each row of q as (256 hi + lo) 2^(E-14), 2^(E-1) <=
  * max |q| < 2^E, int8 planes hi and lo (off by at most 2^-15 of the row's largest
  * entry) and exact int32 sums.  Others: on the fp16 matrix cores with q 2^(14-E),

@@ -209,3 +209,42 @@ def test_offsets_past_32_bits(what):
     got = api.kv_attention(gpu(q).to(torch.bfloat16), codes, scales, gpu(pages[None]), gpu(cu), gpu(kv), rows)
     want, tol = ref.attention(q, *small, np.arange(3, dtype=np.int32)[None], cu, kv, 1 / np.sqrt(D))
     assert np.all(np.abs(got.double().cpu().numpy() - want) <= tol)
+
+
+# Short calls go to the decode kernel alone, by the launch hints: a max_kv above
+# the lengths sends them to the prompt kernel, whole (10^6) or in splits of
+# some tens of pages (40000).
+@pytest.mark.parametrize("max_kv", [40000, 10 ** 6])
+@pytest.mark.parametrize("n_q,H,D", [(4, 1, 64), (4, 2, 128), (2, 2, 192), (2, 1, 256), (8, 1, 256)])
+@pytest.mark.parametrize("q_len,kv_len,causal,window", [
+    ([70], [70], True, 0), ([130, 1, 33], [130, 200, 500], True, 0), ([64, 65], [128, 65], False, 0),
+    ([100, 3], [300, 64], True, 65), ([90], [90], False, 40), ([100, 40, 0, 120], [60, 0, 70, 4200], True, 0),
+    ([130, 1, 2, 40, 0, 3], [2200, 5000, 1700, 40, 100, 64], True, 0), ([1, 90], [5000, 3000], True, 2500)])
+def test_short_prompts_in_the_prompt_kernel(n_q, H, D, q_len, kv_len, causal, window, max_kv):
+    print(n_q, H, D, q_len, kv_len, causal, window, max_kv, flush=True)
+    check(*make(D + sum(kv_len), q_len, kv_len, n_q, H, D)[1:], causal=causal, window=window, max_kv=max_kv)
+
+
+@pytest.mark.parametrize("n_q,H,D", [(16, 2, 64), (12, 2, 128), (4, 2, 192), (8, 1, 256)])
+@pytest.mark.parametrize("q_len,kv_len,window", [
+    ([260], [260], 0), ([200, 1, 33], [250, 2000, 500], 0), ([150], [2300], 0), ([90, 17], [3000, 1700], 333),
+    ([50, 0, 20], [30, 90, 0], 0)])
+def test_short_prompts(n_q, H, D, q_len, kv_len, window):
+    """Prompts of many tiles: on the decode kernel, whole and in splits."""
+    print(n_q, H, D, q_len, kv_len, window, flush=True)
+    check(*make(D + sum(kv_len), q_len, kv_len, n_q, H, D)[1:], window=window)
+
+
+@pytest.mark.parametrize("max_kv", [300, 10 ** 6])
+def test_short_prompts_with_hidden_pages_and_nan_rows(max_kv):
+    rng, q, codes, scales, table, cu, kv = make(14, [80, 40, 64], [300, 129, 64], 4, 2, 64)
+    table[0, 1], table[0, 3] = -1, len(codes)
+    table[1, 2] = 2 ** 31 - 1
+    table[2, 0] = -2 ** 31
+    clean = check(q, codes, scales, table, cu, kv, max_kv=max_kv)
+    assert torch.all(clean[120:] == 0)
+    q[0, 1, 5], q[70, 3, 0], q[100, 0, 63] = np.nan, np.inf, -np.inf
+    got = run(q, codes, scales, table, cu, kv, max_kv=max_kv)
+    hurt = np.zeros(q.shape[:2], bool)
+    hurt[0, 1] = hurt[70, 3] = hurt[100, 0] = True
+    assert torch.all(torch.isnan(got[gpu(hurt)])) and torch.equal(got[gpu(~hurt)], clean[gpu(~hurt)])
