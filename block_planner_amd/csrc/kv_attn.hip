@@ -42,6 +42,10 @@ constexpr float kLog2e = 1.44269504088896341f;
 // maximum (and rescales its sums) only for a score kSlackLog2 above it: weights
 // stay under 2^15.5, below fp16's 65504.
 constexpr float kTopLog2 = 12.f, kSlackLog2 = 3.5f;
+// Size of a maximum (log2 units) from which fp32 no longer holds a score, and its
+// difference to the maximum plus kTopLog2, to the half unit that is left between
+// 2^15.5 and 65504: the prompt kernel then takes the difference first.
+constexpr float kFarLog2 = 0x1p20f;
 
 struct AttnArgs {
     const uint16_t *q;
@@ -306,7 +310,8 @@ __global__ __launch_bounds__(kAttnThreads) void attn_decode_kernel(AttnArgs a) {
                     for (int i = 0; i < 4; ++i) top = fmaxf(top, y[b][i]);
                 top = fmaxf(top, __shfl_xor(top, 16));
                 top = fmaxf(top, __shfl_xor(top, 32));
-                const float m_new = fmaxf(m_run, top), ref = m_new == -INFINITY ? 0.f : m_new - kTopLog2;
+                // the difference first: m_new - kTopLog2 would round to whole powers of two where scores are far from 0
+                const float m_new = fmaxf(m_run, top), ref = m_new == -INFINITY ? 0.f : m_new;
                 const float alpha = __builtin_amdgcn_exp2f(m_run == -INFINITY ? -INFINITY : m_run - m_new);
                 m_run = m_new;
                 float sum = 0.f;
@@ -315,7 +320,7 @@ __global__ __launch_bounds__(kAttnThreads) void attn_decode_kernel(AttnArgs a) {
                 for (int b = 0; b < 4; ++b)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const float w = __builtin_amdgcn_exp2f(y[b][i] - ref);
+                        const float w = __builtin_amdgcn_exp2f((y[b][i] - ref) + kTopLog2);
                         sum += w;
                         pf[b >> 1][(b & 1) * 4 + i] = _Float16(w);
                     }
@@ -531,7 +536,8 @@ __global__ __launch_bounds__(64 * NW, DC <= 2 ? 2 : 1) void attn_prompt_kernel(A
             __syncthreads();   // K of p + 1 and V of p are in LDS; K of p and V of p - 1 have been read
             const int ev = exp_of_scale(sc.y) - 7;
             // above 0 (or NaN), so that a masked score, -inf, stays one
-            const float f = qs * sc.x == 0.f ? 0x1p-120f : qs * sc.x, ef = float(ev);
+            float f = qs * sc.x == 0.f ? 0x1p-120f : qs * sc.x;
+            const float ef = float(ev);
             const int j0 = p * kPage;
             if (id0 < 0 || j0 < w_lo_max || j0 + kPage > w_hi_min) {
                 const int seen = id0 < 0 ? 0 : hi;
@@ -548,7 +554,7 @@ __global__ __launch_bounds__(64 * NW, DC <= 2 ? 2 : 1) void attn_prompt_kernel(A
             for (int b = 0; b < 2; ++b)
 #pragma unroll
                 for (int i = 0; i < 16; ++i) top = fmaxf(top, s[b][i]);
-            const float m_new = fmaxf(m_run, max_halves(top * f + ef));
+            const float m_new = fmaxf(m_run, max_halves(fmaf(top, f, ef)));
             if (__any(m_new > m_run + kSlackLog2)) {
                 const float alpha = m_run == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m_run - m_new);
                 l_run *= alpha;
@@ -556,7 +562,20 @@ __global__ __launch_bounds__(64 * NW, DC <= 2 ? 2 : 1) void attn_prompt_kernel(A
                 for (int d = 0; d < DB; ++d) o[d] *= alpha;
                 m_run = m_new;
             }
-            const float shift = ef - (m_run == -INFINITY ? 0.f : m_run - kTopLog2);
+            const float m = m_run == -INFINITY ? 0.f : m_run;
+            float shift = ef - (m - kTopLog2);
+            if (fabsf(m) > kFarLog2) {
+                // the same rounding as m's, so that the largest score is at 0 and none far above (NaN stays)
+#pragma unroll
+                for (int b = 0; b < 2; ++b)
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const float x = fmaf(s[b][i], f, ef) - m + kTopLog2;
+                        s[b][i] = x > kTopLog2 + kSlackLog2 ? kTopLog2 + kSlackLog2 : x;
+                    }
+                f = 1.f;
+                shift = 0.f;
+            }
             // The next page's 2 KS products with this page's 32 weights between
             // them, then this page's 4 DB products with the conversions of the
             // pages behind: matrix and vector instructions side by side, operands

@@ -1,0 +1,51 @@
+"""ht_kv_attention at the limits of its arithmetic and of its arguments: scores
+of any size, rows of no request, rows of q with one entry far above the rest."""
+import numpy as np
+import pytest
+import torch
+
+import kv_reference as ref
+from test_gpu_kv_attention import bf16, check, make, run
+
+pytestmark = pytest.mark.gpu
+
+
+# rows of the requests, launch hint for kv_len: the decode kernel, the prompt kernel whole, and in splits
+SIDES = {"decode": ([1, 3], {}), "prompt": ([70, 40], dict(max_kv=10 ** 6)), "splits": ([70, 40], dict(max_kv=40000))}
+
+
+@pytest.mark.parametrize("side", SIDES)
+@pytest.mark.parametrize("power", [10, 20, 22, 24, 25, 26, 27, 28, 29, 30, 33, 40, 60, 100])
+def test_scores_of_any_size(side, power):
+    """Scores of about 2^power in log2 units.  From 2^24 on fp32 does not tell
+    a whole unit: a row whose two largest scores differ by more than their
+    rounding gives the value of its largest (a weight is fp16: 2^-11; the result
+    bf16: 2^-8), every row a mean of the values it sees."""
+    q_len, hint = SIDES[side]
+    rng, q, codes, scales, table, cu, kv = make(power, q_len, [200, 2100], 8, 2, 64)
+    D, index = 64, ref.block_index(64)
+    scale = 1 / np.sqrt(D)
+    vals = []
+    for r in range(2):
+        pages = table[r, :-(-kv[r] // 64)]
+        vals.append([[(codes[pages, h, i][:, index[i].reshape(-1)].astype(np.float64)
+                       * scales[pages, h, i].astype(np.float64)[:, None]).reshape(-1, D)[:kv[r]] for i in (0, 1)]
+                     for h in range(2)])
+    far = max(np.abs(vals[r][h][0] @ q[cu[r]:cu[r + 1]].reshape(-1, D).T).max() for r in range(2) for h in range(2))
+    q = bf16(q * np.float32(2.0 ** (power - int(np.floor(np.log2(far * scale * np.log2(np.e)))))))
+    got = run(q, codes, scales, table, cu, kv, **hint).double().cpu().numpy()
+    assert np.isfinite(got).all()
+    sure = 0
+    for r in range(2):
+        for t in range(cu[r], cu[r + 1]):
+            n = kv[r] - (cu[r + 1] - t) + 1
+            for a in range(8):
+                k, v = vals[r][a // 4][0][:n], vals[r][a // 4][1][:n]
+                assert np.all(np.abs(got[t, a]) <= (1 + 2.0 ** -8 + 2.0 ** -11) * np.abs(v).max(0))
+                s = k @ q[t, a].astype(np.float64) * scale * np.log2(np.e)
+                two = np.sort(s)[-2:]
+                if two[1] - two[0] > 64 + 2.0 ** -17 * (np.abs(k) @ np.abs(q[t, a])).max() * scale:
+                    sure += 1
+                    w = v[np.argmax(s)]
+                    assert np.all(np.abs(got[t, a] - w) <= (2.0 ** -8 + 2.0 ** -11) * np.abs(w) + 2.0 ** -30), (t, a)
+    assert power < 20 or sure > 0.9 * 8 * len(q)
