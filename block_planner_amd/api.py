@@ -434,7 +434,7 @@ def kv_attention(q: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, tab
     (ht_kv_attention): bf16 [T, n_q, D].  max_q and max_kv (default: what the
     table can hold) are the largest lengths the caller knows of; scale is
     1 / sqrt(D) by default; window > 0 keeps each row to its last `window`
-    tokens."""
+    tokens.  Rows of no request (from cu_q[R] on) give zeros."""
     if stream is not None:
         with _using(stream):
             return kv_attention(q, codes, scales, table, cu_q, kv_len, max_q, max_kv, scale, causal, window, out, ws)

@@ -60,7 +60,7 @@ struct AttnArgs {
     int64_t dec_rows, prompt_at;
     int32_t dec_per_request;
     int64_t ldq, hsq, ldo, hso, ldt, P;
-    int32_t T, n_q, n_heads, group, n_pages, causal;
+    int32_t T, R, n_q, n_heads, group, n_pages, causal;
     int32_t splits, split_pages;     // of the decode kernel's requests
     int32_t psplits, psplit_pages;   // of the prompt kernel's
     int32_t prompt_from;             // columns from which a request is the prompt kernel's
@@ -108,6 +108,25 @@ __device__ __forceinline__ void row_range(const AttnArgs &a, const Request &q, i
     const int64_t pos = int64_t(q.kv) - q.rows + i;
     hi = a.causal ? int(max(int64_t(0), min(int64_t(q.kv), pos + 1))) : q.kv;
     lo = a.window > 0 ? int(min(int64_t(q.kv), max(int64_t(0), pos + 1 - a.window))) : 0;
+}
+
+// Zeros for the rows of no request: those before the first request's by its
+// workgroups, those past the last one's (a batch padded to a fixed number of rows)
+// by the last one's, which know the border from their own lengths.
+template <int D>
+__device__ __forceinline__ void clear_rows(const AttnArgs &a, const Request &rq, int r, int head) {
+    if (r != 0 && r != a.R - 1) return;
+    const int32_t before = r == 0 ? rq.row0 : 0, last = r == a.R - 1 ? rq.row0 + rq.rows : a.T;
+    if (before == 0 && last == a.T) return;
+    const int64_t per = int64_t(a.n_q) * (D / 8), n = (before + int64_t(a.T - last)) * per;
+    const int64_t wg = (int64_t(blockIdx.z) * gridDim.y + blockIdx.y) * a.n_heads + head;
+    const int64_t step = int64_t(gridDim.z) * gridDim.y * a.n_heads * blockDim.x;
+    for (int64_t i = wg * blockDim.x + threadIdx.x; i < n; i += step) {
+        int64_t row = i / per;
+        const int64_t in = i - row * per, h = in / (D / 8), d = in % (D / 8) * 8;
+        if (row >= before) row += last - before;
+        *reinterpret_cast<uint4 *>(a.out + row * a.ldo + h * a.hso + d) = uint4{0, 0, 0, 0};
+    }
 }
 
 // Eight codes as fp16, exactly: a byte c + 128 under the exponent of 1024 is 1152 + c.
@@ -180,6 +199,7 @@ __global__ __launch_bounds__(kAttnThreads) void attn_decode_kernel(AttnArgs a) {
     const int r = int(blockIdx.x) / a.n_heads, head = int(blockIdx.x) % a.n_heads;
     const Request rq = load_request(a, r);
     const int split = int(blockIdx.y);
+    clear_rows<D>(a, rq, r, head);
     if (rq.rows == 0 || rq.prompt || split >= rq.splits) return;
     const int pa = rq.p0 + split * rq.split_pages;
     const int pb = split == rq.splits - 1 ? rq.p1 : min(rq.p1, pa + rq.split_pages);
@@ -405,6 +425,7 @@ __global__ __launch_bounds__(64 * NW, DC <= 2 ? 2 : 1) void attn_prompt_kernel(A
     const int r = int(blockIdx.x) / a.n_heads, head = int(blockIdx.x) % a.n_heads;
     const Request rq = load_request(a, r);
     const int split = int(blockIdx.y);
+    if (a.prompt_from == 0) clear_rows<D>(a, rq, r, head);   // no decode kernel runs beside this one
     if (rq.rows == 0 || !rq.prompt || split >= rq.splits) return;
     const int pa = rq.p0 + split * rq.split_pages;
     const int pb = split == rq.splits - 1 ? rq.p1 : min(rq.p1, pa + rq.split_pages);
@@ -949,6 +970,7 @@ extern "C" ht_status ht_kv_attention(const uint16_t *q, int64_t ldq, int64_t hsq
     a.prompt_at = ps.dec_total;
     a.ldq = ldq; a.hsq = hsq; a.ldo = ldo; a.hso = hso; a.ldt = ldt; a.P = P;
     a.T = int32_t(T);
+    a.R = int32_t(R);
     a.n_q = n_q;
     a.n_heads = cache->n_heads;
     a.group = n_q / cache->n_heads;

@@ -564,7 +564,8 @@ ht_status ht_kv_write(const void *k, int64_t ldk, int64_t hsk, int32_t kt, const
  *   out[t, a] = sum_j softmax_j(scale * q[t, a] . K_j) V_j
  * over the tokens j of row t's request with j < kv_len, j <= pos (when causal)
  * and j > pos - window (when window > 0), pos = kv_len - q_len + (row in its
- * request); a row that sees no token gives zeros.  Query head a reads KV head
+ * request); a row that sees no token gives zeros, and so does a row of no
+ * request (before cu_q[0] or from cu_q[R] on).  Query head a reads KV head
  * a / (n_q / n_heads).  A table entry outside the cache hides its page.
  *   q         bf16 [T][n_q][D], rows ldq and heads hsq elements apart;
  *   table, P, ldt, cu_q, kv_len   as ht_kv_plan gives them (kv_out), lengths

@@ -49,3 +49,28 @@ def test_scores_of_any_size(side, power):
                     w = v[np.argmax(s)]
                     assert np.all(np.abs(got[t, a] - w) <= (2.0 ** -8 + 2.0 ** -11) * np.abs(w) + 2.0 ** -30), (t, a)
     assert power < 20 or sure > 0.9 * 8 * len(q)
+
+
+@pytest.mark.parametrize("n_q,H,D", [(8, 2, 64), (2, 2, 192)])
+@pytest.mark.parametrize("q_len,hint", [([1, 2], {}), ([40], dict(max_kv=10 ** 6)), ([40, 1, 30], dict(max_kv=40000)),
+                                        ([0, 0], {})])
+@pytest.mark.parametrize("before,after", [(0, 5), (3, 0), (2, 700)])
+def test_rows_of_no_request_are_zero(n_q, H, D, q_len, hint, before, after):
+    """A batch padded to a fixed number of rows (and one that starts late): zeros
+    there, in the output's own buffer too, and nothing else of it is touched."""
+    rng, q, codes, scales, table, cu, kv = make(3, q_len, [300, 70, 90][:len(q_len)], n_q, H, D)
+    clean = run(q, codes, scales, table, cu, kv, **hint)
+    n, T = len(q), before + len(q) + after
+    wide = bf16(rng.normal(size=(T, n_q, D)).astype(np.float32))
+    wide[before:before + n] = q
+    wide[0], wide[-1] = (np.nan if before else wide[0]), (np.nan if after else wide[-1])
+    buf = torch.full((T + 2, n_q + 3, D + 8), 7.0, dtype=torch.bfloat16, device="cuda")
+    out = buf[1:-1, 2:-1, :D]
+    hint = dict(max_q=int(max(q_len)), **hint)
+    got = run(wide, codes, scales, table, cu + np.int32(before), kv, out=out, **hint)
+    assert got.data_ptr() == out.data_ptr()
+    assert torch.equal(out[before:before + n], clean)
+    assert torch.all(out[:before] == 0) and torch.all(out[before + n:] == 0)
+    out.fill_(7.0)
+    assert torch.all(buf == 7)
+    assert torch.all(run(wide, codes, scales, table, cu + np.int32(before), kv, **hint)[before + n:] == 0)
