@@ -155,20 +155,25 @@ __device__ __forceinline__ float max_halves(float v) {
     return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
 }
 
-// 16 elements of a row of q as int8 planes hi, lo with n = rne(x 2^(14-E)) = 256 hi + lo.
-__device__ __forceinline__ void encode16(const uint16_t *x, float f, i32x4 &hi, i32x4 &lo) {
+// 16 elements of a row of q as three int8 planes with n = rne(x 2^(22-E)) =
+// 65536 p[0] + 256 p[1] + p[2]: exact for a bf16 entry of 2^-15 of the row's largest
+// or more.  (Two planes lose the small channels beside a large one: one channel
+// 200 times the rest left outputs off by twice their bound, 5000 times by seven.)
+__device__ __forceinline__ void encode16(const uint16_t *x, float f, i32x4 *p) {
 #pragma unroll
     for (int w = 0; w < 4; ++w) {
-        uint32_t h = 0, l = 0;
+        uint32_t a = 0, b = 0, c = 0;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const int n = int(rintf(__uint_as_float(uint32_t(x[4 * w + j]) << 16) * f));
-            const int nh = (n + 128) >> 8, nl = n - (nh << 8);
-            h |= (uint32_t(nh) & 0xFFu) << (8 * j);
-            l |= (uint32_t(nl) & 0xFFu) << (8 * j);
+            const int nb = (n + 128) >> 8, na = (nb + 128) >> 8;
+            a |= (uint32_t(na) & 0xFFu) << (8 * j);
+            b |= (uint32_t(nb) & 0xFFu) << (8 * j);   // nb - 256 na, modulo 256
+            c |= (uint32_t(n) & 0xFFu) << (8 * j);
         }
-        hi[w] = int(h);
-        lo[w] = int(l);
+        p[0][w] = int(a);
+        p[1][w] = int(b);
+        p[2][w] = int(c);
     }
 }
 
@@ -177,7 +182,7 @@ __device__ __forceinline__ void encode16(const uint16_t *x, float f, i32x4 &hi, 
 // a running maximum and sum of its own, joined through LDS at the end.
 //
 // Codes go from HBM straight into the operands of the MFMAs, which is what the
-// cache's layout is for: K as int8 against q in two int8 planes (exact int32
+// cache's layout is for: K as int8 against q in three int8 planes (exact int32
 // sums; converting K to fp16 would cost 5 vector operations per 4 codes), V to
 // fp16 in registers.  The accumulator of S^T (16 tokens x 16 columns) holds 4
 // tokens of a column per lane, and V's order of tokens makes two such blocks
@@ -191,7 +196,7 @@ __device__ __forceinline__ void encode16(const uint16_t *x, float f, i32x4 &hi, 
 // -> 57 us, 3 x 120k tokens 137 -> 126; with a second tile, which finds the
 // codes in the L2 without the hint, 16 x 7 rows over 3000 tokens 59 -> 65.
 template <int DC, bool ONCE>
-__global__ __launch_bounds__(kAttnThreads) void attn_decode_kernel(AttnArgs a) {
+__global__ __launch_bounds__(kAttnThreads, DC <= 2 ? 2 : 1) void attn_decode_kernel(AttnArgs a) {
     constexpr int D = 64 * DC, NE = D / 16;
     __shared__ float s_o[kWaves][16][D + 4];
     __shared__ float s_m[kWaves][16], s_l[kWaves][16];
@@ -217,16 +222,16 @@ __global__ __launch_bounds__(kAttnThreads) void attn_decode_kernel(AttnArgs a) {
         row_range(a, rq, qi, lo, hi);
         if (!live) hi = lo = 0;
         // q's row as int8 planes in registers
-        i32x4 qh[DC], ql[DC];
+        i32x4 qp[DC][3];
         float qs;
         {
-            const uint16_t *qp = a.q + int64_t(t) * a.ldq + int64_t(hq) * a.hsq + g * 16;
+            const uint16_t *qx = a.q + int64_t(t) * a.ldq + int64_t(hq) * a.hsq + g * 16;
             union { uint4 u[2]; uint16_t h[16]; } x[DC];
             uint32_t top = 0;
 #pragma unroll
             for (int j = 0; j < DC; ++j) {
-                x[j].u[0] = *reinterpret_cast<const uint4 *>(qp + 64 * j);
-                x[j].u[1] = *reinterpret_cast<const uint4 *>(qp + 64 * j + 8);
+                x[j].u[0] = *reinterpret_cast<const uint4 *>(qx + 64 * j);
+                x[j].u[1] = *reinterpret_cast<const uint4 *>(qx + 64 * j + 8);
 #pragma unroll
                 for (int i = 0; i < 16; ++i) top = max(top, uint32_t(x[j].h[i]) & 0x7FFFu);
             }
@@ -234,16 +239,16 @@ __global__ __launch_bounds__(kAttnThreads) void attn_decode_kernel(AttnArgs a) {
             top = max(top, uint32_t(__shfl_xor(int(top), 32)));
             const bool bad = top >= 0x7F80u;
             const int e = max(int(top >> 7) - 126, -100);
-            const float f = bad ? 0.f : pow2f(14 - e) * a.sign;
+            const float f = bad ? 0.f : pow2f(22 - e) * a.sign;
 #pragma unroll
             for (int j = 0; j < DC; ++j) {
                 if (bad) {
-                    qh[j] = ql[j] = i32x4{0, 0, 0, 0};
+                    qp[j][0] = qp[j][1] = qp[j][2] = i32x4{0, 0, 0, 0};
                 } else {
-                    encode16(x[j].h, f, qh[j], ql[j]);
+                    encode16(x[j].h, f, qp[j]);
                 }
             }
-            qs = bad ? __uint_as_float(0x7FC00000u) : pow2f(e - 14) * a.scale_log2;
+            qs = bad ? __uint_as_float(0x7FC00000u) : pow2f(e - 22) * a.scale_log2;
         }
         // pages any live column of the tile sees
         int lo_min = live ? lo : INT32_MAX, hi_max = hi, lo_max = live ? lo : 0, hi_min = live ? hi : INT32_MAX;
@@ -304,14 +309,17 @@ __global__ __launch_bounds__(kAttnThreads) void attn_decode_kernel(AttnArgs a) {
                 float top = -INFINITY;
 #pragma unroll
                 for (int b = 0; b < 4; ++b) {
-                    i32x4 sh = {0, 0, 0, 0}, sl = {0, 0, 0, 0};
+                    i32x4 s0 = {0, 0, 0, 0}, s1 = s0, s2 = s0;
 #pragma unroll
                     for (int j = 0; j < DC; ++j) {
-                        sh = __builtin_amdgcn_mfma_i32_16x16x64_i8(kf[b][j], qh[j], sh, 0, 0, 0);
-                        sl = __builtin_amdgcn_mfma_i32_16x16x64_i8(kf[b][j], ql[j], sl, 0, 0, 0);
+                        s0 = __builtin_amdgcn_mfma_i32_16x16x64_i8(kf[b][j], qp[j][0], s0, 0, 0, 0);
+                        s1 = __builtin_amdgcn_mfma_i32_16x16x64_i8(kf[b][j], qp[j][1], s1, 0, 0, 0);
+                        s2 = __builtin_amdgcn_mfma_i32_16x16x64_i8(kf[b][j], qp[j][2], s2, 0, 0, 0);
                     }
+                    // |s1| <= 256 x 128 x 128 = 2^22: 256 s1 + s2 fits 32 bits
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) y[b][i] = float(sh[i] * 256 + sl[i]) * f + ef;
+                    for (int i = 0; i < 4; ++i)
+                        y[b][i] = fmaf(float(s0[i]), 0x1p16f, float(s1[i] * 256 + s2[i])) * f + ef;
                 }
                 if (at + 1 < count) load_k(next);
                 const int j0 = p * kPage;

@@ -575,14 +575,16 @@ ht_status ht_kv_write(const void *k, int64_t ldk, int64_t hsk, int32_t kt, const
  *             does not depend on them, its rounding does (below);
  *   out       bf16 [T][n_q][D], rows ldo and heads hso elements apart.
  * Requests of few columns (rows x heads per KV head: answers, drafts) and short
- * calls (by R, max_q and max_kv): q.K on
- * the int8 matrix cores with each row of q as (256 hi + lo) 2^(E-14), 2^(E-1) <=
- * max |q| < 2^E, int8 planes hi and lo (off by at most 2^-15 of the row's largest
- * entry) and exact int32 sums.  Others: on the fp16 matrix cores with q 2^(14-E),
- * exact but for entries under 2^-28 of the largest, and fp32 sums.  The weights
- * go to V as fp16 relative to the row's largest contribution; sums in fp32.  A
- * row of q holding Inf or NaN gives NaN.  Bitwise reproducible.  T times the heads
- * per KV head is at most 2^30, R times n_heads 2^22.
+ * calls (by R, max_q and max_kv): q.K on the int8 matrix cores with each row of
+ * q as n 2^(E-22), n = rne(x 2^(22-E)), 2^(E-1) <= max |q| < 2^E, in three int8
+ * planes (exact but for entries under 2^-14 of the largest, which are off by at
+ * most 2^-22 of it) and exact int32 sums.  Others: on the fp16 matrix cores with
+ * q 2^(14-E), exact but for entries under 2^-28 of the largest, and fp32 sums.
+ * The weights go to V as fp16 relative to the row's largest contribution; sums in
+ * fp32.  Scores may have any size that fp32 holds (from 2^24 on in units of log
+ * 2, where it no longer tells a whole unit, the largest take all weight).  A row
+ * of q holding Inf or NaN gives NaN.  Bitwise reproducible.  T times the heads per
+ * KV head is at most 2^30, R times n_heads 2^22.
  *   ws        ht_kv_attention_workspace bytes: partial results of split rows. */
 ht_status ht_kv_attention_workspace(const ht_kv_cache *cache, int64_t T, int64_t R, int32_t n_q, int64_t max_q,
                                     int64_t max_kv, int64_t window, size_t *bytes);

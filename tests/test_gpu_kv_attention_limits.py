@@ -74,3 +74,51 @@ def test_rows_of_no_request_are_zero(n_q, H, D, q_len, hint, before, after):
     out.fill_(7.0)
     assert torch.all(buf == 7)
     assert torch.all(run(wide, codes, scales, table, cu + np.int32(before), kv, **hint)[before + n:] == 0)
+
+
+def attention_bound(q, codes, scales, table, cu, kv, scale, want):
+    """What a result may be off by, [T, n_q, D], with q carried to 2^-22 of its
+    row's largest entry: half a bf16 step (2^-8), fp16 weights (2^-11) and fp32
+    exponents and sums, the weights' errors carried through the weighted mean
+    (a weight off by a factor 1 + e moves the result by e (mean |v| + |out|))."""
+    D, H, tol = q.shape[2], codes.shape[1], np.zeros(want.shape)
+    index = ref.block_index(D)
+    for r in range(len(kv)):
+        pages = table[r, :-(-kv[r] // 64)]
+        for h in range(H):
+            k, v = ((codes[pages, h, i][:, index[i].reshape(-1)].astype(np.float64)
+                     * scales[pages, h, i].astype(np.float64)[:, None]).reshape(-1, D)[:kv[r]] for i in (0, 1))
+            for t in range(cu[r], cu[r + 1]):
+                n = kv[r] - (cu[r + 1] - t) + 1
+                for a in range(h * (q.shape[1] // H), (h + 1) * (q.shape[1] // H)):
+                    x = q[t, a].astype(np.float64)
+                    s = k[:n] @ x * scale
+                    p = np.exp(s - s.max())
+                    p /= p.sum()
+                    off = abs(scale) * 2.0 ** -22 * np.abs(x).max() * np.abs(k[:n]).sum(1).max()
+                    off += 2.0 ** -24 * (64 + 4 * np.abs(s).max() + 4 * abs(scale) * (np.abs(k[:n]) @ np.abs(x)).max())
+                    size = p @ np.abs(v[:n]) + np.abs(want[t, a])
+                    tol[t, a] = 2.0 ** -8 * np.abs(want[t, a]) + (2.0 ** -11 + off) * (1 + 2.0 ** -8) * size + 2.0 ** -126
+    return tol
+
+
+@pytest.mark.parametrize("side", SIDES)
+@pytest.mark.parametrize("n_q,H,D", [(8, 2, 64), (4, 2, 128), (2, 2, 192), (4, 1, 256)])
+@pytest.mark.parametrize("outlier", [30.0, 200.0, 5000.0])
+def test_one_channel_of_q_far_above_the_rest(side, n_q, H, D, outlier):
+    """The other channels of q still count with all their bits: the keys of the
+    large channel differ little from token to token, so that the rest decides."""
+    q_len, hint = SIDES[side]
+    rng, q, codes, scales, table, cu, kv = make(int(outlier) + D, q_len, [500, 1100], n_q, H, D)
+    index = ref.block_index(D)[0]
+    q[:, :, 5] = outlier * np.sign(q[:, :, 5])
+    q = bf16(q)
+    # every page's keys of that channel: the same small value
+    codes[:, :, 0, index[:, 5]] = 4
+    scales[:, :, 0] = 2.0 ** -7
+    scale = 0.5
+    want, _ = ref.attention(q, codes, scales, table, cu, kv, scale)
+    tol = attention_bound(q, codes, scales, table, cu, kv, scale, want)
+    got = run(q, codes, scales, table, cu, kv, scale=scale, **hint).double().cpu().numpy()
+    err = np.abs(got - want)
+    assert np.all(err <= tol), f"{np.max(err / tol)} times the bound"
