@@ -34,7 +34,8 @@ EXPORTS = ("ht_status_string", "ht_plan_params_default", "ht_plan", "ht_plan_cou
            "ht_linear_backward_workspace", "ht_linear_backward_data", "ht_linear_backward_weight",
            "ht_mlp_workspace", "ht_workspace_init", "ht_mlp_forward",
            "ht_kv_cache_bytes", "ht_kv_plan", "ht_kv_release", "ht_qk_norm_rope", "ht_qk_norm_rope_workspace",
-           "ht_qk_norm_rope_backward", "ht_kv_write", "ht_kv_attention_workspace", "ht_kv_attention")
+           "ht_qk_norm_rope_backward", "ht_kv_write", "ht_kv_attention_workspace", "ht_kv_attention_kernels",
+           "ht_kv_attention")
 
 
 class HTError(RuntimeError):
@@ -151,6 +152,8 @@ def load() -> ctypes.CDLL:
     lib.ht_kv_write.argtypes = [P, I64, I64, I32, P, I64, I64, I32, I64, P, PC, P]
     lib.ht_kv_attention_workspace.restype = St
     lib.ht_kv_attention_workspace.argtypes = [PC, I64, I64, I32, I64, I64, I64, PSz]
+    lib.ht_kv_attention_kernels.restype = St
+    lib.ht_kv_attention_kernels.argtypes = [PC, I64, I64, I32, I64, I64, I64, ctypes.POINTER(I32)]
     lib.ht_kv_attention.restype = St
     lib.ht_kv_attention.argtypes = [P, I64, I64, I64, I32, PC, P, I64, I64, P, P, I64, I64, I64, F, I32, I64, P, I64,
                                     I64, P, Sz, P]
@@ -429,6 +432,15 @@ def ht_kv_attention_workspace(desc: KVCacheDesc, T: int, R: int, n_q: int, max_q
     _check("ht_kv_attention_workspace", load().ht_kv_attention_workspace(ctypes.byref(desc), T, R, n_q, max_q, max_kv,
                                                                          window, ctypes.byref(out)))
     return out.value
+
+
+def ht_kv_attention_kernels(desc: KVCacheDesc, T: int, R: int, n_q: int, max_q: int, max_kv: int,
+                            window: int = 0) -> tuple:
+    """(splits of the kernel for few columns, of the kernel for prompts, its wavefronts per workgroup), 0: not run."""
+    info = (ctypes.c_int32 * 3)()
+    _check("ht_kv_attention_kernels", load().ht_kv_attention_kernels(ctypes.byref(desc), T, R, n_q, max_q, max_kv,
+                                                                     window, info))
+    return tuple(info)
 
 
 def ht_kv_attention(q, desc: KVCacheDesc, table, cu_q, kv_len, max_q: int, max_kv: int, scale: float, causal: bool,

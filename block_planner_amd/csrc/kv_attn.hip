@@ -944,6 +944,19 @@ extern "C" ht_status ht_kv_attention_workspace(const ht_kv_cache *cache, int64_t
     return HT_OK;
 }
 
+extern "C" ht_status ht_kv_attention_kernels(const ht_kv_cache *cache, int64_t T, int64_t R, int32_t n_q, int64_t max_q,
+                                             int64_t max_kv, int64_t window, int32_t *info) {
+    if (!info) return HT_EINVAL;
+    const ht_status st = check_attn(cache, T, R, n_q, max_q, max_kv);
+    if (st != HT_OK) return st;
+    if (window < 0) return HT_ESHAPE;
+    const AttnShape sh = attn_shape(T, R, cache->n_heads, cache->head_dim, n_q, max_q, max_kv, window);
+    info[0] = sh.decode ? sh.splits : 0;
+    info[1] = sh.prompt ? sh.psplits : 0;
+    info[2] = sh.prompt ? sh.waves : 0;
+    return HT_OK;
+}
+
 extern "C" ht_status ht_kv_attention(const uint16_t *q, int64_t ldq, int64_t hsq, int64_t T, int32_t n_q,
                                      const ht_kv_cache *cache, const int32_t *table, int64_t P, int64_t ldt,
                                      const int32_t *cu_q, const int32_t *kv_len, int64_t R, int64_t max_q,

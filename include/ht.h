@@ -594,6 +594,15 @@ ht_status ht_kv_attention(const uint16_t *q, int64_t ldq, int64_t hsq, int64_t T
                           int64_t window, uint16_t *out, int64_t ldo, int64_t hso, void *ws, size_t ws_bytes,
                           ht_stream stream);
 
+/* ht_kv_attention_kernels -- what a call of these sizes runs (host only), and so
+ * which arithmetic a request gets:
+ *   info      int32 [3] out: the most parts a request of few columns is split into
+ *             (0: no kernel for few columns is launched), the same of the others'
+ *             kernel, and the wavefronts in a workgroup of that one (4 or 8).
+ * Where both run, a request goes by its own columns: up to 32 is few. */
+ht_status ht_kv_attention_kernels(const ht_kv_cache *cache, int64_t T, int64_t R, int32_t n_q, int64_t max_q,
+                                  int64_t max_kv, int64_t window, int32_t *info);
+
 #ifdef __cplusplus
 }
 #endif

@@ -256,3 +256,20 @@ def test_reference_attention_closed_forms():
     np.testing.assert_allclose(out[0, 0], v[:68].mean(0), rtol=1e-12)
     out, _ = ref.attention(q, codes, scales, np.array([[1, 0]]), [0, 3], [70], 0.125, window=1)
     np.testing.assert_allclose(out[1, 0], v[68], rtol=1e-12)
+
+
+def test_attention_kernels_of_a_call():
+    """Which kernels a call runs, by its sizes: the query's own checks, and one
+    call of each kind."""
+    d = B.KVCacheDesc(A, A, 1000, 8, 128)
+    info = lambda *a, **kw: B.ht_kv_attention_kernels(d, *a, **kw)  # noqa: E731
+    assert info(1, 1, 32, 1, 64) == (1, 0, 0) and info(0, 1, 32, 0, 0) == (1, 0, 0)
+    assert info(64, 64, 32, 1, 8192)[0] > 1 and info(64, 64, 32, 1, 8192)[1:] == (0, 0)
+    assert info(8192, 1, 32, 8192, 8192) == (0, 1, 8)
+    assert info(8208, 17, 32, 8192, 8192)[1:] == (1, 8) and info(8208, 17, 32, 8192, 8192)[0] > 1
+    assert info(600, 1, 32, 600, 30000)[0] == 0 and info(600, 1, 32, 600, 30000)[1] > 1
+    args = dict(cache=ctypes.byref(d), T=4, R=2, n_q=8, max_q=2, max_kv=64, window=0, info=(ctypes.c_int32 * 3)())
+    assert call("ht_kv_attention_kernels", args) == OK
+    for change, code in ((dict(info=None), EINVAL), (dict(cache=None), EINVAL), (dict(T=-1), ESHAPE), (dict(R=0), ESHAPE),
+                         (dict(n_q=7), ESHAPE), (dict(max_q=-1), ESHAPE), (dict(window=-1), ESHAPE)):
+        assert call("ht_kv_attention_kernels", args, **change) == code
