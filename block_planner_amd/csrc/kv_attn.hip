@@ -880,6 +880,9 @@ ht_status check_attn(const ht_kv_cache *c, int64_t T, int64_t R, int32_t n_q, in
     return HT_OK;
 }
 
+// A window of 2^31 tokens or more keeps every token (and would overflow the sums it goes into): none.
+int64_t clamp_window(int64_t window) { return window >= (int64_t(1) << 31) ? 0 : window; }
+
 template <int DC>
 ht_status run_attn(const AttnArgs &a, const AttnShape &sh, int64_t R, int64_t max_q, hipStream_t s) {
     const uint32_t x = uint32_t(R * a.n_heads);
@@ -938,7 +941,7 @@ extern "C" ht_status ht_kv_attention_workspace(const ht_kv_cache *cache, int64_t
     const ht_status st = check_attn(cache, T, R, n_q, max_q, max_kv);
     if (st != HT_OK) return st;
     if (window < 0) return HT_ESHAPE;
-    const AttnShape sh = attn_shape(T, R, cache->n_heads, cache->head_dim, n_q, max_q, max_kv, window);
+    const AttnShape sh = attn_shape(T, R, cache->n_heads, cache->head_dim, n_q, max_q, max_kv, clamp_window(window));
     const size_t rows = size_t(partial_shape(sh, T, R, n_q, cache->n_heads).total);
     *bytes = size_t(align256(rows * 4u)) + rows * size_t(cache->head_dim) * 4u;
     return HT_OK;
@@ -965,6 +968,7 @@ extern "C" ht_status ht_kv_attention(const uint16_t *q, int64_t ldq, int64_t hsq
     ht_status st = check_attn(cache, T, R, n_q, max_q, max_kv);
     if (st != HT_OK) return st;
     if (P <= 0 || P > (int64_t(1) << 24) || ldt < P || window < 0) return HT_ESHAPE;
+    window = clamp_window(window);
     if (!(scale == scale) || scale - scale != 0.f) return HT_EINVAL;
     if (T == 0) return HT_OK;
     if ((st = check_rows(q, ldq, hsq, n_q, cache->head_dim, 2)) != HT_OK) return st;

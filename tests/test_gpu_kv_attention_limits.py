@@ -122,3 +122,14 @@ def test_one_channel_of_q_far_above_the_rest(side, n_q, H, D, outlier):
     got = run(q, codes, scales, table, cu, kv, scale=scale, **hint).double().cpu().numpy()
     err = np.abs(got - want)
     assert np.all(err <= tol), f"{np.max(err / tol)} times the bound"
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("side", SIDES)
+def test_a_window_past_everything_is_none(side, causal):
+    """Up to the largest number, also for requests of more rows than tokens."""
+    q_len, hint = SIDES[side]
+    args = make(8, q_len, [2, 300], 4, 2, 64)[1:]
+    want = check(*args, causal=causal, **hint)
+    for window in (2 ** 31 - 1, 2 ** 31, 2 ** 62, 2 ** 63 - 1):
+        assert torch.equal(run(*args, causal=causal, window=window, **hint), want)

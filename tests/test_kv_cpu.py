@@ -273,3 +273,15 @@ def test_attention_kernels_of_a_call():
     for change, code in ((dict(info=None), EINVAL), (dict(cache=None), EINVAL), (dict(T=-1), ESHAPE), (dict(R=0), ESHAPE),
                          (dict(n_q=7), ESHAPE), (dict(max_q=-1), ESHAPE), (dict(window=-1), ESHAPE)):
         assert call("ht_kv_attention_kernels", args, **change) == code
+
+
+@pytest.mark.parametrize("window", [2 ** 40, 2 ** 62, 2 ** 63 - 1])
+def test_attention_windows_wider_than_any_request(window):
+    """A window past every length is no window: the same kernels and workspace,
+    up to the largest number the argument holds."""
+    d = B.KVCacheDesc(A, A, 1000, 8, 128)
+    for T, R, max_q, max_kv in ((1, 1, 1, 100000), (64, 64, 1, 8192), (600, 1, 600, 30000), (8208, 17, 8192, 131072),
+                                (5, 1, 2 ** 30, 2 ** 30)):
+        sizes = (T, R, 32, max_q, max_kv)
+        assert B.ht_kv_attention_kernels(d, *sizes, window) == B.ht_kv_attention_kernels(d, *sizes, 0)
+        assert B.ht_kv_attention_workspace(d, *sizes, window) == B.ht_kv_attention_workspace(d, *sizes, 0)
