@@ -953,7 +953,7 @@ extern "C" ht_status ht_kv_attention_kernels(const ht_kv_cache *cache, int64_t T
     const ht_status st = check_attn(cache, T, R, n_q, max_q, max_kv);
     if (st != HT_OK) return st;
     if (window < 0) return HT_ESHAPE;
-    const AttnShape sh = attn_shape(T, R, cache->n_heads, cache->head_dim, n_q, max_q, max_kv, window);
+    const AttnShape sh = attn_shape(T, R, cache->n_heads, cache->head_dim, n_q, max_q, max_kv, clamp_window(window));
     info[0] = sh.decode ? sh.splits : 0;
     info[1] = sh.prompt ? sh.psplits : 0;
     info[2] = sh.prompt ? sh.waves : 0;
