@@ -305,6 +305,13 @@ class HyperAttention(torch.nn.Module):
         one = lambda: torch.nn.Parameter(torch.ones(head_dim, device=dev)) if qk_norm else None  # noqa: E731
         self.q_weight, self.k_weight = one(), one()
 
+    def _apply(self, fn, recurse=True):
+        # casts of the module move the frequencies and leave them fp64: rounded ones lose the phase of far positions
+        freq = self.inv_freq
+        super()._apply(fn, recurse)
+        self.inv_freq = freq.to(self.inv_freq.device)
+        return self
+
     @torch.no_grad()
     def forward(self, x: torch.Tensor, pool: KVPool, layer: int, step: api.KVStep) -> torch.Tensor:
         y = self.qkv(x)
@@ -313,8 +320,9 @@ class HyperAttention(torch.nn.Module):
             raise ValueError(f"qkv: expected [rows, {(n + 2 * m) * d}], got {tuple(y.shape)}")
         y = y.unflatten(1, (n + 2 * m, d))
         codes, scales = pool.caches[layer]
-        q, k = api.qk_norm_rope(y[:, :n], y[:, n:n + m], step.positions, self.inv_freq, self.q_weight, self.k_weight,
-                                self.eps, self.interleaved, out_dtype=torch.bfloat16)
+        wq, wk = (None, None) if self.q_weight is None else (self.q_weight.float(), self.k_weight.float())
+        q, k = api.qk_norm_rope(y[:, :n], y[:, n:n + m], step.positions, self.inv_freq, wq, wk, self.eps,
+                                self.interleaved, out_dtype=torch.bfloat16)
         api.kv_write(k, y[:, n + m:], step.slots, codes, scales)
         o = api.kv_attention(q, codes, scales, pool.table, step.cu_q, step.kv_len, pool.max_q, max_kv=pool.max_kv,
                              window=self.window)

@@ -1,0 +1,56 @@
+"""HyperAttention as a module among others: casts, gradients."""
+import pytest
+import torch
+
+from block_planner_amd import nn as htnn
+
+pytestmark = pytest.mark.gpu
+
+
+def dev():
+    return torch.device("cuda:0")
+
+
+class Same(torch.nn.Module):
+    def forward(self, o):
+        return o.float()
+
+
+def layer(seed=3, **kw):
+    torch.manual_seed(seed)
+    lin = torch.nn.Linear(128, (8 + 2 * 2) * 64, bias=False, device=dev())
+    return htnn.HyperAttention(htnn.HyperLinear.from_linear(lin), Same(), 8, 2, 64, **kw)
+
+
+def step(att, x, q_len=(70, 3)):
+    pool = htnn.KVPool(1, 12, 2, 64, len(q_len), 6, dev())
+    with torch.no_grad():
+        return att(x, pool, 0, pool.plan(list(q_len)))
+
+
+@pytest.mark.parametrize("cast", ["float", "half", "bfloat16", "to", "double"])
+@pytest.mark.parametrize("qk_norm", [True, False])
+def test_casts_of_the_module(cast, qk_norm):
+    """The frequencies stay in 64 bits (a cast would lose the phase of far
+    positions); the norm's weights are cast like any weight and used in 32 bits."""
+    x = torch.randn(73, 128, device=dev())
+    att = layer(qk_norm=qk_norm, base=500000.0)
+    if qk_norm:
+        with torch.no_grad():   # values that every type holds
+            att.q_weight.copy_(torch.randint(8, 24, (64,), device=dev()) / 16)
+            att.k_weight.copy_(torch.randint(8, 24, (64,), device=dev()) / 16)
+    want, freq = step(att, x), att.inv_freq.clone()
+    moved = torch.nn.Sequential(att)
+    moved = moved.to(torch.bfloat16) if cast == "to" else getattr(moved, cast)()
+    assert moved[0] is att and att.inv_freq.dtype == torch.float64 and torch.equal(att.inv_freq, freq)
+    assert torch.equal(step(att, x), want)
+
+
+def test_moves_of_the_module():
+    """To the host and back: the frequencies move, and are the same."""
+    att = layer()
+    freq = att.inv_freq.clone()
+    att.cpu()
+    assert att.inv_freq.device.type == "cpu" and torch.equal(att.inv_freq, freq.cpu())
+    att.to(dev())
+    assert att.inv_freq.is_cuda and torch.equal(att.inv_freq, freq)
