@@ -309,7 +309,8 @@ class HyperAttention(torch.nn.Module):
         # casts of the module move the frequencies and leave them fp64: rounded ones lose the phase of far positions
         freq = self.inv_freq
         super()._apply(fn, recurse)
-        self.inv_freq = freq.to(self.inv_freq.device)
+        if not freq.is_meta:
+            self.inv_freq = freq.to(self.inv_freq.device)
         return self
 
     @torch.no_grad()

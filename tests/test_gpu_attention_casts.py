@@ -54,3 +54,12 @@ def test_moves_of_the_module():
     assert att.inv_freq.device.type == "cpu" and torch.equal(att.inv_freq, freq.cpu())
     att.to(dev())
     assert att.inv_freq.is_cuda and torch.equal(att.inv_freq, freq)
+
+
+def test_a_module_made_without_memory():
+    """Moved from the meta device by to_empty, as any module."""
+    att = layer()
+    att.to("meta")
+    assert att.inv_freq.is_meta
+    att.to_empty(device=dev())
+    assert att.inv_freq.is_cuda and att.inv_freq.dtype == torch.float64
