@@ -289,7 +289,11 @@ class HyperAttention(torch.nn.Module):
     hidden to (n_heads + 2 n_kv_heads) * head_dim, out maps n_heads * head_dim
     back.  With qk_norm each head of q and k is normed with a weight; base (or
     inv_freq, fp64) sets the rotation; window > 0 limits every row to its last
-    `window` tokens."""
+    `window` tokens.
+
+    There is no backward pass through the cache: a call with gradients enabled
+    raises where x or a weight requires one (the norm's weights do not by
+    default; nn.qk_norm_rope trains them)."""
 
     def __init__(self, qkv: torch.nn.Module, out: torch.nn.Module, n_heads: int, n_kv_heads: int, head_dim: int,
                  base: float = 10000.0, inv_freq: torch.Tensor | None = None, qk_norm: bool = False, eps: float = 1e-6,
@@ -302,7 +306,7 @@ class HyperAttention(torch.nn.Module):
         self.n_heads, self.n_kv_heads, self.head_dim = int(n_heads), int(n_kv_heads), int(head_dim)
         self.eps, self.interleaved, self.window = float(eps), bool(interleaved), int(window)
         self.register_buffer("inv_freq", api.rope_inv_freq(head_dim, base, dev) if inv_freq is None else inv_freq)
-        one = lambda: torch.nn.Parameter(torch.ones(head_dim, device=dev)) if qk_norm else None  # noqa: E731
+        one = lambda: torch.nn.Parameter(torch.ones(head_dim, device=dev), False) if qk_norm else None  # noqa: E731
         self.q_weight, self.k_weight = one(), one()
 
     def _apply(self, fn, recurse=True):
@@ -313,8 +317,11 @@ class HyperAttention(torch.nn.Module):
             self.inv_freq = freq.to(self.inv_freq.device)
         return self
 
-    @torch.no_grad()
     def forward(self, x: torch.Tensor, pool: KVPool, layer: int, step: api.KVStep) -> torch.Tensor:
+        if torch.is_grad_enabled():
+            if x.requires_grad or any(p.requires_grad for p in self.parameters()):
+                raise RuntimeError("HyperAttention has no backward pass through the cache: call it under torch.no_grad() "
+                                   "(x or a weight of the layer requires a gradient)")
         y = self.qkv(x)
         n, m, d = self.n_heads, self.n_kv_heads, self.head_dim
         if y.dim() != 2 or y.shape[1] != (n + 2 * m) * d:

@@ -63,3 +63,29 @@ def test_a_module_made_without_memory():
     assert att.inv_freq.is_meta
     att.to_empty(device=dev())
     assert att.inv_freq.is_cuda and att.inv_freq.dtype == torch.float64
+
+
+def test_gradients_are_refused():
+    """No backward pass goes through the cache: where something asks for
+    gradients the call raises, instead of returning an output that none reach.
+    Under no_grad, and where nothing asks, it runs."""
+    x = torch.randn(73, 128, device=dev())
+    pool = htnn.KVPool(1, 12, 2, 64, 2, 6, dev())
+    att = layer(qk_norm=True)
+    want = step(att, x)
+    assert torch.equal(att(x, pool, 0, pool.plan([70, 3])), want)   # the norm's weights do not ask by themselves
+    trained = layer(qk_norm=True)
+    trained.q_weight.requires_grad_(True)
+    lin = torch.nn.Linear(128, (8 + 2 * 2) * 64, bias=False, device=dev())
+    for a, y in ((att, x.clone().requires_grad_(True)), (trained, x),
+                 (htnn.HyperAttention(lin, Same(), 8, 2, 64), x),
+                 (htnn.HyperAttention(htnn.HyperLinear.from_linear(lin, inference_only=False), Same(), 8, 2, 64), x)):
+        with pytest.raises(RuntimeError, match="no_grad"):
+            a(y, pool, 0, pool.plan([1, 72]))
+        pool.release([True, True])
+        plan = pool.plan([70, 3])
+        with torch.no_grad():
+            out = a(y, pool, 0, plan)
+        assert not out.requires_grad
+        with torch.inference_mode():
+            assert torch.equal(a(y, pool, 0, plan), out)
