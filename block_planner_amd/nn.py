@@ -215,13 +215,16 @@ class _QKNormRopeFn(torch.autograd.Function):
         positions, inv_freq, *saved = ctx.saved_tensors
         dt, sq, sk = ctx.meta
         eps, interleaved = ctx.args
+        out = None
         if ctx.norm:
             q, k, wq, wk = saved
         else:
+            # the inputs are not read: the gradients' buffers stand for their shape and type
             q = torch.empty(sq, dtype=dt, device=dyq.device)
             k, wq, wk = None if sk is None else torch.empty(sk, dtype=dt, device=dyq.device), None, None
+            out = (q, k)
         dq, dk, dwq, dwk = api.qk_norm_rope_backward(dyq, dyk if k is not None else None, q, k, positions, inv_freq, wq,
-                                                     wk, eps, interleaved)
+                                                     wk, eps, interleaved, out)
         return dq, dk, dwq, dwk, None, None, None, None, None
 
 
