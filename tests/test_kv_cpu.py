@@ -285,3 +285,27 @@ def test_attention_windows_wider_than_any_request(window):
         sizes = (T, R, 32, max_q, max_kv)
         assert B.ht_kv_attention_kernels(d, *sizes, window) == B.ht_kv_attention_kernels(d, *sizes, 0)
         assert B.ht_kv_attention_workspace(d, *sizes, window) == B.ht_kv_attention_workspace(d, *sizes, 0)
+
+
+class On:
+    """What _on_gpu looks at of a tensor."""
+
+    def __init__(self, device):
+        self.device = device
+        self.is_cuda = device >= 0
+
+    def get_device(self):
+        return self.device
+
+
+def test_tensors_of_several_devices_are_refused(monkeypatch):
+    """The kernels run on the current device and get bare addresses: memory of
+    another GPU never reaches them."""
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    api._on_gpu(On(1), None, On(1))
+    api._on_gpu(None)
+    for tensors, match in (((On(1), On(0)), "one GPU"), ((On(0), On(1)), "one GPU"), ((On(0), On(0)), "current device"),
+                           ((On(1), On(-1)), "must be on the GPU"), ((On(-1), On(1)), "must be on the GPU")):
+        with pytest.raises(ValueError, match=match):
+            api._on_gpu(*tensors)
+    assert torch.empty(1, device="meta").get_device() < 0 and torch.empty(1).get_device() < 0
