@@ -172,8 +172,9 @@ def _ptr(t) -> int | None:
 def _stream(stream) -> int | None:
     if stream is None:
         import torch
-        # the handle of torch.cuda.current_stream(), without building its Python object (2 us a call)
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        # the handle without building the stream's Python object (2 us a call), where torch has that private lookup
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        return torch.cuda.current_stream().cuda_stream if raw is None else raw(torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream

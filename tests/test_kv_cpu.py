@@ -309,3 +309,18 @@ def test_tensors_of_several_devices_are_refused(monkeypatch):
         with pytest.raises(ValueError, match=match):
             api._on_gpu(*tensors)
     assert torch.empty(1, device="meta").get_device() < 0 and torch.empty(1).get_device() < 0
+
+
+def test_current_stream_without_torchs_private_lookup(monkeypatch):
+    """The current stream's handle comes from a private torch function where
+    there is one, and from the public one where there is not."""
+    class Stream:
+        cuda_stream = 0x1234
+
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda: Stream)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda device: 0x5678 + device, raising=False)
+    assert B._stream(None) == 0x5678
+    monkeypatch.delattr(torch._C, "_cuda_getCurrentRawStream")
+    assert B._stream(None) == 0x1234
+    assert B._stream(7) == 7 and B._stream(Stream) == 0x1234
