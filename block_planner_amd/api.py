@@ -296,7 +296,9 @@ class KVStep(NamedTuple):
 
 
 def kv_step(R: int, T: int, device) -> KVStep:
-    """Buffers for kv_plan's outputs, for reuse from step to step."""
+    """Buffers for kv_plan's outputs.  A step's lengths are inputs of the next
+    plan, which must not write over them (HT_EINVAL): two sets, used in turn,
+    serve any number of steps."""
     return KVStep(*(torch.empty(n, dtype=torch.int32, device=device) for n in (R + 1, T, T, R, R, 2)))
 
 
