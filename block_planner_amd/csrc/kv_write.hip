@@ -5,9 +5,9 @@
 //
 // Scaling by a power of two is exact, so a code has one rounding and does not
 // depend on the order of anything.  When appended rows raise E by d, older
-// codes become rne(code 2^-d): E only grows, so all such halvings of an entry
-// together add less than half a step of the final scale (1/4 + 1/8 + ...) to
-// the half step of its own rounding.
+// codes become rne(code 2^-d): E only grows, so of an entry's roundings the last
+// adds at most half a step of the final scale, the one before a quarter and so on
+// (the entry's own is the first of them): less than one step together.
 //
 // Bound by HBM for prompts (inputs in, one byte per entry out), by latency for
 // single tokens.  A run -- rows at consecutive slots of one page -- is the

@@ -461,8 +461,9 @@ ht_status ht_mlp_forward(const ht_packed_weight *const *layers, int32_t n_layers
  * at least) the scale is 2^(E-7) and code = clamp(rne(x 2^(7-E)), -127, 127);
  * +-Inf becomes +-127, NaN becomes 0.  Rows appended to a page that holds some
  * raise E when they need to: older codes become rne(code 2^(E_old - E_new)),
- * so an entry is off by less than one scale (half for its own rounding and
- * half at most for all later halvings together), or by one where clamped.
+ * so a finite entry is off by less than one scale: the last rounding adds half at
+ * most, those before (the entry's own, or its clamping, among them) a quarter, an
+ * eighth and so on of the final scale.
  * Scales must be initialised (zeros will do). */
 typedef struct {
     int8_t *codes;               /* 16-byte aligned */

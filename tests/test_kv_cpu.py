@@ -324,3 +324,26 @@ def test_current_stream_without_torchs_private_lookup(monkeypatch):
     monkeypatch.delattr(torch._C, "_cuda_getCurrentRawStream")
     assert B._stream(None) == 0x1234
     assert B._stream(7) == 7 and B._stream(Stream) == 0x1234
+
+
+def test_roundings_of_an_entry_stay_below_one_scale():
+    """Rows appended to a page raise its scale again and again: every entry is
+    off by less than one final scale, the halvings alone by more than half."""
+    rng = np.random.default_rng(4)
+    at = ref.block_index(64)[0]
+    most = halved = 0.0
+    for trial in range(40):
+        codes, scales = np.zeros((1, 1, 2, 4096), np.int8), np.zeros((1, 1, 2), np.float32)
+        rows = np.zeros((12, 1, 64), np.float32)
+        for t in range(12):
+            rows[t, 0] = rng.uniform(-1, 1, 64) * 2.0 ** t
+            rows[t, 0, 0] = 2.0 ** (t + rng.integers(0, 2)) * rng.choice([0.5, 0.75, 1 - 2.0 ** -20])
+            if t == 0:
+                rows[t, 0, 1:4] = [5 / 128, 21 / 128, 1 - 2.0 ** -20]
+            codes, scales = ref.write(rows[t:t + 1], rows[t:t + 1], [t], codes, scales)
+            if t == 0:
+                own = codes[0, 0, 0][at[0]] * float(scales[0, 0, 0])
+            off = np.abs(codes[0, 0, 0][at[:t + 1]] * float(scales[0, 0, 0]) - rows[:t + 1, 0]) / scales[0, 0, 0]
+            most = max(most, off.max())
+            halved = max(halved, (np.abs(codes[0, 0, 0][at[0]] * float(scales[0, 0, 0]) - own) / scales[0, 0, 0]).max())
+    assert 0.7 < most < 1 and halved > 0.5, (most, halved)
