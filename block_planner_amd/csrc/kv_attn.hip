@@ -79,8 +79,10 @@ struct Request {
 // Columns (rows x heads of a group) of a request up to which the decode kernel
 // takes it, where both kernels run.
 constexpr int kDecodeCols = 32;
-// Tiles of 16 columns times pages of a call up to which it runs alone (D <= 128).
-constexpr int kDecodeVisits = 16384;
+// Up to what it runs alone: rounds of its workgroups times (pages of each and
+// kRoundPages) where no request is split (D <= 128; D > 128), tiles of 16 columns
+// times pages (D <= 128) where they are.
+constexpr int kRoundPages = 32, kDecodeRounds = 112, kDecodeRoundsWide = 104, kDecodeVisits = 16384;
 
 __device__ __forceinline__ Request load_request(const AttnArgs &a, int r) {
     Request q;
@@ -809,6 +811,19 @@ void set_splits(int64_t pages, int64_t per, int32_t &splits, int32_t &per_split)
     per_split = int32_t(per > 0 ? per : 1);
 }
 
+// Splits of the decode kernel over `items` tiles of 16 columns: none up to
+// kWholePages pages (a second launch costs more than its four wavefronts' six
+// pages each), else about 4096 workgroups of 16 pages at least -- four per
+// wavefront, which pay for the query's encoding before and the wavefronts' joining
+// after (32 x 4000 tokens of 2 heads x 256: 32 us, with four pages 53) -- or of down
+// to four where that leaves compute units empty.
+void decode_splits(int64_t pages, int64_t items, AttnShape &s) {
+    const int64_t fill = pages * items / 256, least = fill < 4 ? 4 : fill < 16 ? fill : 16;
+    int64_t per = (pages * items + 4095) / 4096;
+    if (per < least) per = least;
+    set_splits(pages, pages <= kWholePages ? pages : per, s.splits, s.split_pages);
+}
+
 AttnShape attn_shape(int64_t T, int64_t R, int32_t n_heads, int32_t D, int32_t n_q, int64_t max_q, int64_t max_kv,
                      int64_t window) {
     // pages a request's rows look at: a window's rows and the pages it cuts at both ends
@@ -819,28 +834,29 @@ AttnShape attn_shape(int64_t T, int64_t R, int32_t n_heads, int32_t D, int32_t n
     // Up to kDecodeCols columns the decode kernel, and also for short prompts:
     // its 16 columns convert no page and come in as many workgroups as its tiles,
     // where the prompt kernel's few would walk the pages one after the other.
-    // What the decode kernel does is counted in tiles times pages.  Prompt kernel
-    // against decode kernel, us, one request of q rows unless said, heads / KV
-    // heads x dim: q 64 of 700, 4 times, 32 / 8 x 128 (5632) 27.3, 13.7; q 1024,
-    // 12 / 2 x 128 (12288) 29.7, 20.1; q 128 of 4000, 32 / 8 x 128 (16128) 36.3,
-    // 35.4; q 256 of 1000, 4 times, the same heads (32768) 35.6, 50.1.  At D = 256
-    // a tile's page takes twice as long: q 512, 8 / 1 (2048) 37.5, 13.9; q 1024
-    // (8192) 47.0, 28.7; q 512, 32 / 8 (8192) 39.2, 42.9; q 2048, 8 / 1 (32768)
-    // 89.6, 118.9.
-    const double visits = double((max_q * group + 15) / 16) * double(R * n_heads) * double(pages > 0 ? pages : 1);
-    s.prompt = max_q * group > kDecodeCols && visits * (D > 128 ? D : 128) > 128.0 * kDecodeVisits;
+    // Whole requests: a round of the decode kernel's workgroups (512 at once, 256
+    // above D = 128) costs its pages and about kRoundPages more for starting and
+    // joining; split ones, which fill the card in any case, by tiles times pages.
+    // Prompt kernel against decode kernel, us, heads / KV heads x dim, rounds x
+    // (pages + 32):
+    //   D = 128  512, 8 / 1 (1 x 40) 20.0, 14.5;  1024, 8 / 1 (1 x 48) 27.1, 14.8;
+    //            1500, 8 / 1 (2 x 56 = 112) 30.8, 23.2;  4 x 300, 32 / 8 (5 x 37) 21.4, 36.6;
+    //            4 x 200, 32 / 8 (4 x 36) 18.2, 26.1;  800 of 1000, 32 / 8 (4 x 48) 42.6, 36.7
+    //   D = 256  512, 8 / 1 (1 x 40) 36.0, 14.7;  1024, 8 / 1 (2 x 48 = 96) 46.1, 31.4;
+    //            300, 32 / 8 (3 x 37 = 111) 28.5, 33.9;  4 x 200, 32 / 8 (7 x 36) 29.3, 69.7
+    // and split, tiles x pages: 64 rows of 4000, 4 times, 32 / 8 x 128 (16128) 48,
+    // 51; 40 of 4000, the same heads x 256 (5040 of 8192) 55.9, 40.3.
+    const int64_t tiles = max_q > 0 ? (max_q * group + 15) / 16 : 1, items = R * n_heads * tiles;
+    const double visits = double(items) * double(pages > 0 ? pages : 1);
+    s.prompt = max_q * group > kDecodeCols;
+    if (s.prompt && items <= 65536) {   // more items are many rounds
+        decode_splits(pages, items, s);
+        const int64_t at_once = D > 128 ? 256 : 512, rounds = (items + at_once - 1) / at_once;
+        if (s.splits > 1) s.prompt = visits * (D > 128 ? D : 128) > 128.0 * kDecodeVisits;
+        else s.prompt = rounds * (pages + kRoundPages) > (D > 128 ? kDecodeRoundsWide : kDecodeRounds);
+    }
     s.decode = !s.prompt || R > 1;
-    const int64_t tiles = s.prompt ? (kDecodeCols + 15) / 16 : max_q > 0 ? (max_q * group + 15) / 16 : 1;
-    // Splits of the decode kernel: none up to kWholePages pages (a second launch
-    // costs more than its four wavefronts' six pages each), else about 4096
-    // workgroups of 16 pages at least -- four per wavefront, which pay for the
-    // query's encoding before and the wavefronts' joining after (32 x 4000
-    // tokens of 2 heads x 256: 32 us, with four pages 53) -- or of down to four
-    // where that leaves compute units empty.
-    const int64_t ditems = R * n_heads * tiles, fill = pages * ditems / 256, least = fill < 4 ? 4 : fill < 16 ? fill : 16;
-    int64_t per = (pages * ditems + 4095) / 4096;
-    if (per < least) per = least;
-    set_splits(pages, pages <= kWholePages ? pages : per, s.splits, s.split_pages);
+    decode_splits(pages, s.prompt ? R * n_heads * ((kDecodeCols + 15) / 16) : items, s);
     // 8 wavefronts share a page's conversion, 4 fill the card with fewer rows
     // and run two workgroups per compute unit out of step.  D = 128: 566 us
     // against 587 at 8192 rows; D = 64: 132 against 86 us a round of workgroups.
@@ -851,9 +867,9 @@ AttnShape attn_shape(int64_t T, int64_t R, int32_t n_heads, int32_t D, int32_t n
     // of each and kJoinPages a split for writing and joining its partial results.
     // Splitting more than fills the card loses: 596 workgroups' worth of rows and
     // heads with a window of 4096 took 130 us whole, 142 in 3 splits.
-    const int64_t items = ptiles * n_heads, slots = s.waves == 8 ? 256 : 512;
+    const int64_t pitems = ptiles * n_heads, slots = s.waves == 8 ? 256 : 512;
     int64_t best = pages, want = 1;
-    for (int64_t n = 2; n <= kMaxSplits && n * items <= slots && n * 2 <= pages; ++n) {
+    for (int64_t n = 2; n <= kMaxSplits && n * pitems <= slots && n * 2 <= pages; ++n) {
         const int64_t cost = (pages + n - 1) / n + kJoinPages * n;
         if (cost < best) { best = cost; want = n; }
     }

@@ -347,3 +347,22 @@ def test_roundings_of_an_entry_stay_below_one_scale():
             most = max(most, off.max())
             halved = max(halved, (np.abs(codes[0, 0, 0][at[0]] * float(scales[0, 0, 0]) - own) / scales[0, 0, 0]).max())
     assert 0.7 < most < 1 and halved > 0.5, (most, halved)
+
+
+@pytest.mark.parametrize("D,n_q,H,R,q,kv,prompt", [
+    # us measured, prompt kernel against decode kernel
+    (64, 32, 4, 4, 300, 300, True), (64, 32, 8, 4, 300, 300, True),       # 17 28; 18 27
+    (64, 8, 1, 1, 1500, 1500, False), (64, 32, 4, 1, 100, 1000, False),   # 22 17; 25 15
+    (128, 32, 8, 4, 300, 300, True), (128, 32, 8, 4, 200, 200, True),     # 21 37; 18 26
+    (128, 32, 8, 4, 512, 512, True), (128, 8, 1, 1, 512, 512, False),     # 29 62; 20 15
+    (128, 8, 1, 1, 1500, 1500, False), (128, 32, 8, 1, 100, 1000, False),   # 31 23; 29 15
+    (192, 32, 8, 4, 200, 200, True), (192, 32, 4, 4, 100, 100, True),     # 23 56; 19 32
+    (192, 8, 1, 1, 1024, 1024, False), (192, 12, 2, 1, 300, 1000, False),   # 38 26; 38 16
+    (256, 32, 8, 4, 200, 200, True), (256, 32, 8, 1, 300, 300, True),     # 29 70; 28 34
+    (256, 32, 8, 1, 512, 512, True), (256, 8, 1, 1, 1024, 1024, False),   # 37 46; 46 31
+    (256, 8, 1, 1, 512, 512, False), (256, 32, 8, 1, 40, 4000, False),    # 36 15; 56 40
+    (256, 32, 8, 1, 100, 4000, True), (128, 32, 8, 1, 300, 4000, True)])  # 63 74; 50 70
+def test_attention_kernel_of_short_prompts(D, n_q, H, R, q, kv, prompt):
+    """The kernel that is faster for the shape."""
+    info = B.ht_kv_attention_kernels(B.KVCacheDesc(A, A, 1000, H, D), R * q, R, n_q, q, kv)
+    assert (info[1] > 0) == prompt
