@@ -189,7 +189,7 @@ __device__ __forceinline__ void encode16(const uint16_t *x, float f, i32x4 *p) {
 // fp16 in registers.  The accumulator of S^T (16 tokens x 16 columns) holds 4
 // tokens of a column per lane, and V's order of tokens makes two such blocks
 // the B operand of P.V as they are.  Bound by HBM: 258 MB of 64 ragged requests
-// in 52 us + 5 us for the join (5.0 TB/s), 683 MB of 3 x 120k tokens in 119 + 8
+// in 53 us + 6 us for the join (4.8 TB/s), 683 MB of 3 x 120k tokens in 121 + 8
 // (5.7 TB/s; a copy reaches 4.8).  A request of 17 pages takes 9 us, five page
 // round trips per wavefront.
 //
@@ -197,6 +197,11 @@ __device__ __forceinline__ void encode16(const uint16_t *x, float f, i32x4 *p) {
 // are hinted not to stay in the caches: 64 ragged requests of 32 x 128 heads 64
 // -> 57 us, 3 x 120k tokens 137 -> 126; with a second tile, which finds the
 // codes in the L2 without the hint, 16 x 7 rows over 3000 tokens 59 -> 65.
+//
+// Two wavefronts per SIMD are asked for up to D = 128: without, the compiler takes
+// 284 registers there for the three planes' accumulators and one wavefront, with
+// it 231.  The third plane costs 1% where HBM bounds (64 ragged requests 58.0 ->
+// 58.6 us) and up to 7% where the matrix units do (short prompts at D = 256).
 template <int DC, bool ONCE>
 __global__ __launch_bounds__(kAttnThreads, DC <= 2 ? 2 : 1) void attn_decode_kernel(AttnArgs a) {
     constexpr int D = 64 * DC, NE = D / 16;
@@ -418,12 +423,14 @@ __global__ __launch_bounds__(kAttnThreads, DC <= 2 ? 2 : 1) void attn_decode_ker
 // product to the next in registers.  The next page is loaded into registers
 // while this one is multiplied, and converted into the other LDS buffer after.
 //
-// 8192 rows of 32 x 128 heads: 556 us, 989 TFLOP/s, where a large library
-// product reaches 1211 on this card.  The matrix units are busy 46% of the time
-// and the vector units 55%: a 32x32x16 product leaves room for about four vector
-// instructions, and a page has eight per product (two exponentials, their
-// sums, maxima and conversions).  At D = 64 the same vector work meets half the
-// products: six windowed chunks take 128 us, 490 TFLOP/s.
+// 8192 rows of 32 x 128 heads: 561 us, 980 TFLOP/s (551 to 570 us on several
+// cards), where a large library product reaches 1211.  The matrix units are busy
+// 47% of the time that a compute unit has work, the vector units 53%: a 32x32x16
+// product leaves room for about four vector instructions, and a page has eight
+// per product (two exponentials, their sums, maxima and conversions).  At D = 64
+// the same vector work meets half the products (vector units 63%, matrix units
+// 30%): six windowed chunks take 127 us, 490 TFLOP/s, a third of it with most
+// compute units idle, in the second round of 577 workgroups on 512 places.
 template <int DC, int NW>
 __global__ __launch_bounds__(64 * NW, DC <= 2 ? 2 : 1) void attn_prompt_kernel(AttnArgs a) {
     constexpr int D = 64 * DC, KS = D / 16, DB = D / 32, kCols = 32 * NW, kThr = 64 * NW;
@@ -858,8 +865,12 @@ AttnShape attn_shape(int64_t T, int64_t R, int32_t n_heads, int32_t D, int32_t n
     s.decode = !s.prompt || R > 1;
     decode_splits(pages, s.prompt ? R * n_heads * ((kDecodeCols + 15) / 16) : items, s);
     // 8 wavefronts share a page's conversion, 4 fill the card with fewer rows
-    // and run two workgroups per compute unit out of step.  D = 128: 566 us
-    // against 587 at 8192 rows; D = 64: 132 against 86 us a round of workgroups.
+    // and run two workgroups per compute unit out of step.  D = 128, 8 against 4,
+    // us, by tiles of 256 columns times heads: 192 (4096 rows, 12 / 2 heads) 122.9,
+    // 104.3; 256 (2048, 32 / 8) 77.6, 68.7; 512 (4096, 32 / 8) 165.1, 176.2; 640 (4096,
+    // 40 / 40) 220.8, 208.8; 752 (3000, 64 / 8) 185.9, 186.0; 960 (6000, 40 / 40) 436.1,
+    // 435.7; 1024 (8192, 32 / 8) 575.6, 595.3; 1504 (12000, 32 / 8) 1154, 1217; 4096
+    // (16384, 64 / 8) 4265, 4447.  D = 64: 132 against 86 us a round of workgroups.
     s.waves = D == 128 && (T * group + 255) / 256 * n_heads >= 1024 ? 8 : 4;
     const int64_t cols = 32 * s.waves, ptiles = (T * group + cols - 1) / cols + (R - 1);
     // Splits of prompts: only into places for workgroups (two of 4 wavefronts or

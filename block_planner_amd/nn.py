@@ -247,7 +247,8 @@ class KVPool:
 
     plan() advances the lengths; nothing is read back to the host.  A request
     that finds no pages keeps its length and stores none of its new rows
-    (step.status[1] counts those): release others and plan its rows again."""
+    (step.status[1] counts those): its rows' outputs of that step mean nothing,
+    release others and plan its rows again."""
 
     def __init__(self, layers: int, n_pages: int, n_kv_heads: int, head_dim: int, max_requests: int, max_pages: int,
                  device):
@@ -331,6 +332,8 @@ class HyperAttention(torch.nn.Module):
             raise ValueError(f"qkv: expected [rows, {(n + 2 * m) * d}], got {tuple(y.shape)}")
         y = y.unflatten(1, (n + 2 * m, d))
         codes, scales = pool.caches[layer]
+        # q and k come out in one type, bf16 (the attention's): k's rounding to it adds at most a quarter of a step of
+        # the cache's scale to the half step of its code, and spares a second pass for an fp32 k
         wq, wk = (None, None) if self.q_weight is None else (self.q_weight.float(), self.k_weight.float())
         q, k = api.qk_norm_rope(y[:, :n], y[:, n:n + m], step.positions, self.inv_freq, wq, wk, self.eps,
                                 self.interleaved, out_dtype=torch.bfloat16)
