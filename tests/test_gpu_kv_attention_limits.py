@@ -5,6 +5,7 @@ import pytest
 import torch
 
 import kv_reference as ref
+from block_planner_amd import binding as B
 from test_gpu_kv_attention import bf16, check, make, run
 
 pytestmark = pytest.mark.gpu
@@ -12,6 +13,12 @@ pytestmark = pytest.mark.gpu
 
 # rows of the requests, launch hint for kv_len: the decode kernel, the prompt kernel whole, and in splits
 SIDES = {"decode": ([1, 3], {}), "prompt": ([70, 40], dict(max_kv=10 ** 6)), "splits": ([70, 40], dict(max_kv=40000))}
+
+
+def assert_side(side, q, codes, q_len, kv, hint):
+    d = B.KVCacheDesc(1 << 20, 1 << 20, codes.shape[0], codes.shape[1], codes.shape[3] // 64)
+    info = B.ht_kv_attention_kernels(d, len(q), len(q_len), q.shape[1], max(q_len), hint.get("max_kv", int(max(kv))))
+    assert (info[1] > 1 if side == "splits" else info[1] > 0) == (side != "decode"), info
 
 
 @pytest.mark.parametrize("side", SIDES)
@@ -23,6 +30,7 @@ def test_scores_of_any_size(side, power):
     bf16: 2^-8), every row a mean of the values it sees."""
     q_len, hint = SIDES[side]
     rng, q, codes, scales, table, cu, kv = make(power, q_len, [200, 2100], 8, 2, 64)
+    assert_side(side, q, codes, q_len, kv, hint)
     D, index = 64, ref.block_index(64)
     scale = 1 / np.sqrt(D)
     vals = []
@@ -110,6 +118,7 @@ def test_one_channel_of_q_far_above_the_rest(side, n_q, H, D, outlier):
     large channel differ little from token to token, so that the rest decides."""
     q_len, hint = SIDES[side]
     rng, q, codes, scales, table, cu, kv = make(int(outlier) + D, q_len, [500, 1100], n_q, H, D)
+    assert_side(side, q, codes, q_len, kv, hint)
     index = ref.block_index(D)[0]
     q[:, :, 5] = outlier * np.sign(q[:, :, 5])
     q = bf16(q)
@@ -130,6 +139,7 @@ def test_a_window_past_everything_is_none(side, causal):
     """Up to the largest number, also for requests of more rows than tokens."""
     q_len, hint = SIDES[side]
     args = make(8, q_len, [2, 300], 4, 2, 64)[1:]
+    assert_side(side, args[0], args[1], q_len, args[-1], hint)
     want = check(*args, causal=causal, **hint)
     for window in (2 ** 31 - 1, 2 ** 31, 2 ** 62, 2 ** 63 - 1):
         assert torch.equal(run(*args, causal=causal, window=window, **hint), want)
