@@ -579,6 +579,7 @@ __global__ __launch_bounds__(64 * NW, DC <= 2 ? 2 : 1) void attn_prompt_kernel(A
             const int j0 = p * kPage;
             if (id0 < 0 || j0 < w_lo_max || j0 + kPage > w_hi_min) {
                 const int seen = id0 < 0 ? 0 : hi;
+                if (id0 < 0) f = 1.f;   // page 0 stands in, and its scale may be anything
 #pragma unroll
                 for (int b = 0; b < 2; ++b)
 #pragma unroll

@@ -143,3 +143,24 @@ def test_a_window_past_everything_is_none(side, causal):
     want = check(*args, causal=causal, **hint)
     for window in (2 ** 31 - 1, 2 ** 31, 2 ** 62, 2 ** 63 - 1):
         assert torch.equal(run(*args, causal=causal, window=window, **hint), want)
+
+
+@pytest.mark.parametrize("n_q,H,D", [(8, 2, 64), (4, 2, 128), (2, 2, 192)])
+@pytest.mark.parametrize("side", SIDES)
+def test_hidden_pages_are_nobodys(side, n_q, H, D):
+    """What the cache holds in pages that no request owns, NaN scales among
+    them, does not reach a request with hidden pages."""
+    q_len, hint = SIDES[side]
+    rng, q, codes, scales, table, cu, kv = make(D, q_len, [300, 2100], n_q, H, D)
+    assert_side(side, q, codes, q_len, kv, hint)
+    table[0, 1], table[1, 3:5], table[1, -1] = -1, len(codes), -7
+    want = check(q, codes, scales, table, cu, kv, **hint)
+    free = np.setdiff1d(np.arange(len(codes)), table)
+    if 0 not in free:   # page 0 and a free one change places
+        other = free[0]
+        codes[[0, other]], scales[[0, other]] = codes[[other, 0]], scales[[other, 0]]
+        table[table == 0] = other
+        free = np.setdiff1d(np.arange(len(codes)), table)
+    assert 0 in free
+    codes[free], scales[free] = -128, np.float32(np.nan)
+    assert torch.equal(run(q, codes, scales, table, cu, kv, **hint), want)
