@@ -79,10 +79,9 @@ struct Request {
 // Columns (rows x heads of a group) of a request up to which the decode kernel
 // takes it, where both kernels run.
 constexpr int kDecodeCols = 32;
-// Up to what it runs alone: rounds of its workgroups times (pages of each and
-// kRoundPages) where no request is split (D <= 128; D > 128), tiles of 16 columns
-// times pages (D <= 128) where they are.
-constexpr int kRoundPages = 32, kDecodeRounds = 112, kDecodeRoundsWide = 104, kDecodeVisits = 16384;
+// Tiles of 16 columns times pages of a call up to which it runs alone (D <= 128),
+// where requests are split.
+constexpr int kDecodeVisits = 16384;
 
 __device__ __forceinline__ Request load_request(const AttnArgs &a, int r) {
     Request q;
@@ -842,26 +841,30 @@ AttnShape attn_shape(int64_t T, int64_t R, int32_t n_heads, int32_t D, int32_t n
     // Up to kDecodeCols columns the decode kernel, and also for short prompts:
     // its 16 columns convert no page and come in as many workgroups as its tiles,
     // where the prompt kernel's few would walk the pages one after the other.
-    // Whole requests: a round of the decode kernel's workgroups (512 at once, 256
-    // above D = 128) costs its pages and about kRoundPages more for starting and
-    // joining; split ones, which fill the card in any case, by tiles times pages.
-    // Prompt kernel against decode kernel, us, heads / KV heads x dim, rounds x
-    // (pages + 32):
-    //   D = 128  512, 8 / 1 (1 x 40) 20.0, 14.5;  1024, 8 / 1 (1 x 48) 27.1, 14.8;
-    //            1500, 8 / 1 (2 x 56 = 112) 30.8, 23.2;  4 x 300, 32 / 8 (5 x 37) 21.4, 36.6;
-    //            4 x 200, 32 / 8 (4 x 36) 18.2, 26.1;  800 of 1000, 32 / 8 (4 x 48) 42.6, 36.7
-    //   D = 256  512, 8 / 1 (1 x 40) 36.0, 14.7;  1024, 8 / 1 (2 x 48 = 96) 46.1, 31.4;
-    //            300, 32 / 8 (3 x 37 = 111) 28.5, 33.9;  4 x 200, 32 / 8 (7 x 36) 29.3, 69.7
-    // and split, tiles x pages: 64 rows of 4000, 4 times, 32 / 8 x 128 (16128) 48,
-    // 51; 40 of 4000, the same heads x 256 (5040 of 8192) 55.9, 40.3.
+    // Split requests, which fill the card in any case, by tiles times pages; whole
+    // ones by both kernels' times in us, fitted to 3070 shapes of 10 to 1500 rows
+    // (standard errors 8 to 12%): the decode kernel's workgroups come in rounds of
+    // 512 (256 above D = 128) that cost their pages and a start each, the prompt
+    // kernel's walk all pages whatever their number.  Above D = 128, where a few
+    // rounds are all, tiles times pages bound whole requests too.
+    // Prompt kernel against decode kernel, us, rows of each request, heads / KV heads:
+    //   D = 128  512, 8 / 1 20.0, 14.5;  1024, 8 / 1 27.1, 14.8;  1500, 8 / 1 30.8, 23.2;
+    //            700, 32 / 8 34.6, 27.7;  512 of 1000, 32 / 8 33.4, 26.1;
+    //            4 x 200, 32 / 8 18.2, 26.1;  4 x 300, 32 / 8 21.4, 36.6
+    //   D = 256  512, 8 / 1 36.0, 14.7;  1024, 8 / 1 46.1, 31.4;  300, 32 / 8 28.5, 33.9;
+    //            512, 32 / 8 37.2, 46.4;  4 x 200, 32 / 8 29.3, 69.7
+    // and split: 64 rows of 4000, 4 times, 32 / 8 x 128 (16128 visits) 48, 51; 40 of
+    // 4000, the same heads x 256 (5040 of 8192) 55.9, 40.3.
     const int64_t tiles = max_q > 0 ? (max_q * group + 15) / 16 : 1, items = R * n_heads * tiles;
-    const double visits = double(items) * double(pages > 0 ? pages : 1);
+    const double p = double(pages > 0 ? pages : 1);
     s.prompt = max_q * group > kDecodeCols;
-    if (s.prompt && items <= 65536) {   // more items are many rounds
+    if (s.prompt && items <= 65536) {   // more are the prompt kernel's
         decode_splits(pages, items, s);
-        const int64_t at_once = D > 128 ? 256 : 512, rounds = (items + at_once - 1) / at_once;
-        if (s.splits > 1) s.prompt = visits * (D > 128 ? D : 128) > 128.0 * kDecodeVisits;
-        else s.prompt = rounds * (pages + kRoundPages) > (D > 128 ? kDecodeRoundsWide : kDecodeRounds);
+        const bool many = double(items) * p * (D > 128 ? D : 128) > 128.0 * kDecodeVisits;
+        const double cols = double(R) * double(max_q * group) * n_heads / 128 / 512;   // prompt workgroups per place
+        const double d_us = D > 128 ? 10 + items / 256.0 * (0.5 * p + 5) : 12 + items / 512.0 * (0.32 * p + 1);
+        const double p_us = D > 128 ? 18 + p * (0.8 + 5.5 * cols) : 14 + p * (0.35 + 1.8 * cols);
+        s.prompt = s.splits > 1 ? many : d_us > p_us || (D > 128 && many);
     }
     s.decode = !s.prompt || R > 1;
     decode_splits(pages, s.prompt ? R * n_heads * ((kDecodeCols + 15) / 16) : items, s);
