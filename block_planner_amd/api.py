@@ -206,17 +206,15 @@ def _ints(*specs) -> None:
 def _on_gpu(*tensors) -> None:
     """The kernels run on the current device and get bare addresses: host
     memory and other devices' never reach them."""
-    on = -1
+    on = None
     for t in tensors:
-        if t is not None:
-            d = t.get_device()   # -1: not on a GPU
-            if d < 0:
+        if t is not None and t.get_device() != on:
+            if t.get_device() < 0:
                 raise ValueError("every tensor must be on the GPU")
-            if on < 0:
-                on = d
-            elif d != on:
-                raise ValueError(f"every tensor must be on one GPU, got cuda:{on} and cuda:{d}")
-    if on >= 0 and on != torch.cuda.current_device():
+            if on is not None:
+                raise ValueError(f"every tensor must be on one GPU, got cuda:{on} and cuda:{t.get_device()}")
+            on = t.get_device()
+    if on is not None and on != torch.cuda.current_device():
         raise ValueError(f"the tensors are on cuda:{on}, the current device is cuda:{torch.cuda.current_device()}")
 
 
