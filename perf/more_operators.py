@@ -188,18 +188,16 @@ def prepare(case, seed):
 
 
 def _stats(x, scale):
-    """What the forward pass keeps of each row for the backward pass: fp32 (a, b), log2 sum exp(z) = a + b with a the
-    largest entry's, and the entropy."""
-    z = x.double() * (scale / math.log(2))
-    top = z.amax(-1)
-    some = top > -math.inf
-    a = torch.where(some, top, 0.0).float()
-    d = z - a.double()[:, None]
+    """What the forward pass keeps of each row for the backward pass: fp32 (a, b), the largest logit (-Inf: the row allows
+    nothing) and log2 sum exp((x - a) scale), and the entropy."""
+    a = x.amax(-1, keepdim=True)
+    some = a > -math.inf
+    d = (x.double() - torch.where(some, a, 0.0)) * (scale / math.log(2))
     p = torch.exp2(d)
-    total = p.sum(-1)
-    b = torch.where(some, total, 1.0).log2()
-    entropy = (b - (p * d.clamp(min=-2000.0)).sum(-1) / torch.where(some, total, 1.0)) * math.log(2)
-    return torch.stack([torch.where(some, a, -math.inf), b.float()], 1), entropy.float()
+    total = torch.where(some, p.sum(-1, keepdim=True), 1.0)
+    b = total.log2()
+    entropy = (b - (p * d.clamp(min=-2000.0)).sum(-1, keepdim=True) / total) * math.log(2)
+    return torch.cat([a, b], 1).float(), entropy[:, 0].float()
 
 
 # ---------------------------------------------------------------------------
@@ -283,15 +281,14 @@ def _logprobs(s):
 def _logprobs_backward(s):
     x, t = s["logits"], s["temperature"]
     a, b = s["stats"][:, :1], s["stats"][:, 1:]
-    z = x.double() / (t * math.log(2))
-    logp = ((z - torch.where(a > -math.inf, a, 0.0).double() - b.double()) * math.log(2)).float()
+    some = a > -math.inf
+    logp = ((x.double() - torch.where(some, a, 0.0)) / t - b.double() * math.log(2)).float()
     ids = s["ids"].long().view(x.shape[0], -1)
     g = torch.where(ids >= 0, s["dlogp"].view(x.shape[0], -1), 0.0)
     d = logp.clamp(min=-1e4).add_(s["entropy"][:, None]).mul_(s["dent"][:, None]).add_(g.sum(-1, keepdim=True))
     d = d.mul_(logp.exp_()).neg_()
     d.scatter_add_(1, ids.clamp(min=0), g)
-    d = torch.where(a > -math.inf, d, 0.0)
-    return (d / t).to(x.dtype)
+    return (torch.where(some, d, 0.0) / t).to(x.dtype)
 
 
 def _teacher(s):
