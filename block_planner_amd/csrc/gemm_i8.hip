@@ -529,9 +529,15 @@ I8Plan i8_plan(const ht_packed_weight *w, int64_t Mt) {
 bool i8_ok(const ht_packed_weight *w) { return w->row_tile == 16; }
 
 size_t i8_ws(const ht_packed_weight *w, int64_t M, bool w8) {
-    const int64_t Mt = M < kI8ChunkRows ? M : kI8ChunkRows;
-    const I8Plan P = i8_plan(w, Mt);
-    return i8_layout(w, Mt, P.S, P.mode != kNone, w8).total;
+    // the last chunk, of fewer rows, may be split along K where the others are not
+    size_t most = 0;
+    for (const int64_t Mt : {M < kI8ChunkRows ? M : kI8ChunkRows, M % kI8ChunkRows}) {
+        if (Mt == 0) continue;
+        const I8Plan P = i8_plan(w, Mt);
+        const size_t n = i8_layout(w, Mt, P.S, P.mode != kNone, w8).total;
+        most = n > most ? n : most;
+    }
+    return most;
 }
 
 ht_status run_gemm_i8(const ht_packed_weight *w, const uint16_t *x, int64_t M, int64_t ldx, float *y, uint16_t *ybf,

@@ -1,0 +1,489 @@
+// norm.hip -- the residual's addition and the root-mean-square norm between two
+// layers in one pass, its output as the next linear takes it (fp32, bfloat16
+// or 8-bit rows), its backward pass, and 8-bit rows read back.
+//
+//   h = x + res;  r = 1 / sqrt(mean(h^2) + eps);  y = h r w
+//   backward, with g = w dy:  d = dh + r g - h r^3 / K sum(g h),
+//   dw = sum over rows of dy h r.
+//
+// Bound by HBM: a few fp32 operations per 16 bytes.  A row is held in
+// registers (8 consecutive values per thread and group), so its sum of squares
+// costs no second read: by one wavefront up to 2048 columns (four rows per
+// workgroup, no barrier), by 256 threads up to 8192, by 1024 above.
+#include "rows.h"
+
+namespace ht {
+
+namespace {
+
+constexpr int64_t kNormMaxK = 32768;
+
+struct NormArgs {
+    const void *x, *res;
+    void *h, *y;
+    int64_t ldx, ldr, ldh, ldy;
+    const float *w;
+    uint8_t *codes;          // 8-bit rows, or null
+    float *scales;
+    int64_t M, Mp;           // Mp = 16 * groups
+    int32_t K, y_bf16;
+    float eps, inv_k;
+};
+
+// Sum over the row's TPR threads (a wavefront, or the workgroup).
+template <int TPR>
+__device__ __forceinline__ float row_total(float v, float *part) {
+    v = wave_sum(v);
+    if constexpr (TPR > 64) {
+        if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = v;
+        __syncthreads();
+        v = 0.f;
+#pragma unroll
+        for (int i = 0; i < TPR / 64; ++i) v += part[i];
+    }
+    return v;
+}
+
+// The row's 8 values of one lane as codes; the 64-wide block's 8 lanes share
+// the scale.  The largest magnitude's bits, compared as whole numbers, tell a
+// block that holds Inf or NaN too.
+__device__ __forceinline__ void encode8(const Row8 &y, const NormArgs &a, int64_t m, int col, bool live) {
+    uint32_t top = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) top = max(top, __float_as_uint(y.v[j]) & 0x7FFFFFFFu);
+    top = max(top, dpp_u32<kDppXor1>(top));
+    top = max(top, dpp_u32<kDppXor2>(top));
+    top = max(top, dpp_u32<kDppHalfMirror>(top));
+    const bool bad = top >= 0x7F800000u;
+    int E = 7;
+    if (top > 0 && !bad) (void)frexpf(__uint_as_float(top), &E);
+    uint32_t c[2] = {0, 0};
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const float v = fminf(127.0f, fmaxf(-127.0f, rintf(ldexpf(y.v[j], 7 - E))));
+        c[j >> 2] |= (uint32_t(int32_t(bad ? 0.0f : v)) & 0xFFu) << (8 * (j & 3));
+    }
+    if (!live) return;
+    const int64_t g = m >> 4;
+    const uint32_t r = uint32_t(m) & 15u, kb = uint32_t(col) >> 6, e = uint32_t(col) & 63u;
+    uint8_t *dst = a.codes + (g * (a.K / 64) + kb) * 1024 + 16u * (r + 16u * (e >> 4)) + (e & 15u);
+    *reinterpret_cast<u32x2 *>(dst) = u32x2{c[0], c[1]};
+    if (e == 0) a.scales[int64_t(kb) * a.Mp + m] = bad ? __builtin_nanf("") : ldexpf(1.0f, E - 7);
+}
+
+template <int TPR, int NV, typename X, typename R, bool RES>
+__global__ __launch_bounds__(TPR > 256 ? TPR : 256) void norm_kernel(NormArgs a) {
+    constexpr int kRows = TPR >= 256 ? 1 : 256 / TPR;
+    __shared__ float part[16];
+    const int t = threadIdx.x & (TPR - 1);
+    uint32_t b = blockIdx.x;
+    // 8-bit rows: the 16 rows of a group share cache lines, so neighbouring
+    // workgroups are placed on one XCD (workgroups go to the 8 XCDs in turn)
+    if (a.codes && (gridDim.x & 7u) == 0) b = (b & 7u) * (gridDim.x >> 3) + (b >> 3);
+    const int64_t m = int64_t(b) * kRows + (threadIdx.x / TPR);
+    if (m >= a.M) return;    // whole wavefronts (TPR = 64), never part of a workgroup that meets at a barrier
+    const X *x = static_cast<const X *>(a.x) + m * a.ldx;
+    Row8 v[NV];
+    float ss = 0.f;
+#pragma unroll
+    for (int g = 0; g < NV; ++g) {
+        const int c = 8 * (t + TPR * g);
+        if (c < a.K) {
+            v[g] = load8(x + c);
+            if constexpr (RES) {
+                const Row8 r = load8(static_cast<const R *>(a.res) + m * a.ldr + c);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[g].v[j] += r.v[j];
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[g].v[j] = 0.f;
+        }
+    }
+    if constexpr (RES) {
+        // the norm sees h as it is stored: the backward pass, which has h, differentiates what was computed
+#pragma unroll
+        for (int g = 0; g < NV; ++g) {
+            const int c = 8 * (t + TPR * g);
+            if constexpr (sizeof(R) == 2) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[g].v[j] = __uint_as_float(uint32_t(f32_to_bf16_rne(v[g].v[j])) << 16);
+            }
+            if (a.h && c < a.K) store8(static_cast<R *>(a.h) + m * a.ldh + c, v[g]);
+        }
+    }
+#pragma unroll
+    for (int g = 0; g < NV; ++g)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) ss += v[g].v[j] * v[g].v[j];
+    const float rn = 1.0f / sqrtf(row_total<TPR>(ss, part) * a.inv_k + a.eps);
+#pragma unroll
+    for (int g = 0; g < NV; ++g) {
+        const int c = 8 * (t + TPR * g);
+        const bool live = c < a.K;
+        if (live) {
+            const Row8 w = load8(a.w + c);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[g].v[j] = v[g].v[j] * rn * w.v[j];
+            if (a.y) {
+                if (a.y_bf16) store8(static_cast<uint16_t *>(a.y) + m * a.ldy + c, v[g]);
+                else store8(static_cast<float *>(a.y) + m * a.ldy + c, v[g]);
+            }
+        }
+        if (a.codes) encode8(v[g], a, m, c, live);
+    }
+}
+
+struct NormBwdArgs {
+    const void *dy, *h, *dh;
+    void *dres, *dx;         // in h's type; in the other type, or null
+    int64_t lddy, ldh, lddh, lddres, lddx;
+    const float *w;
+    float *part;             // [gridDim.x][K], or dw itself where one workgroup does it all
+    int64_t M;
+    int32_t K;
+    float eps, inv_k;
+};
+
+// A workgroup takes every gridDim.x-th set of rows and keeps its part of dw in
+// registers; the parts are added by norm_dw_kernel in a fixed order.
+template <int TPR, int NV, typename Y, typename H>
+__global__ __launch_bounds__(TPR > 256 ? TPR : 256) void norm_bwd_kernel(NormBwdArgs a) {
+    constexpr int kRows = TPR >= 256 ? 1 : 256 / TPR;
+    __shared__ float part[2][32];
+    extern __shared__ __align__(16) float acc[];     // TPR = 64: [4][K]
+    const int t = threadIdx.x & (TPR - 1);
+    const int sub = threadIdx.x / TPR;
+    Row8 w[NV], dw[NV];
+#pragma unroll
+    for (int g = 0; g < NV; ++g) {
+        const int c = 8 * (t + TPR * g);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) w[g].v[j] = dw[g].v[j] = 0.f;
+        if (c < a.K) w[g] = load8(a.w + c);
+    }
+    int at = 0;
+    for (int64_t m0 = int64_t(blockIdx.x) * kRows; m0 < a.M; m0 += int64_t(gridDim.x) * kRows) {
+        const int64_t m = m0 + sub;
+        if (kRows > 1 && m >= a.M) break;            // a wavefront of its own: no barrier inside the loop
+        const H *hp = static_cast<const H *>(a.h) + m * a.ldh;
+        const Y *yp = static_cast<const Y *>(a.dy) + m * a.lddy;
+        Row8 h[NV], dy[NV];
+        float ss = 0.f, dot = 0.f;
+#pragma unroll
+        for (int g = 0; g < NV; ++g) {
+            const int c = 8 * (t + TPR * g);
+            if (c < a.K) {
+                h[g] = load8(hp + c);
+                dy[g] = load8(yp + c);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) h[g].v[j] = dy[g].v[j] = 0.f;
+            }
+        }
+#pragma unroll
+        for (int g = 0; g < NV; ++g)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                ss += h[g].v[j] * h[g].v[j];
+                dot += dy[g].v[j] * w[g].v[j] * h[g].v[j];
+            }
+        ss = wave_sum(ss);
+        dot = wave_sum(dot);
+        if constexpr (TPR > 64) {
+            float *p = part[at];
+            at ^= 1;                                 // two sets in turn: one barrier a row
+            if ((threadIdx.x & 63) == 0) {
+                p[threadIdx.x >> 6] = ss;
+                p[16 + (threadIdx.x >> 6)] = dot;
+            }
+            __syncthreads();
+            ss = dot = 0.f;
+#pragma unroll
+            for (int i = 0; i < TPR / 64; ++i) {
+                ss += p[i];
+                dot += p[16 + i];
+            }
+        }
+        const float rn = 1.0f / sqrtf(ss * a.inv_k + a.eps);
+        const float k = dot * a.inv_k * rn * rn;     // d = dh + r (g - h k)
+#pragma unroll
+        for (int g = 0; g < NV; ++g) {
+            const int c = 8 * (t + TPR * g);
+            if (c >= a.K) continue;
+            Row8 d;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                dw[g].v[j] += dy[g].v[j] * (h[g].v[j] * rn);
+                d.v[j] = rn * (dy[g].v[j] * w[g].v[j] - h[g].v[j] * k);
+            }
+            if (a.dh) {
+                const Row8 e = load8(static_cast<const H *>(a.dh) + m * a.lddh + c);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) d.v[j] += e.v[j];
+            }
+            store8(static_cast<H *>(a.dres) + m * a.lddres + c, d);
+            if (a.dx) {
+                if constexpr (sizeof(H) == 4) store8(static_cast<uint16_t *>(a.dx) + m * a.lddx + c, d);
+                else store8(static_cast<float *>(a.dx) + m * a.lddx + c, d);
+            }
+        }
+    }
+    float *out = a.part + int64_t(blockIdx.x) * a.K;
+    if constexpr (kRows > 1) {
+#pragma unroll
+        for (int g = 0; g < NV; ++g) {
+            const int c = 8 * (t + TPR * g);
+            if (c < a.K) store8(acc + sub * a.K + c, dw[g]);
+        }
+        __syncthreads();
+        for (int c = threadIdx.x; c < a.K; c += 256) {
+            float s = 0.f;
+#pragma unroll
+            for (int i = 0; i < kRows; ++i) s += acc[i * a.K + c];
+            out[c] = s;
+        }
+    } else {
+#pragma unroll
+        for (int g = 0; g < NV; ++g) {
+            const int c = 8 * (t + TPR * g);
+            if (c < a.K) store8(out + c, dw[g]);
+        }
+    }
+}
+
+// dw from the workgroups' parts: 16 columns per workgroup, 64 threads per
+// column over the parts in turn, then a tree: a fixed order.
+__global__ __launch_bounds__(1024) void norm_dw_kernel(const float *part, int n, int K, float *dw) {
+    __shared__ float acc[64][17];
+    const int col = threadIdx.x & 15, row = threadIdx.x >> 4;
+    const int c = int(blockIdx.x) * 16 + col;
+    float s = 0.f;
+    if (c < K) {
+#pragma unroll 8
+        for (int i = row; i < n; i += 64) s += part[int64_t(i) * K + c];
+    }
+    acc[row][col] = s;
+    __syncthreads();
+    for (int k = 32; k > 0; k >>= 1) {
+        if (row < k) acc[row][col] += acc[row + k][col];
+        __syncthreads();
+    }
+    if (row == 0 && c < K) dw[c] = acc[0][col];
+}
+
+// 8-bit rows as the values they stand for: a wavefront turns one 1 KiB record
+// (16 rows x 64 columns) round, each lane 16 codes of one row.
+template <typename Y>
+__global__ __launch_bounds__(256) void q8_values_kernel(const uint8_t *codes, const float *scales, int64_t M, int64_t Mp,
+                                                        uint32_t KB, int64_t records, Y *y, int64_t ldy) {
+    const int64_t rec = int64_t(blockIdx.x) * 4 + (threadIdx.x >> 6);
+    if (rec >= records) return;
+    const uint32_t lane = threadIdx.x & 63;
+    const int64_t g = rec / KB;
+    const uint32_t kb = uint32_t(rec - g * KB);
+    const int64_t m = 16 * g + (lane & 15u);
+    if (m >= M) return;
+    const u32x4 u = reinterpret_cast<const u32x4 *>(codes + rec * 1024)[lane];
+    const float s = scales[int64_t(kb) * Mp + m];
+    Y *p = y + m * ldy + 64u * kb + 16u * (lane >> 4);
+    Row8 a, b;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        a.v[j] = float(int8_t(u[j >> 2] >> (8 * (j & 3)))) * s;
+        b.v[j] = float(int8_t(u[2 + (j >> 2)] >> (8 * (j & 3)))) * s;
+    }
+    store8(p, a);
+    store8(p + 8, b);
+}
+
+template <int TPR, int NV>
+void launch_norm(const NormArgs &a, int32_t xt, int32_t rt, hipStream_t s) {
+    constexpr int kThreads = TPR > 256 ? TPR : 256, kRows = TPR >= 256 ? 1 : 256 / TPR;
+    const uint32_t grid = uint32_t((a.M + kRows - 1) / kRows);
+    const bool xb = xt == HT_BF16, rb = rt == HT_BF16;
+    if (!a.res) {
+        if (xb) norm_kernel<TPR, NV, uint16_t, float, false><<<grid, kThreads, 0, s>>>(a);
+        else norm_kernel<TPR, NV, float, float, false><<<grid, kThreads, 0, s>>>(a);
+    } else if (xb) {
+        if (rb) norm_kernel<TPR, NV, uint16_t, uint16_t, true><<<grid, kThreads, 0, s>>>(a);
+        else norm_kernel<TPR, NV, uint16_t, float, true><<<grid, kThreads, 0, s>>>(a);
+    } else {
+        if (rb) norm_kernel<TPR, NV, float, uint16_t, true><<<grid, kThreads, 0, s>>>(a);
+        else norm_kernel<TPR, NV, float, float, true><<<grid, kThreads, 0, s>>>(a);
+    }
+}
+
+template <int TPR, int NV>
+void launch_norm_bwd(const NormBwdArgs &a, uint32_t grid, int32_t yt, int32_t ht, hipStream_t s) {
+    constexpr int kThreads = TPR > 256 ? TPR : 256, kRows = TPR >= 256 ? 1 : 256 / TPR;
+    const size_t lds = kRows > 1 ? size_t(kRows) * size_t(a.K) * 4 : 0;
+    const bool yb = yt == HT_BF16, hb = ht == HT_BF16;
+    if (yb && hb) norm_bwd_kernel<TPR, NV, uint16_t, uint16_t><<<grid, kThreads, lds, s>>>(a);
+    else if (yb) norm_bwd_kernel<TPR, NV, uint16_t, float><<<grid, kThreads, lds, s>>>(a);
+    else if (hb) norm_bwd_kernel<TPR, NV, float, uint16_t><<<grid, kThreads, lds, s>>>(a);
+    else norm_bwd_kernel<TPR, NV, float, float><<<grid, kThreads, lds, s>>>(a);
+}
+
+// The instance for K columns: threads per row and groups of 8 per thread.
+#define HT_NORM_SHAPES(K, CALL)           \
+    do {                                  \
+        if (K <= 512) CALL(64, 1);        \
+        else if (K <= 1024) CALL(64, 2);  \
+        else if (K <= 2048) CALL(64, 4);  \
+        else if (K <= 4096) CALL(256, 2); \
+        else if (K <= 8192) CALL(256, 4); \
+        else if (K <= 16384) CALL(1024, 2); \
+        else CALL(1024, 4);               \
+    } while (0)
+
+// Workgroups of the backward pass.
+uint32_t norm_bwd_grid(int64_t M, int64_t K) {
+    const int64_t rows = K <= 2048 ? 4 : 1, most = K <= 8192 ? 512 : 256;
+    const int64_t sets = (M + rows - 1) / rows;
+    return uint32_t(sets < most ? sets : most);
+}
+
+ht_status check_norm(int64_t M, int64_t K) {
+    if (M < 0 || M > (int64_t(1) << 30) || K <= 0 || K % 8 || K > kNormMaxK) return HT_ESHAPE;
+    return HT_OK;
+}
+
+}  // namespace
+}  // namespace ht
+
+using namespace ht;
+
+#define HT_TRY(e)                       \
+    do {                                \
+        const ht_status st_ = (e);      \
+        if (st_ != HT_OK) return st_;   \
+    } while (0)
+
+extern "C" ht_status ht_q8_bytes(int64_t M, int64_t K, size_t *codes, size_t *scales) {
+    if (!codes || !scales) return HT_EINVAL;
+    HT_TRY(check_q8_shape(M, K));
+    *codes = size_t(q8_groups(M)) * size_t(K / 64) * 1024;
+    *scales = size_t(q8_groups(M)) * size_t(K / 64) * 16 * sizeof(float);
+    return HT_OK;
+}
+
+extern "C" ht_status ht_q8_values(const ht_q8_rows *q, void *y, int64_t ldy, int32_t yt, ht_stream stream) {
+    if (!q || !act_size(yt)) return HT_EINVAL;
+    HT_TRY(check_q8_shape(q->M, q->K));
+    if (q->M == 0) return HT_OK;
+    HT_TRY(check_q8(q));
+    HT_TRY(check_matrix(y, ldy, q->M, q->K, act_size(yt)));
+    const uint32_t KB = uint32_t(q->K / 64);
+    const int64_t records = q8_groups(q->M) * KB;
+    if ((records + 3) / 4 >= (int64_t(1) << 24)) return HT_ESHAPE;   // the launch's limit on threads
+    const uint32_t grid = uint32_t((records + 3) / 4);
+    const hipStream_t s = hipStream_t(stream);
+    const uint8_t *codes = reinterpret_cast<const uint8_t *>(q->codes);
+    const int64_t Mp = 16 * q8_groups(q->M);
+    if (yt == HT_BF16) q8_values_kernel<<<grid, 256, 0, s>>>(codes, q->scales, q->M, Mp, KB, records, static_cast<uint16_t *>(y), ldy);
+    else q8_values_kernel<<<grid, 256, 0, s>>>(codes, q->scales, q->M, Mp, KB, records, static_cast<float *>(y), ldy);
+    HT_LAUNCH_CHECK();
+    return HT_OK;
+}
+
+extern "C" ht_status ht_add_rms_norm(const void *x, int64_t ldx, int32_t xt, const void *res, int64_t ldr, int32_t rt,
+                                     int64_t M, int64_t K, const float *w, float eps, void *h, int64_t ldh, void *y,
+                                     int64_t ldy, int32_t yt, const ht_q8_rows *q, ht_stream stream) {
+    HT_TRY(check_norm(M, K));
+    if (!act_size(xt) || (res && !act_size(rt)) || (y && !act_size(yt)) || (!y && !q) || (h && !res) || !(eps >= 0.f))
+        return HT_EINVAL;
+    if (q && (q->M != M || q->K != K)) return HT_ESHAPE;
+    if (M == 0) return HT_OK;
+    HT_TRY(check_matrix(x, ldx, M, K, act_size(xt)));
+    if (res) HT_TRY(check_matrix(res, ldr, M, K, act_size(rt)));
+    if (h) HT_TRY(check_matrix(h, ldh, M, K, act_size(rt)));
+    if (y) HT_TRY(check_matrix(y, ldy, M, K, act_size(yt)));
+    if (q) HT_TRY(check_q8(q));
+    if (!w) return HT_EINVAL;
+    if (!al16p(w)) return HT_EALIGN;
+    if (M >= (int64_t(1) << 22)) return HT_ESHAPE;   // the launch's limit on threads (1024 a row)
+    NormArgs a{};
+    a.x = x;
+    a.res = res;
+    a.h = h;
+    a.y = y;
+    a.ldx = ldx;
+    a.ldr = ldr;
+    a.ldh = ldh;
+    a.ldy = ldy;
+    a.w = w;
+    if (q) {
+        a.codes = reinterpret_cast<uint8_t *>(q->codes);
+        a.scales = q->scales;
+    }
+    a.M = M;
+    a.Mp = 16 * q8_groups(M);
+    a.K = int32_t(K);
+    a.y_bf16 = yt == HT_BF16;
+    a.eps = eps;
+    a.inv_k = 1.0f / float(K);
+    const hipStream_t s = hipStream_t(stream);
+#define HT_NORM_CALL(T, V) launch_norm<T, V>(a, xt, rt, s)
+    HT_NORM_SHAPES(K, HT_NORM_CALL);
+#undef HT_NORM_CALL
+    HT_LAUNCH_CHECK();
+    return HT_OK;
+}
+
+extern "C" ht_status ht_add_rms_norm_workspace(int64_t M, int64_t K, size_t *bytes) {
+    if (!bytes) return HT_EINVAL;
+    HT_TRY(check_norm(M, K));
+    const uint32_t grid = norm_bwd_grid(M, K);
+    *bytes = grid > 1 ? size_t(grid) * size_t(K) * sizeof(float) : 0;
+    return HT_OK;
+}
+
+extern "C" ht_status ht_add_rms_norm_backward(const void *dy, int64_t lddy, int32_t yt, const void *h, int64_t ldh,
+                                              int32_t ht, const void *dh, int64_t lddh, int64_t M, int64_t K,
+                                              const float *w, float eps, void *dres, int64_t lddres, void *dx,
+                                              int64_t lddx, float *dw, void *ws, size_t ws_bytes, ht_stream stream) {
+    HT_TRY(check_norm(M, K));
+    if (!act_size(yt) || !act_size(ht) || !(eps >= 0.f) || !w || !dw) return HT_EINVAL;
+    if (!al16p(w) || !al16p(dw) || !al16p(ws)) return HT_EALIGN;
+    const hipStream_t s = hipStream_t(stream);
+    if (M > 0) {
+        const int size = act_size(ht);
+        HT_TRY(check_matrix(dy, lddy, M, K, act_size(yt)));
+        HT_TRY(check_matrix(h, ldh, M, K, size));
+        if (dh) HT_TRY(check_matrix(dh, lddh, M, K, size));
+        HT_TRY(check_matrix(dres, lddres, M, K, size));
+        if (dx) HT_TRY(check_matrix(dx, lddx, M, K, 6 - size));
+        size_t need = 0;
+        HT_TRY(ht_add_rms_norm_workspace(M, K, &need));
+        if (need && (!ws || ws_bytes < need)) return HT_ESMALL;
+        const uint32_t grid = norm_bwd_grid(M, K);
+        NormBwdArgs a{};
+        a.dy = dy;
+        a.h = h;
+        a.dh = dh;
+        a.dres = dres;
+        a.dx = dx;
+        a.lddy = lddy;
+        a.ldh = ldh;
+        a.lddh = lddh;
+        a.lddres = lddres;
+        a.lddx = lddx;
+        a.w = w;
+        a.part = grid > 1 ? static_cast<float *>(ws) : dw;
+        a.M = M;
+        a.K = int32_t(K);
+        a.eps = eps;
+        a.inv_k = 1.0f / float(K);
+#define HT_NORM_CALL(T, V) launch_norm_bwd<T, V>(a, grid, yt, ht, s)
+        HT_NORM_SHAPES(K, HT_NORM_CALL);
+#undef HT_NORM_CALL
+        HT_LAUNCH_CHECK();
+        if (grid == 1) return HT_OK;
+        norm_dw_kernel<<<uint32_t((K + 15) / 16), 1024, 0, s>>>(static_cast<const float *>(ws), int(grid), int(K), dw);
+    } else {
+        norm_dw_kernel<<<uint32_t((K + 15) / 16), 1024, 0, s>>>(nullptr, 0, int(K), dw);   // no rows: zeros
+    }
+    HT_LAUNCH_CHECK();
+    return HT_OK;
+}

@@ -1,0 +1,71 @@
+// rows.h -- rows of fp32 or bfloat16 values: loads and stores of 8 and 16-byte
+// pieces, and the checks of 8-bit rows, shared by the norm (norm.hip), the
+// linear that takes 8-bit rows (gemm_i8.hip) and the operators over logits.
+#pragma once
+#include "kv.h"
+
+namespace ht {
+
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+
+struct Row8 {
+    float v[8];
+};
+
+__device__ __forceinline__ float bf_lo(uint32_t u) { return __uint_as_float(u << 16); }
+__device__ __forceinline__ float bf_hi(uint32_t u) { return __uint_as_float(u & 0xFFFF0000u); }
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    return uint32_t(f32_to_bf16_rne(lo)) | (uint32_t(f32_to_bf16_rne(hi)) << 16);
+}
+
+// 8 consecutive values, 16-byte aligned.
+__device__ __forceinline__ Row8 load8(const float *p) {
+    const f32x4 a = reinterpret_cast<const f32x4 *>(p)[0], b = reinterpret_cast<const f32x4 *>(p)[1];
+    return Row8{{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w}};
+}
+__device__ __forceinline__ Row8 load8(const uint16_t *p) {
+    const u32x4 u = *reinterpret_cast<const u32x4 *>(p);
+    return Row8{{bf_lo(u.x), bf_hi(u.x), bf_lo(u.y), bf_hi(u.y), bf_lo(u.z), bf_hi(u.z), bf_lo(u.w), bf_hi(u.w)}};
+}
+__device__ __forceinline__ void store8(float *p, const Row8 &r) {
+    reinterpret_cast<f32x4 *>(p)[0] = f32x4{r.v[0], r.v[1], r.v[2], r.v[3]};
+    reinterpret_cast<f32x4 *>(p)[1] = f32x4{r.v[4], r.v[5], r.v[6], r.v[7]};
+}
+__device__ __forceinline__ void store8(uint16_t *p, const Row8 &r) {
+    *reinterpret_cast<u32x4 *>(p) = u32x4{pack_bf16(r.v[0], r.v[1]), pack_bf16(r.v[2], r.v[3]),
+                                          pack_bf16(r.v[4], r.v[5]), pack_bf16(r.v[6], r.v[7])};
+}
+
+// Sum over a wavefront, the same on all lanes.
+__device__ __forceinline__ float wave_sum(float v) {
+    v = group_sum<16>(v);
+    v += __shfl_xor(v, 16);
+    v += __shfl_xor(v, 32);
+    return v;
+}
+
+// Host check of a matrix of rows: ld >= K, pointer and stride in 16-byte pieces.
+inline ht_status check_matrix(const void *p, int64_t ld, int64_t M, int64_t K, int size) {
+    if (!p) return HT_EINVAL;
+    if (M > 1 && ld < K) return HT_ESHAPE;
+    if (!al16p(p) || (M > 1 && (ld * size) % 16)) return HT_EALIGN;
+    return HT_OK;
+}
+
+inline int64_t q8_groups(int64_t M) { return (M + 15) / 16; }
+
+inline ht_status check_q8_shape(int64_t M, int64_t K) {
+    if (M < 0 || M > (int64_t(1) << 30) || K <= 0 || K % 64 || K > (1 << 20)) return HT_ESHAPE;
+    return HT_OK;
+}
+
+inline ht_status check_q8(const ht_q8_rows *q) {
+    if (!q || !q->codes || !q->scales) return HT_EINVAL;
+    const ht_status st = check_q8_shape(q->M, q->K);
+    if (st != HT_OK) return st;
+    if (!al16p(q->codes) || !al16p(q->scales)) return HT_EALIGN;
+    return HT_OK;
+}
+
+}  // namespace ht

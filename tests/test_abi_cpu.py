@@ -513,3 +513,20 @@ def test_refresh_argument_checks(orc):
     with pytest.raises(B.HTError) as e:
         B.ht_refresh_desc(256, 256, 16, c, buf, buf_bytes=size - 1)
     assert e.value.code == 4
+
+
+@pytest.mark.parametrize("path", [B.HT_PATH_GEMM_I8, B.HT_PATH_W8A8])
+@pytest.mark.parametrize("N,K", [(38400, 1024), (20480, 2048), (4096, 4096)])
+def test_int8_workspace_holds_the_last_chunk(path, N, K):
+    """Rows beyond 8192 run as a further launch, which may be split along K
+    where the launches before it are not: its partial sums need room too."""
+    total = N * K // 64
+    d = all_int8(N, K, total)
+    for last in (1, 64, 128, 1000, 8191):
+        assert B.ht_linear_workspace(d, 8192 + last, path) >= B.ht_linear_workspace(d, last, path)
+
+
+def all_int8(N, K, blocks):
+    """Descriptor of a weight whose blocks are all INT8, at an address nobody
+    reads (ht_refresh_desc enqueues nothing)."""
+    return B.ht_refresh_desc(N, K, 16, [0, blocks, 0, 0, 0], 0x10000, buf_bytes=1 << 32)
