@@ -14,6 +14,11 @@ paged cache of keys and values in 8 bits (formats and formulas in ht.h):
     q, k = qk_norm_rope(q, k, step.positions, inv_freq, q_weight=..., k_weight=...)
     kv_write(k, v, step.slots, codes, scales)
     o    = kv_attention(q, codes, scales, table, step.cu_q, step.kv_len, max_q)
+
+between two layers and around the last linear (formulas in ht.h):
+
+    y, h = add_rms_norm(x, weight, residual)               # y bf16 for the next linear
+    rows, h = add_rms_norm_q8(x, weight, residual)         # or 8-bit rows: linear(pw, rows)
 """
 from __future__ import annotations
 
@@ -124,8 +129,11 @@ def workspace(nbytes: int, device) -> torch.Tensor | None:
     return _aligned_empty(nbytes, device)
 
 
-def linear(pw: PackedLinear, x: torch.Tensor, act: int = B.HT_ACT_NONE, out: torch.Tensor | None = None,
+def linear(pw: PackedLinear, x, act: int = B.HT_ACT_NONE, out: torch.Tensor | None = None,
            ws: torch.Tensor | None = None, path: int = B.HT_PATH_AUTO, stream=None) -> torch.Tensor:
+    """x: bf16 [M, K], or Q8Rows (ht_linear_forward_q8, which takes no path)."""
+    if isinstance(x, Q8Rows):
+        return _linear_q8(pw, x, act, out, ws, path, stream)
     M = x.shape[0]
     y = torch.empty((M, pw.N), dtype=torch.float32, device=x.device) if out is None else out
     if ws is None:
@@ -470,3 +478,172 @@ def kv_attention(q: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, tab
     B.ht_kv_attention(q, desc, table, cu_q, kv_len, max_q, max_kv, 1.0 / math.sqrt(D) if scale is None else scale,
                       causal, window, out, ws=ws)
     return out
+
+
+# -----------------------------------------------------------------------------
+# Between two layers, and around the last linear
+# -----------------------------------------------------------------------------
+class Q8Rows(NamedTuple):
+    """Rows in 8 bits with a scale per 64 columns, as the W8A8 linear takes
+    them (ht_q8_rows)."""
+    codes: torch.Tensor       # int8 [ceil(M / 16), K / 64, 64, 16]
+    scales: torch.Tensor      # fp32 [K / 64, 16 * ceil(M / 16)]
+    M: int
+
+
+def q8_rows(M: int, K: int, device) -> Q8Rows:
+    """Buffers for 8-bit rows [M, K]."""
+    B.ht_q8_bytes(M, K)       # refuses what the kernels do not take
+    G = -(-M // 16)
+    return Q8Rows(torch.empty(G, K // 64, 64, 16, dtype=torch.int8, device=device),
+                  torch.empty(K // 64, 16 * G, dtype=torch.float32, device=device), int(M))
+
+
+def _q8_desc(q: Q8Rows) -> B.Q8Desc:
+    codes, scales, M = q
+    G, KB = -(-M // 16), codes.shape[1] if codes.dim() == 4 else -1
+    _need(codes, "codes", torch.int8, (G, KB, 64, 16))
+    _need(scales, "scales", torch.float32, (KB, 16 * G))
+    return B.Q8Desc(codes.data_ptr(), scales.data_ptr(), M, 64 * KB)
+
+
+def q8_values(q: Q8Rows, dtype=torch.bfloat16, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """The values of 8-bit rows, [M, K] bf16 (where they are exact) or fp32
+    (ht_q8_values)."""
+    if stream is not None:
+        with _using(stream):
+            return q8_values(q, dtype, out)
+    desc = _q8_desc(q)
+    if dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError(f"dtype: expected fp32 or bf16, got {dtype}")
+    if out is None:
+        out = torch.empty(desc.M, desc.K, dtype=dtype, device=q.codes.device)
+    else:
+        _out_matrix(out, "out", (desc.M, desc.K), dtype)
+    _on_gpu(q.codes, q.scales, out)
+    B.ht_q8_values(desc, out)
+    return out
+
+
+def _linear_q8(pw: PackedLinear, x: Q8Rows, act, out, ws, path, stream) -> torch.Tensor:
+    if stream is not None:
+        with _using(stream):
+            return _linear_q8(pw, x, act, out, ws, path, None)
+    if path != B.HT_PATH_AUTO:
+        raise ValueError("8-bit rows take no path")
+    desc = _q8_desc(x)
+    if out is None:
+        out = torch.empty(desc.M, pw.N, dtype=torch.float32, device=x.codes.device)
+    else:
+        _out_matrix(out, "out", (desc.M, pw.N), torch.float32)
+    _on_gpu(pw.buf, x.codes, x.scales, out, ws)
+    if desc.M == 0:
+        return out
+    if ws is None:
+        ws = workspace(B.ht_linear_q8_workspace(pw.desc, desc.M), out.device)
+    B.ht_linear_forward_q8(pw.desc, desc, out, act=act, ws=ws)
+    return out
+
+
+def _matrix(t: torch.Tensor, name: str, shape=None) -> torch.Tensor:
+    """[M, K] fp32 or bf16 as the kernels read it: dense rows, pointer and
+    stride in whole 16-byte pieces (a copy where they are not)."""
+    s, dt = t.shape, t.dtype
+    if len(s) != 2 or (dt is not torch.float32 and dt is not torch.bfloat16):
+        raise ValueError(f"{name}: expected fp32 or bf16 [rows, columns], got {dt} {tuple(s)}")
+    if shape is not None and s != shape:
+        raise ValueError(f"{name}: expected {tuple(shape)}, got {tuple(s)}")
+    ld, cs = t.stride()
+    if cs == 1 and (s[0] == 1 or (ld >= s[1] and not ld & (3 if dt is torch.float32 else 7))) and not t.data_ptr() & 15:
+        return t
+    return t.clone(memory_format=torch.contiguous_format)
+
+
+def _out_matrix(t: torch.Tensor, name: str, shape, dtype) -> torch.Tensor:
+    if t.dtype is not dtype or t.shape != shape or (t.stride(1) != 1 and t.shape[1] != 1):
+        raise ValueError(f"{name}: expected {dtype} {tuple(shape)} with dense rows, got {t.dtype} {tuple(t.shape)}")
+    return t
+
+
+def _norm_args(x, weight, residual):
+    x = _matrix(x, "x")
+    if residual is not None:
+        residual = _matrix(residual, "residual", x.shape)
+    _need(weight, "weight", torch.float32, x.shape[1:])
+    return x, residual
+
+
+def add_rms_norm(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor | None = None, eps: float = 1e-6,
+                 out_dtype=None, out=None, stream=None) -> tuple:
+    """(y, h): h = x + residual in residual's type (None without one) and the
+    norm y of it times weight fp32 [K], in out_dtype (bf16 by default, what
+    the next linear takes), in one pass (ht_add_rms_norm).  x and residual
+    [M, K] fp32 or bf16, each its own type; out: (y, h), which may be x and
+    residual themselves."""
+    if stream is not None:
+        with _using(stream):
+            return add_rms_norm(x, weight, residual, eps, out_dtype, out)
+    x, residual = _norm_args(x, weight, residual)
+    dt = torch.bfloat16 if out_dtype is None else out_dtype
+    if dt not in (torch.float32, torch.bfloat16):
+        raise ValueError(f"out_dtype: expected fp32 or bf16, got {dt}")
+    if out is None:
+        y = torch.empty(x.shape, dtype=dt, device=x.device)
+        h = torch.empty(x.shape, dtype=residual.dtype, device=x.device) if residual is not None else None
+    else:
+        y = _out_matrix(out[0], "out[0]", x.shape, dt)
+        h = _out_matrix(out[1], "out[1]", x.shape, residual.dtype) if residual is not None else None
+    _on_gpu(x, residual, weight, y, h)
+    B.ht_add_rms_norm(x, residual, weight, eps, h, y)
+    return y, h
+
+
+def add_rms_norm_q8(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor | None = None, eps: float = 1e-6,
+                    out=None, stream=None) -> tuple:
+    """(rows, h) as add_rms_norm, the norm as Q8Rows for linear(); K % 64 == 0.
+    out: (q8_rows(M, K), h)."""
+    if stream is not None:
+        with _using(stream):
+            return add_rms_norm_q8(x, weight, residual, eps, out)
+    x, residual = _norm_args(x, weight, residual)
+    if out is None:
+        q = q8_rows(*x.shape, x.device)
+        h = torch.empty(x.shape, dtype=residual.dtype, device=x.device) if residual is not None else None
+    else:
+        q, h = out[0], _out_matrix(out[1], "out[1]", x.shape, residual.dtype) if residual is not None else None
+    desc = _q8_desc(q)
+    _on_gpu(x, residual, weight, q.codes, q.scales, h)
+    B.ht_add_rms_norm(x, residual, weight, eps, h, None, desc)
+    return q, h
+
+
+def add_rms_norm_backward(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tensor, dh: torch.Tensor | None = None,
+                          eps: float = 1e-6, x_dtype=None, out: torch.Tensor | None = None,
+                          ws: torch.Tensor | None = None, stream=None) -> tuple:
+    """(dx, dresidual, dweight) of add_rms_norm: dy the gradient of y, h what
+    the norm saw (x where there was no residual), dh the gradient h has from
+    elsewhere, in h's type.  dx in x_dtype (h's by default) is dresidual itself
+    where the types agree; dweight fp32 [K].  out: dresidual's buffer."""
+    if stream is not None:
+        with _using(stream):
+            return add_rms_norm_backward(dy, h, weight, dh, eps, x_dtype, out, ws)
+    h, _ = _norm_args(h, weight, None)
+    dy = _matrix(dy, "dy", h.shape)
+    if dh is not None:
+        if dh.dtype != h.dtype:
+            raise ValueError(f"dh: expected h's type {h.dtype}, got {dh.dtype}")
+        dh = _matrix(dh, "dh", h.shape)
+    dt = h.dtype if x_dtype is None else x_dtype
+    if dt not in (torch.float32, torch.bfloat16):
+        raise ValueError(f"x_dtype: expected fp32 or bf16, got {dt}")
+    if out is None:
+        dres = torch.empty(h.shape, dtype=h.dtype, device=h.device)
+    else:
+        dres = _out_matrix(out, "out", h.shape, h.dtype)
+    dx = None if dt is h.dtype else torch.empty(h.shape, dtype=dt, device=h.device)
+    dw = torch.empty_like(weight)
+    _on_gpu(dy, h, dh, weight, dres, ws)
+    if ws is None:
+        ws = _scratch(B.ht_add_rms_norm_workspace(*h.shape), h.device)
+    B.ht_add_rms_norm_backward(dy, h, dh, weight, eps, dres, dx, dw, ws=ws)
+    return dres if dx is None else dx, dres, dw

@@ -35,7 +35,9 @@ EXPORTS = ("ht_status_string", "ht_plan_params_default", "ht_plan", "ht_plan_cou
            "ht_mlp_workspace", "ht_workspace_init", "ht_mlp_forward",
            "ht_kv_cache_bytes", "ht_kv_plan", "ht_kv_release", "ht_qk_norm_rope", "ht_qk_norm_rope_workspace",
            "ht_qk_norm_rope_backward", "ht_kv_write", "ht_kv_attention_workspace", "ht_kv_attention_kernels",
-           "ht_kv_attention")
+           "ht_kv_attention",
+           "ht_q8_bytes", "ht_q8_values", "ht_linear_q8_workspace", "ht_linear_forward_q8",
+           "ht_add_rms_norm", "ht_add_rms_norm_workspace", "ht_add_rms_norm_backward")
 
 
 class HTError(RuntimeError):
@@ -63,6 +65,11 @@ class KVCacheDesc(ctypes.Structure):
     """ht_kv_cache."""
     _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("n_pages", ctypes.c_int64),
                 ("n_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32)]
+
+
+class Q8Desc(ctypes.Structure):
+    """ht_q8_rows."""
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("M", ctypes.c_int64), ("K", ctypes.c_int64)]
 
 
 _lib = None
@@ -157,6 +164,22 @@ def load() -> ctypes.CDLL:
     lib.ht_kv_attention.restype = St
     lib.ht_kv_attention.argtypes = [P, I64, I64, I64, I32, PC, P, I64, I64, P, P, I64, I64, I64, F, I32, I64, P, I64,
                                     I64, P, Sz, P]
+    PQ = ctypes.POINTER(Q8Desc)
+    lib.ht_q8_bytes.restype = St
+    lib.ht_q8_bytes.argtypes = [I64, I64, PSz, PSz]
+    lib.ht_q8_values.restype = St
+    lib.ht_q8_values.argtypes = [PQ, P, I64, I32, P]
+    lib.ht_linear_q8_workspace.restype = St
+    lib.ht_linear_q8_workspace.argtypes = [ctypes.POINTER(PackedWeight), I64, PSz]
+    lib.ht_linear_forward_q8.restype = St
+    lib.ht_linear_forward_q8.argtypes = [ctypes.POINTER(PackedWeight), PQ, P, I64, I32, P, Sz, P]
+    lib.ht_add_rms_norm.restype = St
+    lib.ht_add_rms_norm.argtypes = [P, I64, I32, P, I64, I32, I64, I64, P, F, P, I64, P, I64, I32, PQ, P]
+    lib.ht_add_rms_norm_workspace.restype = St
+    lib.ht_add_rms_norm_workspace.argtypes = [I64, I64, PSz]
+    lib.ht_add_rms_norm_backward.restype = St
+    lib.ht_add_rms_norm_backward.argtypes = [P, I64, I32, P, I64, I32, P, I64, I64, I64, P, F, P, I64, P, I64, P, P, Sz,
+                                             P]
     _lib = lib
     return lib
 
@@ -452,3 +475,55 @@ def ht_kv_attention(q, desc: KVCacheDesc, table, cu_q, kv_len, max_q: int, max_k
     _check("ht_kv_attention", load().ht_kv_attention(
         *_heads(q), T, n_q, ctypes.byref(desc), table.data_ptr(), P, _ld(table), cu_q.data_ptr(), kv_len.data_ptr(), R,
         max_q, max_kv, scale, causal, window, *_heads(out), _ptr(ws), wsb, _stream(stream)))
+
+
+# -----------------------------------------------------------------------------
+# Around the last linear
+# -----------------------------------------------------------------------------
+def _mat(t) -> tuple:
+    """(pointer, row stride) of [M, K], zeros for None."""
+    return (0, 0) if t is None else (t.data_ptr(), _ld(t))
+
+
+def ht_q8_bytes(M: int, K: int) -> tuple:
+    """(bytes of the codes, bytes of the scales)."""
+    c, s = ctypes.c_size_t(0), ctypes.c_size_t(0)
+    _check("ht_q8_bytes", load().ht_q8_bytes(M, K, ctypes.byref(c), ctypes.byref(s)))
+    return c.value, s.value
+
+
+def ht_q8_values(q: Q8Desc, y, stream=None) -> None:
+    _check("ht_q8_values", load().ht_q8_values(ctypes.byref(q), *_mat(y), _act(y), _stream(stream)))
+
+
+def ht_linear_q8_workspace(desc: PackedWeight, M: int) -> int:
+    out = ctypes.c_size_t(0)
+    _check("ht_linear_q8_workspace", load().ht_linear_q8_workspace(ctypes.byref(desc), M, ctypes.byref(out)))
+    return out.value
+
+
+def ht_linear_forward_q8(desc: PackedWeight, x: Q8Desc, y, act: int = HT_ACT_NONE, ws=None, stream=None) -> None:
+    wsb = ws.numel() * ws.element_size() if ws is not None else 0
+    _check("ht_linear_forward_q8", load().ht_linear_forward_q8(ctypes.byref(desc), ctypes.byref(x), *_mat(y), act,
+                                                               _ptr(ws), wsb, _stream(stream)))
+
+
+def ht_add_rms_norm(x, res, w, eps: float, h, y, q: Q8Desc | None = None, stream=None) -> None:
+    M, K = x.shape
+    _check("ht_add_rms_norm", load().ht_add_rms_norm(
+        *_mat(x), _act(x), *_mat(res), HT_FP32 if res is None else _act(res), M, K, w.data_ptr(), eps, *_mat(h),
+        *_mat(y), HT_FP32 if y is None else _act(y), None if q is None else ctypes.byref(q), _stream(stream)))
+
+
+def ht_add_rms_norm_workspace(M: int, K: int) -> int:
+    out = ctypes.c_size_t(0)
+    _check("ht_add_rms_norm_workspace", load().ht_add_rms_norm_workspace(M, K, ctypes.byref(out)))
+    return out.value
+
+
+def ht_add_rms_norm_backward(dy, h, dh, w, eps: float, dres, dx, dw, ws=None, stream=None) -> None:
+    M, K = h.shape
+    wsb = ws.numel() * ws.element_size() if ws is not None else 0
+    _check("ht_add_rms_norm_backward", load().ht_add_rms_norm_backward(
+        *_mat(dy), _act(dy), *_mat(h), _act(h), *_mat(dh), M, K, w.data_ptr(), eps, *_mat(dres), *_mat(dx),
+        dw.data_ptr(), _ptr(ws), wsb, _stream(stream)))

@@ -186,7 +186,7 @@ struct I8Args {
     const uint8_t *q;         // x planes
     const float *rs;          // x row scales (two-plane encoding), or
     const float *sx;          // x block scales [KB][Mp] (W8A8 encoding)
-    uint32_t Mp;
+    uint32_t Mp, rows;        // their stride, and the rows of them from sx on
     float *y;                 // fp32 output, or
     uint16_t *ybf;            // bfloat16 output (round to nearest even), or
     float *partial;           // per-split partial sums [S][M][N] (no activation)
@@ -284,7 +284,7 @@ __global__ __launch_bounds__(kI8Threads) void gemm_i8_kernel(I8Args a) {
         if constexpr (W8) {
             lds_copy16(a.q + (uint64_t(ga) * KB + kb) * 1024u + 16u * lane, S + wave * 1024u);
             if (wave == 4 || wave == 5)
-                lds_copy4(a.sx + uint64_t(kb) * a.Mp + min(m0 + 64u * (wave - 4u) + lane, a.Mp - 1u),
+                lds_copy4(a.sx + uint64_t(kb) * a.Mp + min(m0 + 64u * (wave - 4u) + lane, a.rows - 1u),
                           S + kI8A / 2 + (wave - 4u) * 256u);
         } else {
             const uint8_t *qa = a.q + ((uint64_t(ga) * KB + kb) * 2u) * 1024u + 16u * lane;
@@ -528,33 +528,48 @@ I8Plan i8_plan(const ht_packed_weight *w, int64_t Mt) {
 
 bool i8_ok(const ht_packed_weight *w) { return w->row_tile == 16; }
 
-size_t i8_ws(const ht_packed_weight *w, int64_t M, bool w8) {
+size_t i8_ws(const ht_packed_weight *w, int64_t M, bool w8, bool encoded) {
     // the last chunk, of fewer rows, may be split along K where the others are not
     size_t most = 0;
     for (const int64_t Mt : {M < kI8ChunkRows ? M : kI8ChunkRows, M % kI8ChunkRows}) {
         if (Mt == 0) continue;
         const I8Plan P = i8_plan(w, Mt);
-        const size_t n = i8_layout(w, Mt, P.S, P.mode != kNone, w8).total;
+        const size_t n = i8_layout(w, Mt, P.S, P.mode != kNone && !encoded, w8).total;
         most = n > most ? n : most;
     }
     return most;
 }
 
+bool i8_reads_x(const ht_packed_weight *w, int64_t M) {
+    for (const int64_t Mt : {M < kI8ChunkRows ? M : kI8ChunkRows, M % kI8ChunkRows})
+        if (Mt != 0 && i8_plan(w, Mt).mode != kAll8) return true;
+    return false;
+}
+
+bool i8_takes(const ht_packed_weight *w, int64_t M) {
+    return i8_ok(w) && i8_plan(w, M < kI8ChunkRows ? M : kI8ChunkRows).mode != kNone;
+}
+
 ht_status run_gemm_i8(const ht_packed_weight *w, const uint16_t *x, int64_t M, int64_t ldx, float *y, uint16_t *ybf,
-                      int64_t ldy, int act, void *ws, hipStream_t s, bool w8) {
+                      int64_t ldy, int act, void *ws, hipStream_t s, bool w8, const ht_q8_rows *xq) {
     uint8_t *wsb = static_cast<uint8_t *>(ws);
     for (int64_t m0 = 0; m0 < M; m0 += kI8ChunkRows) {
         const int64_t Mt = M - m0 < kI8ChunkRows ? M - m0 : kI8ChunkRows;
         const I8Plan P = i8_plan(w, Mt);
         const uint32_t S = P.S;
-        const I8Layout Lw = i8_layout(w, Mt, S, P.mode != kNone, w8);
+        const I8Layout Lw = i8_layout(w, Mt, S, P.mode != kNone && !xq, w8);
         float *yc = y ? y + m0 * ldy : nullptr;
         uint16_t *ybc = ybf ? ybf + m0 * ldy : nullptr;
         float *part = reinterpret_cast<float *>(wsb + Lw.partial);
         if (P.mode != kNone) {
             const uint32_t G = uint32_t((Mt + 15) / 16);
             I8Args a;
-            if (w8) {
+            if (xq) {
+                a.q = reinterpret_cast<const uint8_t *>(xq->codes) + uint64_t(m0 / 16) * uint64_t(w->K / kBlockK) * 1024u;
+                a.rs = nullptr;
+                a.sx = xq->scales + m0;
+                a.Mp = uint32_t(16 * ((M + 15) / 16));
+            } else if (w8) {
                 Xq8Args q;
                 q.x = x + m0 * ldx;
                 q.ldx = ldx;
@@ -591,6 +606,7 @@ ht_status run_gemm_i8(const ht_packed_weight *w, const uint16_t *x, int64_t M, i
             a.ldy = ldy;
             a.M = uint32_t(Mt);
             a.G = G;
+            a.rows = 16u * G;
             a.KBs = (a.w.KB + S - 1) / S;
             a.MT = uint32_t((Mt + kI8BM - 1) / kI8BM);
             a.NT = uint32_t((a.w.N + kI8TileRows - 1) / kI8TileRows);

@@ -339,6 +339,53 @@ extern "C" ht_status ht_linear_forward(const ht_packed_weight *w, const uint16_t
     return run_linear(w, x, M, ldx, y, nullptr, ldy, act, ws, s);
 }
 
+// Workspace of the linear over 8-bit rows: their values in bfloat16 where a
+// bfloat16 kernel reads them, then that of the path.
+struct Q8Plan {
+    bool int8;          // the int8 matrix cores take part
+    int32_t path;       // else: the path of the linear over the values
+    size_t values, total;
+};
+
+static Q8Plan q8_plan(const ht_packed_weight *w, int64_t M) {
+    Q8Plan p;
+    // few rows: the kernels for those read the weight faster than the int8 tiles of 128 rows
+    p.int8 = M > 32 && i8_takes(w, M);
+    p.path = auto_linear_path(w, M);
+    const bool values = !p.int8 || i8_reads_x(w, M);
+    p.values = values ? align256(size_t(M) * size_t(w->K) * 2) : 0;
+    p.total = p.values + (p.int8 ? i8_ws(w, M, true, true) : path_ws(w, M, p.path));
+    return p;
+}
+
+extern "C" ht_status ht_linear_q8_workspace(const ht_packed_weight *w, int64_t M, size_t *bytes) {
+    if (!bytes || !desc_ok(w)) return HT_EINVAL;
+    if (M <= 0) return HT_ESHAPE;
+    *bytes = q8_plan(w, M).total;
+    return HT_OK;
+}
+
+extern "C" ht_status ht_linear_forward_q8(const ht_packed_weight *w, const ht_q8_rows *x, float *y, int64_t ldy,
+                                          int32_t act, void *ws, size_t ws_bytes, ht_stream stream) {
+    if (!desc_ok(w) || !x || !x->codes || !x->scales || !y) return HT_EINVAL;
+    if (act != HT_ACT_NONE && act != HT_ACT_RELU) return HT_EINVAL;
+    const int64_t M = x->M;
+    if (M <= 0 || M > (int64_t(1) << 30) || x->K != w->K || ldy < w->N) return HT_ESHAPE;
+    if (!al16(x->codes) || !al16(x->scales) || !al16(y) || !al16(w->base)) return HT_EALIGN;
+    const Q8Plan p = q8_plan(w, M);
+    if (p.total && (!ws || ws_bytes < p.total)) return HT_ESMALL;
+    if (ws && !al16(ws)) return HT_EALIGN;
+    uint16_t *xv = p.values ? static_cast<uint16_t *>(ws) : nullptr;
+    if (xv) {
+        const ht_status st = ht_q8_values(x, xv, w->K, HT_BF16, stream);
+        if (st != HT_OK) return st;
+    }
+    void *rest = ws ? static_cast<uint8_t *>(ws) + p.values : nullptr;
+    const hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+    if (p.int8) return run_gemm_i8(w, xv, M, w->K, y, nullptr, ldy, act, rest, s, true, x);
+    return ht_linear_forward(w, xv, M, w->K, y, ldy, act, p.path, rest, ws_bytes - p.values, stream);
+}
+
 extern "C" ht_status ht_linear_backward_workspace(const ht_packed_weight *w, int64_t M, size_t *bytes) {
     if (!bytes || !desc_ok(w)) return HT_EINVAL;
     if (M <= 0) return HT_ESHAPE;

@@ -391,10 +391,10 @@ extern "C" ht_status ht_add_rms_norm(const void *x, int64_t ldx, int32_t xt, con
                                      int64_t M, int64_t K, const float *w, float eps, void *h, int64_t ldh, void *y,
                                      int64_t ldy, int32_t yt, const ht_q8_rows *q, ht_stream stream) {
     HT_TRY(check_norm(M, K));
-    if (!act_size(xt) || (res && !act_size(rt)) || (y && !act_size(yt)) || (!y && !q) || (h && !res) || !(eps >= 0.f))
-        return HT_EINVAL;
+    if (!act_size(xt) || (res && !act_size(rt)) || (y && !act_size(yt)) || !(eps >= 0.f)) return HT_EINVAL;
     if (q && (q->M != M || q->K != K)) return HT_ESHAPE;
     if (M == 0) return HT_OK;
+    if ((!y && !q) || (h && !res)) return HT_EINVAL;
     HT_TRY(check_matrix(x, ldx, M, K, act_size(xt)));
     if (res) HT_TRY(check_matrix(res, ldr, M, K, act_size(rt)));
     if (h) HT_TRY(check_matrix(h, ldh, M, K, act_size(rt)));

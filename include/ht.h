@@ -604,6 +604,80 @@ ht_status ht_kv_attention(const uint16_t *q, int64_t ldq, int64_t hsq, int64_t T
 ht_status ht_kv_attention_kernels(const ht_kv_cache *cache, int64_t T, int64_t R, int32_t n_q, int64_t max_q,
                                   int64_t max_kv, int64_t window, int32_t *info);
 
+/* ---------------------------------------------------------------------------
+ * Around the last linear: the norm between layers with the residual's
+ * addition, what rows of logits say, and the loss against a teacher.
+ *
+ * Conventions of these calls, beside the ones at the top of this file: `dtype`
+ * arguments are HT_FP32 or HT_BF16; rows of activations start at 16-byte
+ * aligned addresses (pointer and row stride); rows of logits need no alignment
+ * beyond their type's, any number of columns and any row stride.
+ * ------------------------------------------------------------------------- */
+
+/* 8-bit rows [M][K]: the encoding HT_PATH_W8A8 makes of x, in the order in which
+ * its kernel takes it.  Per row and 64 columns one scale: 2^(E-1) <= max |v| <
+ * 2^E, code = clamp(rne(v 2^(7-E)), -127, 127), value = code 2^(E-7); an all-zero
+ * block has scale 1, one that holds Inf or NaN a NaN scale and codes 0.
+ *   codes   int8 [ceil(M/16)][K/64][64][16]: row m, column 64 kb + e at
+ *           [m / 16][kb][m % 16 + 16 (e / 16)][e % 16];
+ *   scales  fp32 [K/64][16 ceil(M/16)]: row m's at [kb][m].
+ * Entries of the rows past M in the last group of 16 are neither written nor
+ * used. */
+typedef struct {
+    int8_t *codes;               /* 16-byte aligned, as the scales */
+    float *scales;
+    int64_t M, K;                /* M <= 2^30; K % 64 == 0, K <= 2^20 */
+} ht_q8_rows;
+
+/* ht_q8_bytes -- sizes of the two arrays (host only). */
+ht_status ht_q8_bytes(int64_t M, int64_t K, size_t *codes, size_t *scales);
+
+/* ht_q8_values -- the values 8-bit rows stand for, y [M][ldy] of dtype yt (exact
+ * in either type unless below its normal range). */
+ht_status ht_q8_values(const ht_q8_rows *q, void *y, int64_t ldy, int32_t yt, ht_stream stream);
+
+/* ht_linear_forward_q8 -- the linear over 8-bit rows: y = act(x_hat . W_hat^T), x_hat
+ * the rows' values; fp32 y [M][ldy].  Above 32 rows the weight tiles whose blocks
+ * are all INT8 run as HT_PATH_W8A8 runs them (bitwise its results for x with
+ * these codes), without encoding x; other tiles, and calls of up to 32 rows, run
+ * the bfloat16 kernels over x_hat (exact in bfloat16).
+ *   ws   ht_linear_q8_workspace bytes. */
+ht_status ht_linear_q8_workspace(const ht_packed_weight *w, int64_t M, size_t *bytes);
+ht_status ht_linear_forward_q8(const ht_packed_weight *w, const ht_q8_rows *x, float *y, int64_t ldy, int32_t act,
+                               void *ws, size_t ws_bytes, ht_stream stream);
+
+/* ht_add_rms_norm -- the residual's addition and the root-mean-square norm in
+ * one pass over [M][K] rows:  h = x + res (x itself where res is NULL), the fp32
+ * sum rounded to res's dtype;  y = h / sqrt(mean(h^2) + eps) * w, of the rounded h.
+ *   x, res     dtypes xt and rt;  K % 8 == 0, K <= 32768;  M < 2^22;
+ *   w          fp32 [K];  eps >= 0;
+ *   h          out, dtype rt, or NULL (always without res);
+ *   y          out, dtype yt, or NULL;
+ *   q          (host) out: y as 8-bit rows (K % 64 == 0, q->M == M), or NULL;
+ *              y or q or both.  The codes are of the fp32 values.
+ * h and y may be x or res themselves where dtype and stride are the same.  Sums
+ * and products in fp32, one rounding at the end. */
+ht_status ht_add_rms_norm(const void *x, int64_t ldx, int32_t xt, const void *res, int64_t ldr, int32_t rt, int64_t M,
+                          int64_t K, const float *w, float eps, void *h, int64_t ldh, void *y, int64_t ldy, int32_t yt,
+                          const ht_q8_rows *q, ht_stream stream);
+
+/* ht_add_rms_norm_backward -- its gradients: with r = 1 / sqrt(mean(h^2) + eps),
+ *   d = dh + r w dy - h r^3 / K sum(w dy h),   dw = sum over rows of dy h r;
+ * d is the gradient of x and of res alike.
+ *   dy         gradient of y, dtype yt;
+ *   h          what the norm saw (the call's h, or x without res), dtype ht;
+ *   dh         gradient that h has from elsewhere, dtype ht, or NULL;
+ *   dres       out: d in dtype ht;  dx  out: d in the other dtype, or NULL;
+ *   dw         fp32 [K] out (zeros for M = 0);
+ *   ws         ht_add_rms_norm_workspace bytes: partial sums of dw, added in a
+ *              fixed order (bitwise reproducible).
+ * dres may be dy, h or dh where dtype and stride are the same. */
+ht_status ht_add_rms_norm_workspace(int64_t M, int64_t K, size_t *bytes);
+ht_status ht_add_rms_norm_backward(const void *dy, int64_t lddy, int32_t yt, const void *h, int64_t ldh, int32_t ht,
+                                   const void *dh, int64_t lddh, int64_t M, int64_t K, const float *w, float eps,
+                                   void *dres, int64_t lddres, void *dx, int64_t lddx, float *dw, void *ws,
+                                   size_t ws_bytes, ht_stream stream);
+
 #ifdef __cplusplus
 }
 #endif
