@@ -19,6 +19,8 @@ between two layers and around the last linear (formulas in ht.h):
 
     y, h = add_rms_norm(x, weight, residual)               # y bf16 for the next linear
     rows, h = add_rms_norm_q8(x, weight, residual)         # or 8-bit rows: linear(pw, rows)
+    r = token_logprobs(logits, tokens, top=20)             # r.logprobs, r.entropy, r.top_logprobs, r.top_tokens
+    loss, dlogits = distill_step(logits, r.top_tokens, r.top_logprobs, weight)   # of another model's top ones
 """
 from __future__ import annotations
 
@@ -647,3 +649,156 @@ def add_rms_norm_backward(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tenso
         ws = _scratch(B.ht_add_rms_norm_workspace(*h.shape), h.device)
     B.ht_add_rms_norm_backward(dy, h, dh, weight, eps, dres, dx, dw, ws=ws)
     return dres if dx is None else dx, dres, dw
+
+
+def _logits(t: torch.Tensor) -> torch.Tensor:
+    """[M, V] fp32 or bf16 with dense rows (a copy where they are not)."""
+    s, dt = t.shape, t.dtype
+    if len(s) != 2 or (dt is not torch.float32 and dt is not torch.bfloat16):
+        raise ValueError(f"logits: expected fp32 or bf16 [rows, vocabulary], got {dt} {tuple(s)}")
+    ld, cs = t.stride()
+    if (cs == 1 or s[1] == 1) and (s[0] == 1 or ld >= s[1]):
+        return t
+    return t.clone(memory_format=torch.contiguous_format)
+
+
+def _tokens(t: torch.Tensor, M: int) -> None:
+    if t.dtype is not torch.int32 or t.dim() not in (1, 2) or t.shape[0] != M or not t.is_contiguous():
+        raise ValueError(f"tokens: expected contiguous int32 [{M}] or [{M}, n], got {t.dtype} {tuple(t.shape)}")
+
+
+def _dlogits(logits: torch.Tensor, out: torch.Tensor | None) -> torch.Tensor:
+    if out is None:
+        return torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
+    return _out_matrix(out, "out", logits.shape, logits.dtype)
+
+
+class TokenLogprobs(NamedTuple):
+    """What token_logprobs gives (all fp32 but top_tokens, int32)."""
+    logprobs: torch.Tensor | None   # of the given tokens, in their shape
+    entropy: torch.Tensor           # [M]
+    top_logprobs: torch.Tensor      # [M, top]
+    top_tokens: torch.Tensor        # [M, top]
+    stats: torch.Tensor             # [M, 2], for token_logprobs_backward
+
+
+def token_logprobs(logits: torch.Tensor, tokens: torch.Tensor | None = None, top: int = 0, temperature: float = 1.0,
+                   ws: torch.Tensor | None = None, stream=None) -> TokenLogprobs:
+    """Log probabilities of given tokens, entropy and the `top` most likely
+    tokens of rows of logits [M, V], fp32 or bf16, any row stride, in one pass
+    (ht_token_logprobs).  tokens int32 [M] or [M, n]; one outside [0, V) is not
+    scored (0).  -Inf logits are not allowed ones."""
+    if stream is not None:
+        with _using(stream):
+            return token_logprobs(logits, tokens, top, temperature, ws)
+    logits = _logits(logits)
+    M, V = logits.shape
+    if tokens is not None:
+        _tokens(tokens, M)
+    if not 0 <= top <= min(64, V):
+        raise ValueError(f"top: expected 0 to {min(64, V)}, got {top}")
+    _on_gpu(logits, tokens, ws)
+    new = lambda shape, dt=torch.float32: torch.empty(shape, dtype=dt, device=logits.device)  # noqa: E731
+    r = TokenLogprobs(None if tokens is None else new(tokens.shape), new((M,)), new((M, top)),
+                      new((M, top), torch.int32), new((M, 2)))
+    if ws is None:
+        ws = _scratch(B.ht_token_logprobs_workspace(M, V, top), logits.device)
+    B.ht_token_logprobs(logits, tokens, temperature, *r, ws=ws)
+    return r
+
+
+def token_logprobs_backward(d_logprobs: torch.Tensor | None, d_entropy: torch.Tensor | None, logits: torch.Tensor,
+                            tokens: torch.Tensor | None, stats: torch.Tensor, entropy: torch.Tensor | None = None,
+                            temperature: float = 1.0, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Gradient of the logits, in their type, from those of the given tokens'
+    log probabilities and of the entropy (either may be None); stats and
+    entropy of the forward call.  out may be the logits themselves."""
+    if stream is not None:
+        with _using(stream):
+            return token_logprobs_backward(d_logprobs, d_entropy, logits, tokens, stats, entropy, temperature, out)
+    x = _logits(logits)
+    M = x.shape[0]
+    if (tokens is None) != (d_logprobs is None):
+        raise ValueError("tokens and d_logprobs: both or neither")
+    if tokens is not None:
+        _tokens(tokens, M)
+        _need(d_logprobs, "d_logprobs", torch.float32, tokens.shape)
+    _need(stats, "stats", torch.float32, (M, 2))
+    if d_entropy is not None:
+        _need(d_entropy, "d_entropy", torch.float32, (M,))
+        if entropy is None:
+            raise ValueError("d_entropy needs the entropy of the forward call: both or neither")
+        _need(entropy, "entropy", torch.float32, (M,))
+    out = _dlogits(x, out)
+    _on_gpu(d_logprobs, d_entropy, x, tokens, stats, entropy, out)
+    B.ht_token_logprobs_backward(d_logprobs, d_entropy, x, tokens, stats, entropy, temperature, out)
+    return out
+
+
+def _teacher(logits: torch.Tensor, ids: torch.Tensor, teacher: torch.Tensor) -> None:
+    M = logits.shape[0]
+    if ids.dim() != 2 or not 1 <= ids.shape[1] <= 1024:
+        raise ValueError(f"ids: expected int32 [{M}, 1 to 1024], got {ids.dtype} {tuple(ids.shape)}")
+    _need(ids, "ids", torch.int32, (M, ids.shape[1]))
+    _need(teacher, "teacher", torch.float32, ids.shape)
+
+
+def distill_loss(logits: torch.Tensor, ids: torch.Tensor, teacher: torch.Tensor, temperature: float = 1.0,
+                 stream=None) -> tuple:
+    """(loss, stats) of a student's logits [M, V] against a teacher's top
+    entries: ids int32 [M, k] (outside [0, V): not kept), teacher fp32 [M, k]
+    its logits or log probabilities there (ht_distill_loss).  loss fp32 [M] is
+    the divergence of the softmax over the kept entries from the student's
+    over all, both at the temperature."""
+    if stream is not None:
+        with _using(stream):
+            return distill_loss(logits, ids, teacher, temperature)
+    logits = _logits(logits)
+    _teacher(logits, ids, teacher)
+    M = logits.shape[0]
+    loss, stats = (torch.empty(s, dtype=torch.float32, device=logits.device) for s in ((M,), (M, 2)))
+    _on_gpu(logits, ids, teacher)
+    B.ht_distill_loss(logits, ids, teacher, temperature, loss, stats)
+    return loss, stats
+
+
+def distill_backward(d_loss: torch.Tensor, logits: torch.Tensor, ids: torch.Tensor, teacher: torch.Tensor,
+                     stats: torch.Tensor, temperature: float = 1.0, out: torch.Tensor | None = None,
+                     stream=None) -> torch.Tensor:
+    """Gradient of the student's logits, in their type, from the loss's, fp32
+    [M] (ht_distill_backward).  out may be the logits themselves."""
+    if stream is not None:
+        with _using(stream):
+            return distill_backward(d_loss, logits, ids, teacher, stats, temperature, out)
+    x = _logits(logits)
+    _teacher(x, ids, teacher)
+    _need(d_loss, "d_loss", torch.float32, x.shape[:1])
+    _need(stats, "stats", torch.float32, (x.shape[0], 2))
+    out = _dlogits(x, out)
+    _on_gpu(d_loss, x, ids, teacher, stats, out)
+    B.ht_distill_backward(d_loss, x, ids, teacher, stats, temperature, out)
+    return out
+
+
+def distill_step(logits: torch.Tensor, ids: torch.Tensor, teacher: torch.Tensor, weight: torch.Tensor | None = None,
+                 temperature: float = 1.0, out: torch.Tensor | None = None, stats: torch.Tensor | None = None,
+                 stream=None) -> tuple:
+    """(loss, dlogits): distill_loss and, in the same pass, the gradient of
+    sum(weight * loss), weight fp32 [M] (1 without; rows of weight 0 are not
+    read, their loss is 0) (ht_distill_step).  out may be the logits
+    themselves; stats fp32 [M, 2] gets what distill_backward starts from."""
+    if stream is not None:
+        with _using(stream):
+            return distill_step(logits, ids, teacher, weight, temperature, out, stats)
+    x = _logits(logits)
+    _teacher(x, ids, teacher)
+    M = x.shape[0]
+    if weight is not None:
+        _need(weight, "weight", torch.float32, (M,))
+    if stats is not None:
+        _need(stats, "stats", torch.float32, (M, 2))
+    out = _dlogits(x, out)
+    loss = torch.empty(M, dtype=torch.float32, device=x.device)
+    _on_gpu(x, ids, teacher, weight, out, stats)
+    B.ht_distill_step(x, ids, teacher, weight, temperature, loss, stats, out)
+    return loss, out

@@ -37,7 +37,9 @@ EXPORTS = ("ht_status_string", "ht_plan_params_default", "ht_plan", "ht_plan_cou
            "ht_qk_norm_rope_backward", "ht_kv_write", "ht_kv_attention_workspace", "ht_kv_attention_kernels",
            "ht_kv_attention",
            "ht_q8_bytes", "ht_q8_values", "ht_linear_q8_workspace", "ht_linear_forward_q8",
-           "ht_add_rms_norm", "ht_add_rms_norm_workspace", "ht_add_rms_norm_backward")
+           "ht_add_rms_norm", "ht_add_rms_norm_workspace", "ht_add_rms_norm_backward",
+           "ht_token_logprobs_workspace", "ht_token_logprobs", "ht_token_logprobs_backward",
+           "ht_distill_loss", "ht_distill_backward", "ht_distill_step")
 
 
 class HTError(RuntimeError):
@@ -180,6 +182,18 @@ def load() -> ctypes.CDLL:
     lib.ht_add_rms_norm_backward.restype = St
     lib.ht_add_rms_norm_backward.argtypes = [P, I64, I32, P, I64, I32, P, I64, I64, I64, P, F, P, I64, P, I64, P, P, Sz,
                                              P]
+    lib.ht_token_logprobs_workspace.restype = St
+    lib.ht_token_logprobs_workspace.argtypes = [I64, I64, I32, PSz]
+    lib.ht_token_logprobs.restype = St
+    lib.ht_token_logprobs.argtypes = [P, I64, I32, I64, I64, P, I32, I32, F, P, P, P, P, P, P, Sz, P]
+    lib.ht_token_logprobs_backward.restype = St
+    lib.ht_token_logprobs_backward.argtypes = [P, P, P, I64, I32, I64, I64, P, I32, P, P, F, P, I64, P]
+    lib.ht_distill_loss.restype = St
+    lib.ht_distill_loss.argtypes = [P, I64, I32, I64, I64, P, P, I32, F, P, P, P]
+    lib.ht_distill_backward.restype = St
+    lib.ht_distill_backward.argtypes = [P, P, I64, I32, I64, I64, P, P, I32, P, F, P, I64, P]
+    lib.ht_distill_step.restype = St
+    lib.ht_distill_step.argtypes = [P, I64, I32, I64, I64, P, P, I32, P, F, P, P, P, I64, P]
     _lib = lib
     return lib
 
@@ -527,3 +541,48 @@ def ht_add_rms_norm_backward(dy, h, dh, w, eps: float, dres, dx, dw, ws=None, st
     _check("ht_add_rms_norm_backward", load().ht_add_rms_norm_backward(
         *_mat(dy), _act(dy), *_mat(h), _act(h), *_mat(dh), M, K, w.data_ptr(), eps, *_mat(dres), *_mat(dx),
         dw.data_ptr(), _ptr(ws), wsb, _stream(stream)))
+
+
+def ht_token_logprobs_workspace(M: int, V: int, k: int) -> int:
+    out = ctypes.c_size_t(0)
+    _check("ht_token_logprobs_workspace", load().ht_token_logprobs_workspace(M, V, k, ctypes.byref(out)))
+    return out.value
+
+
+def _count(t) -> int:
+    """Entries per row of [M] or [M, n], 0 for None."""
+    return 0 if t is None else 1 if t.dim() == 1 else t.shape[1]
+
+
+def ht_token_logprobs(logits, tokens, temperature: float, logp, entropy, top, top_tokens, stats, ws=None,
+                      stream=None) -> None:
+    """tokens, logp [M] or [M, n]; top, top_tokens [M, k]; any may be None."""
+    wsb = ws.numel() * ws.element_size() if ws is not None else 0
+    _check("ht_token_logprobs", load().ht_token_logprobs(
+        *_mat(logits), _act(logits), *logits.shape, _ptr(tokens), _count(tokens), _count(top), temperature, _ptr(logp),
+        _ptr(entropy), _ptr(top), _ptr(top_tokens), _ptr(stats), _ptr(ws), wsb, _stream(stream)))
+
+
+def ht_token_logprobs_backward(d_logp, d_entropy, logits, tokens, stats, entropy, temperature: float, dx,
+                               stream=None) -> None:
+    _check("ht_token_logprobs_backward", load().ht_token_logprobs_backward(
+        _ptr(d_logp), _ptr(d_entropy), *_mat(logits), _act(logits), *logits.shape, _ptr(tokens), _count(tokens),
+        stats.data_ptr(), _ptr(entropy), temperature, *_mat(dx), _stream(stream)))
+
+
+def ht_distill_loss(logits, ids, teacher, temperature: float, loss, stats=None, stream=None) -> None:
+    _check("ht_distill_loss", load().ht_distill_loss(
+        *_mat(logits), _act(logits), *logits.shape, ids.data_ptr(), teacher.data_ptr(), ids.shape[1], temperature,
+        loss.data_ptr(), _ptr(stats), _stream(stream)))
+
+
+def ht_distill_backward(d_loss, logits, ids, teacher, stats, temperature: float, dx, stream=None) -> None:
+    _check("ht_distill_backward", load().ht_distill_backward(
+        d_loss.data_ptr(), *_mat(logits), _act(logits), *logits.shape, ids.data_ptr(), teacher.data_ptr(), ids.shape[1],
+        stats.data_ptr(), temperature, *_mat(dx), _stream(stream)))
+
+
+def ht_distill_step(logits, ids, teacher, weight, temperature: float, loss, stats, dx, stream=None) -> None:
+    _check("ht_distill_step", load().ht_distill_step(
+        *_mat(logits), _act(logits), *logits.shape, ids.data_ptr(), teacher.data_ptr(), ids.shape[1], _ptr(weight),
+        temperature, loss.data_ptr(), _ptr(stats), *_mat(dx), _stream(stream)))

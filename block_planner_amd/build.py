@@ -21,7 +21,7 @@ BUILD_DIR = os.path.join(ROOT, "_build")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 SOURCES = ["api.cpp", "plan.hip", "pack.hip", "linear.hip", "gemm.hip", "gemm_xw.hip", "gemm_i8.hip", "gemv_mfma.hip", "mlp.hip", "backward.hip", "bwd_gemm.hip", "noalloc.hip", "refresh.hip",
-           "kv_plan.hip", "qk_rope.hip", "kv_write.hip", "kv_attn.hip", "norm.hip"]
+           "kv_plan.hip", "qk_rope.hip", "kv_write.hip", "kv_attn.hip", "norm.hip", "logprobs.hip", "distill.hip"]
 
 # -packed-fp32-ops off: no v_pk_{add,mul,fma}_f32 are generated.
 COMMON = ["--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-Wall",

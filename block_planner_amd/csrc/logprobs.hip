@@ -1,0 +1,278 @@
+// logprobs.hip -- log probabilities of given tokens, the entropy and the most
+// likely alternatives of every row of logits, in one pass over them.
+//
+//   z = x / temperature;  lse = log sum exp z;  logp(v) = z_v - lse;
+//   H = lse - sum_v p_v z_v;  alternatives: the k largest z, ties by lower index.
+//
+// Bound by HBM: every logit is read once.  A workgroup takes a row, or one of
+// S parts of it where rows are few; each lane keeps (mx, s, t) of its entries,
+// each wavefront its k largest; they meet in LDS, and for parts in a second
+// kernel over the workspace.
+#include "logits.h"
+
+namespace ht {
+
+namespace {
+
+struct LogprobArgs {
+    const void *x;
+    int64_t ld, V, part;        // part: columns per workgroup
+    int32_t S, k, n_tok;
+    float c, inv_t;             // log2(e) / temperature, 1 / temperature
+    const int32_t *tokens;
+    float *logp, *entropy, *top, *stats;
+    int32_t *top_tokens;
+    RowStat *ws_stats;          // [M][S], then
+    uint64_t *ws_top;           // [M][S][k]
+};
+
+// Statistics and largest entries of n entries from p on, whose first has index
+// i0; every wavefront's result in its lanes.
+template <typename T, int NT, int U, bool ENT, bool TOP>
+__device__ __forceinline__ RowStat scan_row(const T *p, int64_t n, uint32_t i0, float c, int k, TopList &list) {
+    using L = LogitType<T>;
+    constexpr int kVec = L::kVec;
+    const int lane = threadIdx.x & 63;
+    const Span sp = span_of(p, n);
+    RowStat r = stat_none();
+    const auto single = [&](const T *q, int count, uint32_t i) {
+        if (threadIdx.x >= 64 || count == 0) return;          // the first wavefront's
+        const bool live = lane < count;
+        const float x = live ? L::get(q + lane) : -__builtin_inff();
+        stat_add<1, ENT>(r, &x, x, c);
+        if constexpr (TOP) list.add<1>(&x, x, i + uint32_t(lane), live, k, lane);
+    };
+    single(p, sp.head, i0);
+    const u32x4 *v = reinterpret_cast<const u32x4 *>(p + sp.head);
+    const u32x4 none = sizeof(T) == 4 ? u32x4{0xFF800000u, 0xFF800000u, 0xFF800000u, 0xFF800000u}
+                                      : u32x4{0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u};   // -Inf
+    u32x4 next[U];
+    const auto load = [&](int32_t at) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int32_t i = at + u * NT + int32_t(threadIdx.x);
+            next[u] = i < sp.vecs ? __builtin_nontemporal_load(v + i) : none;
+        }
+    };
+    load(0);
+    for (int32_t at = 0; at < sp.vecs; at += U * NT) {
+        float x[U * kVec], top[U], most;
+#pragma unroll
+        for (int u = 0; u < U; ++u) L::unpack(next[u], x + u * kVec);
+        if (at + U * NT < sp.vecs) load(at + U * NT);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            top[u] = x[u * kVec];
+#pragma unroll
+            for (int j = 1; j < kVec; ++j) top[u] = fmaxf(top[u], x[u * kVec + j]);
+            most = u ? fmaxf(most, top[u]) : top[u];
+        }
+        stat_add<U * kVec, ENT>(r, x, most, c);
+        if constexpr (TOP) {
+            if (__any(most >= list.thr)) {
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const int32_t i = at + u * NT + int32_t(threadIdx.x);
+                    list.add<kVec>(x + u * kVec, top[u], i0 + uint32_t(sp.head) + uint32_t(i) * kVec, i < sp.vecs, k, lane);
+                }
+            }
+        }
+    }
+    single(p + sp.head + int64_t(sp.vecs) * kVec, sp.tail, i0 + uint32_t(n - sp.tail));
+    if constexpr (TOP) {
+        if (list.pending) list.flush(k, lane);
+    }
+    return stat_wave(r, c);
+}
+
+// The wavefronts' lists and statistics as one, valid in the first wavefront
+// (statistics in all).
+template <int NW, bool TOP>
+__device__ __forceinline__ RowStat meet(RowStat r, float c, uint64_t &list, uint64_t *lists, RowStat *stats) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    __syncthreads();
+    if (lane == 0) stats[wave] = r;
+    if constexpr (TOP) lists[wave * 64 + lane] = list;
+    __syncthreads();
+    r = stats[0];
+#pragma unroll
+    for (int w = 1; w < NW; ++w) r = stat_join(r, stats[w], c);
+    if constexpr (TOP) {
+        for (int w = NW / 2; w > 0; w >>= 1) {
+            if (wave < w) {
+                list = join_lists(list, lists[(wave + w) * 64 + 63 - lane], lane);
+                lists[wave * 64 + lane] = list;
+            }
+            __syncthreads();
+        }
+    }
+    return r;
+}
+
+template <typename T>
+__device__ __forceinline__ void write_row(const LogprobArgs &a, int64_t m, RowStat r, uint64_t list, bool tops) {
+    const RowOut o = row_out(r);
+    const T *row = static_cast<const T *>(a.x) + m * a.ld;
+    for (int j = threadIdx.x; j < a.n_tok; j += blockDim.x) {
+        const int32_t v = a.tokens[m * a.n_tok + j];
+        a.logp[m * a.n_tok + j] = v >= 0 && v < a.V ? logp_of(o, LogitType<T>::get(row + v), a.inv_t) : 0.f;
+    }
+    if (threadIdx.x == 0) {
+        if (a.entropy) a.entropy[m] = o.entropy;
+        if (a.stats) {
+            a.stats[2 * m] = o.mx;
+            a.stats[2 * m + 1] = o.b;
+        }
+    }
+    if (tops && int(threadIdx.x) < a.k) {
+        a.top[m * a.k + threadIdx.x] = logp_of(o, key_value(uint32_t(list >> 32)), a.inv_t);
+        a.top_tokens[m * a.k + threadIdx.x] = o.kind == 2 ? -1 : int32_t(entry_index(list));
+    }
+}
+
+template <typename T, int NT, bool TOP, bool PARTS>
+__global__ __launch_bounds__(NT) void logprob_kernel(LogprobArgs a) {
+    constexpr int NW = NT / 64;
+    __shared__ uint64_t buf[TOP ? NW * 128 : 1];
+    __shared__ RowStat stats[NW];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int64_t m = PARTS ? int64_t(blockIdx.x) / a.S : int64_t(blockIdx.x);
+    const int64_t sl = PARTS ? int64_t(blockIdx.x) - m * a.S : 0;
+    const int64_t c0 = sl * a.part, n = min(a.V - c0, a.part);
+    const T *p = static_cast<const T *>(a.x) + m * a.ld + c0;
+    TopList list;
+    if constexpr (TOP) list.init(buf + wave * 128);
+    RowStat r = scan_row<T, NT, 16 / LogitType<T>::kVec, true, TOP>(p, n, uint32_t(c0), a.c, a.k, list);
+    r = meet<NW, TOP>(r, a.c, list.list, buf, stats);
+    if constexpr (PARTS) {
+        const int64_t rec = m * a.S + sl;
+        if (threadIdx.x == 0) a.ws_stats[rec] = r;
+        if (TOP && wave == 0 && lane < a.k) a.ws_top[rec * a.k + lane] = list.list;
+    } else {
+        write_row<T>(a, m, r, TOP ? list.list : 0, TOP);
+    }
+}
+
+// A row's parts as one: the wavefronts take them in turn.
+template <typename T, bool TOP>
+__global__ __launch_bounds__(256) void logprob_join_kernel(LogprobArgs a) {
+    __shared__ uint64_t lists[TOP ? 256 : 1];
+    __shared__ RowStat stats[4];
+    const int64_t m = blockIdx.x;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    RowStat r = stat_none();
+    for (int i = threadIdx.x; i < a.S; i += 256) r = stat_join(r, a.ws_stats[m * a.S + i], a.c);
+    r = stat_wave(r, a.c);
+    uint64_t list = 0;
+    if constexpr (TOP) {
+        for (int i = wave; i < a.S; i += 4) {
+            const int from = 63 - lane;
+            const uint64_t up = from < a.k ? a.ws_top[(m * a.S + i) * a.k + from] : 0;
+            list = join_lists(list, up, lane);
+        }
+    }
+    r = meet<4, TOP>(r, a.c, list, lists, stats);
+    write_row<T>(a, m, r, list, TOP);
+}
+
+struct LogprobShape {
+    int32_t S;
+    int64_t part;
+};
+
+// Parts of a row: enough workgroups for the card, each of at least 4096
+// entries (one step of its 256 threads).
+LogprobShape logprob_shape(int64_t M, int64_t V) {
+    LogprobShape s{1, V};
+    if (M >= 256) return s;
+    int64_t S = (1024 + M - 1) / M;
+    const int64_t most = (V + 4095) / 4096;
+    if (S > most) S = most;
+    if (S > 256) S = 256;
+    if (S <= 1) return s;
+    s.part = ((V + S - 1) / S + 7) / 8 * 8;    // whole 16-byte pieces
+    s.S = int32_t((V + s.part - 1) / s.part);
+    return s;
+}
+
+template <typename T>
+ht_status launch_logprobs(LogprobArgs &a, int64_t M, hipStream_t s) {
+    const bool top = a.k > 0;
+    if (a.S == 1) {
+        const uint32_t grid = uint32_t(M);
+        if (top) logprob_kernel<T, 256, true, false><<<grid, 256, 0, s>>>(a);
+        else logprob_kernel<T, 256, false, false><<<grid, 256, 0, s>>>(a);
+    } else {
+        const uint32_t grid = uint32_t(M * a.S);
+        if (top) logprob_kernel<T, 256, true, true><<<grid, 256, 0, s>>>(a);
+        else logprob_kernel<T, 256, false, true><<<grid, 256, 0, s>>>(a);
+        HT_LAUNCH_CHECK();
+        if (top) logprob_join_kernel<T, true><<<uint32_t(M), 256, 0, s>>>(a);
+        else logprob_join_kernel<T, false><<<uint32_t(M), 256, 0, s>>>(a);
+    }
+    HT_LAUNCH_CHECK();
+    return HT_OK;
+}
+
+ht_status check_top(int64_t V, int32_t k, int32_t n_tok) {
+    return k < 0 || k > kMaxTop || k > V || n_tok < 0 || n_tok > 1024 ? HT_ESHAPE : HT_OK;
+}
+
+}  // namespace
+}  // namespace ht
+
+using namespace ht;
+
+#define HT_TRY(e)                       \
+    do {                                \
+        const ht_status st_ = (e);      \
+        if (st_ != HT_OK) return st_;   \
+    } while (0)
+
+extern "C" ht_status ht_token_logprobs_workspace(int64_t M, int64_t V, int32_t k, size_t *bytes) {
+    if (!bytes) return HT_EINVAL;
+    HT_TRY(check_logit_shape(M, V, HT_FP32, 1.0f));
+    HT_TRY(check_top(V, k, 0));
+    *bytes = 0;
+    if (M == 0) return HT_OK;
+    const LogprobShape sh = logprob_shape(M, V);
+    if (sh.S > 1) *bytes = align256(size_t(M) * size_t(sh.S) * sizeof(RowStat)) + size_t(M) * size_t(sh.S) * size_t(k) * 8;
+    return HT_OK;
+}
+
+extern "C" ht_status ht_token_logprobs(const void *logits, int64_t ld, int32_t type, int64_t M, int64_t V,
+                                       const int32_t *tokens, int32_t n_tok, int32_t k, float temperature, float *logp,
+                                       float *entropy, float *top, int32_t *top_tokens, float *stats, void *ws,
+                                       size_t ws_bytes, ht_stream stream) {
+    HT_TRY(check_logit_shape(M, V, type, temperature));
+    HT_TRY(check_top(V, k, n_tok));
+    if (M == 0) return HT_OK;
+    HT_TRY(check_logits(logits, ld, M, V, type));
+    if ((n_tok > 0 && (!tokens || !logp)) || (k > 0 && (!top || !top_tokens))) return HT_EINVAL;
+    if (!al4(tokens) || !al4(logp) || !al4(entropy) || !al4(top) || !al4(top_tokens) || !al4(stats) || !al16p(ws))
+        return HT_EALIGN;
+    size_t need = 0;
+    HT_TRY(ht_token_logprobs_workspace(M, V, k, &need));
+    if (need && (!ws || ws_bytes < need)) return HT_ESMALL;
+    const LogprobShape sh = logprob_shape(M, V);
+    LogprobArgs a{};
+    a.x = logits;
+    a.ld = ld;
+    a.V = V;
+    a.part = sh.part;
+    a.S = sh.S;
+    a.k = k;
+    a.n_tok = n_tok;
+    a.c = kLog2e / temperature;
+    a.inv_t = 1.0f / temperature;
+    a.tokens = tokens;
+    a.logp = logp;
+    a.entropy = entropy;
+    a.top = top;
+    a.top_tokens = top_tokens;
+    a.stats = stats;
+    a.ws_stats = static_cast<RowStat *>(ws);
+    if (sh.S > 1) a.ws_top = reinterpret_cast<uint64_t *>(static_cast<uint8_t *>(ws) + align256(size_t(M) * size_t(sh.S) * sizeof(RowStat)));
+    return type == HT_BF16 ? launch_logprobs<uint16_t>(a, M, hipStream_t(stream))
+                           : launch_logprobs<float>(a, M, hipStream_t(stream));
+}

@@ -678,6 +678,75 @@ ht_status ht_add_rms_norm_backward(const void *dy, int64_t lddy, int32_t yt, con
                                    void *dres, int64_t lddres, void *dx, int64_t lddx, float *dw, void *ws,
                                    size_t ws_bytes, ht_stream stream);
 
+/* Rows of logits: x [M][ld] of dtype `type`, V < 2^31 - 64 columns, M <= 2^22,
+ * temperature in [1e-30, 1e30];  z = x / temperature.  Entries of -Inf are not
+ * allowed (probability 0); a row of nothing else has no distribution: log
+ * probabilities of -Inf, entropy 0, gradients of 0.  Entries of the type's
+ * lowest finite value are ordinary ones.  A row that holds NaN or +Inf gives
+ * NaN.  Results of a row do not depend on the others, on ld or on where it
+ * lies, but by rounding; calls are bitwise reproducible.
+ *
+ * ht_token_logprobs -- per row the log probabilities z_v - log sum exp z of given
+ * tokens, the entropy -sum p log p and the most likely tokens, in one pass.
+ *   tokens      int32 [M][n_tok] (0 <= n_tok <= 1024);  logp  fp32 [M][n_tok]
+ *               out; a token outside [0, V) is not scored: 0;
+ *   entropy     fp32 [M] out, or NULL;
+ *   top         fp32 [M][k] out (0 <= k <= 64, k <= V): log probabilities of the k
+ *               largest entries, in order, equal ones by lower token;
+ *   top_tokens  int32 [M][k] out (-1 in rows that hold NaN or +Inf);
+ *   stats       fp32 [M][2] out, or NULL: the largest logit a (-Inf: nothing is
+ *               allowed) and b = log2 sum exp((x - a) / temperature), from which
+ *               the gradients start;  log sum exp z = a / temperature + b log 2;
+ *   ws          ht_token_logprobs_workspace bytes: results of parts of rows.
+ * Natural logarithms; arithmetic in fp32 whatever the type. */
+ht_status ht_token_logprobs_workspace(int64_t M, int64_t V, int32_t k, size_t *bytes);
+ht_status ht_token_logprobs(const void *logits, int64_t ld, int32_t type, int64_t M, int64_t V, const int32_t *tokens,
+                            int32_t n_tok, int32_t k, float temperature, float *logp, float *entropy, float *top,
+                            int32_t *top_tokens, float *stats, void *ws, size_t ws_bytes, ht_stream stream);
+
+/* ht_token_logprobs_backward -- the logits' gradient, of their dtype:
+ *   dx_v = 1 / temperature (sum_{j: token_j = v} g_j - p_v (sum_j g_j + e (log p_v + H)))
+ * with g_j = d_logp (of scored tokens) and e = d_entropy (NULL: 0).
+ *   stats, entropy   of the forward call (entropy only with d_entropy).
+ * A row whose g and e are all 0 gives zeros and is not read.  dx may be the
+ * logits themselves, or lie apart from them. */
+ht_status ht_token_logprobs_backward(const float *d_logp, const float *d_entropy, const void *logits, int64_t ld,
+                                     int32_t type, int64_t M, int64_t V, const int32_t *tokens, int32_t n_tok,
+                                     const float *stats, const float *entropy, float temperature, void *dx, int64_t ldd,
+                                     ht_stream stream);
+
+/* ht_distill_loss -- a student's logits against a teacher's top ones: with p the
+ * softmax of teacher / temperature over a row's kept entries and q that of the
+ * student's logits over all V columns,
+ *   loss = sum_j p_j (log p_j - log q[id_j]).
+ *   ids         int32 [M][k] (1 <= k <= 1024): an id outside [0, V) is not kept;
+ *               an id that comes twice counts twice;
+ *   teacher     fp32 [M][k]: the teacher's logits or log probabilities of them
+ *               (ht_token_logprobs' top); -Inf: no weight;
+ *   loss        fp32 [M] out;  0 where nothing is kept, +Inf where the student
+ *               does not allow what the teacher gives weight;
+ *   stats       fp32 [M][2] out, or NULL, as ht_token_logprobs'. */
+ht_status ht_distill_loss(const void *logits, int64_t ld, int32_t type, int64_t M, int64_t V, const int32_t *ids,
+                          const float *teacher, int32_t k, float temperature, float *loss, float *stats,
+                          ht_stream stream);
+
+/* ht_distill_backward -- the student's gradient from the loss's:
+ *   dx_v = d_loss / temperature (q_v - sum_{j: id_j = v} p_j)
+ * (zeros where nothing is kept or allowed, or d_loss is 0: those rows are not
+ * read).  stats of ht_distill_loss; dx as above. */
+ht_status ht_distill_backward(const float *d_loss, const void *logits, int64_t ld, int32_t type, int64_t M, int64_t V,
+                              const int32_t *ids, const float *teacher, int32_t k, const float *stats,
+                              float temperature, void *dx, int64_t ldd, ht_stream stream);
+
+/* ht_distill_step -- loss and gradient in one call, each logit read once where a
+ * row fits a compute unit's registers (65536 fp32 or 131072 bf16 columns), with
+ * the loss's gradient known beforehand.
+ *   weight      fp32 [M], d_loss of ht_distill_backward, or NULL (1); a row of
+ *               weight 0 is not read: loss 0, gradient 0 (stats 0). */
+ht_status ht_distill_step(const void *logits, int64_t ld, int32_t type, int64_t M, int64_t V, const int32_t *ids,
+                          const float *teacher, int32_t k, const float *weight, float temperature, float *loss,
+                          float *stats, void *dx, int64_t ldd, ht_stream stream);
+
 #ifdef __cplusplus
 }
 #endif
