@@ -6,16 +6,23 @@
 //   loss = sum_j p_j (log p_j - log q[id_j]);
 //   d loss / d x_v = 1 / temperature (q_v - sum_{j: id_j = v} p_j).
 //
-// Every gradient here is  scale (sum_{j: id_j = v} g_j - q_v (G + E (log q_v + H)))
-// with few g_j: log probabilities of given tokens have G = sum g and E the
-// entropy's gradient, distillation g_j = p_j, G = 1, E = 0 and a scale of the
-// other sign.  The dense part is written for every entry, then the few given
+// Every gradient here is  scale sum_{j: id_j = v} g_j + q_v (f + e log2 q_v)  with
+// few g_j: of log probabilities of given tokens, f = -scale (sum g + h H) and
+// e = -scale h log 2 with h the entropy's gradient; of distillation, g_j = p_j,
+// f = -scale and e = 0.  The dense part is written for every entry, then the few given
 // ones are written again, whole.
 //
 // Bound by HBM: logits once and the gradient once.  The step holds a row in the
-// registers of 1024 threads between its sum and its gradient where it fits
-// (16-byte pieces per thread: up to 16), else it reads the row a second time,
-// which the Infinity Cache serves: the rows in work are fewer than it holds.
+// registers of a workgroup between its sum and its gradient, up to 20 pieces of
+// 16 bytes per thread, and reads what lies behind them a second time, which the
+// Infinity Cache serves: the rows in work are fewer than it holds.
+// Measured with 20 entries per row, 2 bytes moved per byte of logits:
+//   4096 x 32000 fp32: 180 us, 5.8 TB/s;  4096 x 128000 bf16: 390 us, 5.4 TB/s;
+//   512 x 32000 fp32: 28 us;  two rows on a compute unit at a time and the next
+//   row's loads behind the stores of this one's were slower (190 and 214 against
+//   180 us, 434 and 462 against 390): one workgroup's phases are covered by the others'.
+#include <type_traits>
+
 #include "logits.h"
 
 namespace ht {
@@ -98,16 +105,7 @@ __device__ __forceinline__ RowStat group_stat(RowStat r, float c, RowStat *stats
     __syncthreads();
     if ((threadIdx.x & 63) == 0) stats[threadIdx.x >> 6] = r;
     __syncthreads();
-    r = stats[0];
-#pragma unroll
-    for (int w = 1; w < NT / 64; ++w) r = stat_join(r, stats[w], c);
-    return r;
-}
-
-template <typename T>
-__device__ __forceinline__ u32x4 no_entries() {
-    return sizeof(T) == 4 ? u32x4{0xFF800000u, 0xFF800000u, 0xFF800000u, 0xFF800000u}
-                          : u32x4{0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u};   // -Inf
+    return stat_group<NT / 64>(stats, c);
 }
 
 // Statistics of a row (without entropy), read once by a workgroup.
@@ -189,39 +187,35 @@ __global__ __launch_bounds__(NT) void distill_loss_kernel(GradArgs a) {
 // ---------------------------------------------------------------------------
 // Gradients
 // ---------------------------------------------------------------------------
-// The dense part's coefficients of a row.
+// The dense part's coefficients of a row: dx_v = f q_v, with the entropy's
+// gradient dx_v = (f + e log2 q_v) q_v.
 struct Dense {
-    float mx, b, c, G, E, H, scale;
+    float mx, b, c, f, e;
+    float scale;         // of the given entries
     bool zero;           // the row's gradient is zero whatever its logits are
 };
 
-__device__ __forceinline__ float dense_of(const Dense &d, float x, bool ent) {
-    const float l = (x - d.mx) * d.c - d.b;
-    const float q = exp2_fast(l);
-    float w = d.G;
-    if (ent) w += d.E * (fmaxf(l, kFar) * kLn2 + d.H);
-    return -d.scale * (q * w);
+template <bool ENT>
+__device__ __forceinline__ float dense_of(const Dense &d, float x) {
+    const float l = (x - d.mx) * d.c - d.b, q = exp2_fast(l);
+    if constexpr (ENT) return q * (d.f + d.e * fmaxf(l, kFar));
+    else return q * d.f;
 }
 
-// Whole pieces and single entries of [c0, c0 + n) of a row; HELD 16-byte pieces
-// per thread are in registers already.
-template <typename T, int NT, bool ENT>
+template <typename T, bool ENT>
 __device__ __forceinline__ u32x4 dense_piece(const Dense &d, u32x4 u) {
     using L = LogitType<T>;
     float x[L::kVec];
     L::unpack(u, x);
 #pragma unroll
-    for (int j = 0; j < L::kVec; ++j) x[j] = d.zero ? 0.f : dense_of(d, x[j], ENT);
+    for (int j = 0; j < L::kVec; ++j) x[j] = dense_of<ENT>(d, x[j]);
     return L::pack(x);
 }
 
+// A piece entry by entry, where dx's rows lie otherwise than x's.
 template <typename T>
-__device__ __forceinline__ void put_piece(T *y, u32x4 u, bool whole) {
+__device__ __forceinline__ void put_piece(T *y, u32x4 u) {
     using L = LogitType<T>;
-    if (whole) {
-        *reinterpret_cast<u32x4 *>(y) = u;
-        return;
-    }
     float x[L::kVec];
     L::unpack(u, x);
 #pragma unroll
@@ -230,182 +224,280 @@ __device__ __forceinline__ void put_piece(T *y, u32x4 u, bool whole) {
 
 // Entry j's place written whole: the dense part and every g of that place, in
 // order, so that equal places write equal values.
-template <typename T>
-__device__ __forceinline__ void put_given(T *dx, const Dense &d, float x, int32_t v, const int32_t *id, const float *g, int k,
-                                          bool ent) {
+template <typename T, bool ENT>
+__device__ __forceinline__ void put_given(T *dx, const Dense &d, float x, int32_t v, const int32_t *id, const float *g, int k) {
     float sum = 0.f;
     for (int i = 0; i < k; ++i) sum += id[i] == v ? g[i] : 0.f;
-    LogitType<T>::put(dx + v, d.zero ? 0.f : d.scale * sum + dense_of(d, x, ent));
+    LogitType<T>::put(dx + v, d.scale * sum + dense_of<ENT>(d, x));
 }
 
-// Loss and gradient; a row is held in NV pieces per thread (0: read twice).
-template <typename T, int NT, int NV>
-__global__ __launch_bounds__(NT) void distill_step_kernel(GradArgs a) {
+// The teacher's distribution of a row by one wavefront: ids (-1: not kept), p, log2 p
+// and the student's logits of its k entries (those in [lo, hi)) into LDS;
+// returns whether any has weight.
+template <typename T>
+__device__ __forceinline__ bool teacher_wave(const int32_t *ids, const float *t, const T *row, int64_t lo, int64_t hi, int k,
+                                             int64_t V, float c, int32_t *id, float *p, float *logs, float *given) {
+    const int lane = threadIdx.x & 63;
+    float top = kLowest;
+    for (int j = lane; j < k; j += 64) {
+        const int32_t v = ids[j];
+        const bool in = v >= 0 && v < V;
+        const float z = in ? t[j] : -__builtin_inff();
+        id[j] = in ? v : -1;
+        given[j] = v >= lo && v < hi ? LogitType<T>::get(row + v) : 0.f;
+        logs[j] = z;
+        top = fmaxf(top, z);
+    }
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) top = fmaxf(top, __shfl_xor(top, d));
+    float sum = 0.f;
+    for (int j = lane; j < k; j += 64) {
+        const float d = (logs[j] - top) * c, e = exp2_fast(d);
+        logs[j] = d;
+        p[j] = e;
+        sum += e;
+    }
+    sum = wave_sum(sum);
+    const float inv = 1.0f / sum, b = log2f(sum);
+    for (int j = lane; j < k; j += 64) {
+        p[j] = sum == 0.f ? 0.f : p[j] * inv;
+        logs[j] -= b;
+    }
+    return sum != 0.f;
+}
+
+// Loss and gradient of a row held in NV pieces per thread; FAR: there are more,
+// read twice.  The first wavefront deals with the teacher while the others are at
+// their sums.  SAME: dx's rows lie as x's do within 16 bytes, so its pieces are
+// whole too.  ONCE: a gradient of more than the 256 MB Infinity Cache is neither
+// read nor written with a view to the caches (524 MB: 196 -> 180 us); a smaller
+// one stays for who reads it next (65 MB: 45 us with a sum over it, 56 with the
+// hints).
+template <typename T, int NT, int NV, bool SAME, bool ONCE, bool FAR>
+__global__ __launch_bounds__(NT, NV == 4 ? 6 : 4) void distill_step_kernel(GradArgs a) {
     using L = LogitType<T>;
-    constexpr int kVec = L::kVec;
+    constexpr int kVec = L::kVec, NW = NT / 64, kGroup = 16 / kVec < NV ? 16 / kVec : NV;
     extern __shared__ float lds[];                   // ids, p, log p, logits of the ids
-    __shared__ float part[NT / 64];
-    __shared__ RowStat stats[NT / 64];
+    __shared__ RowStat stats[NW];
+    __shared__ int some;
     int32_t *id = reinterpret_cast<int32_t *>(lds);
     float *p = lds + a.k, *logs = lds + 2 * a.k, *given = lds + 3 * a.k;
-    const int64_t m = blockIdx.x, V = a.V;
+    const int32_t t = threadIdx.x, lane = t & 63, wave = __builtin_amdgcn_readfirstlane(t >> 6);
+    const int64_t m = blockIdx.x;
     const T *row = static_cast<const T *>(a.x) + m * a.ld;
     T *dx = static_cast<T *>(a.dx) + m * a.ldd;
-    const Span sp = span_of(row, V);
-    const u32x4 *v = reinterpret_cast<const u32x4 *>(row + sp.head);
+    const Span sp = span_of(row, a.V);
     const float w = a.weight ? a.weight[m] : 1.0f;
-    const int32_t t = threadIdx.x;
     // the single entries before and after the whole pieces: at most one per thread
     const bool single = t < sp.head + sp.tail;
-    const int64_t at1 = t < sp.head ? int64_t(t) : V - sp.tail + (t - sp.head);
+    const int64_t at1 = t < sp.head ? int64_t(t) : a.V - sp.tail + (t - sp.head);
     Dense d{};
     d.zero = true;
     float x1 = 0.f;
-    u32x4 held[NV > 0 ? NV : 1];
+    u32x4 held[NV];
+    const Pieces in(row + sp.head, sp.vecs);
     if (w != 0.f) {                                  // one value per row: every thread takes the same way
+#pragma unroll
+        for (int i = 0; i < NV; ++i) held[i] = in.load<ONCE ? 2 : 0>(16u * uint32_t(t + i * NT));
         RowStat r = stat_none();
-        if constexpr (NV > 0) {
-#pragma unroll
-            for (int i = 0; i < NV; ++i) held[i] = t + i * NT < sp.vecs ? v[t + i * NT] : no_entries<T>();
-        } else {
-            r = read_row<T, NT, 16 / kVec>(row, V, a.c);
+        if (wave == 0) {
+            const bool any = teacher_wave<T>(a.ids + m * a.k, a.teacher + m * a.k, row, 0, a.V, a.k, a.V, a.c, id, p, logs, given);
+            if (lane == 0) some = any;
         }
-        const bool any = teacher_row<NT>(a.ids + m * a.k, a.teacher + m * a.k, a.k, V, a.c, id, p, logs, part);
-        for (int j = t; j < a.k; j += NT) given[j] = id[j] >= 0 ? L::get(row + id[j]) : 0.f;
-        if (single) x1 = L::get(row + at1);
-        if constexpr (NV > 0) {
-            if (single) stat_add<1, false>(r, &x1, x1, a.c);
+        if (single) {
+            x1 = L::get(row + at1);
+            stat_add<1, false>(r, &x1, x1, a.c);
+        }
 #pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                float x[kVec], most;
-                L::unpack(held[i], x);
-                most = x[0];
+        for (int i = 0; i < NV; i += kGroup) {
+            constexpr int N = kGroup * kVec;
+            float x[N];
 #pragma unroll
-                for (int j = 1; j < kVec; ++j) most = fmaxf(most, x[j]);
-                stat_add<kVec, false>(r, x, most, a.c);
+            for (int g = 0; g < kGroup; ++g) {
+                u32x4 u = held[i + g];
+                if ((i + g + 1) * NT > sp.vecs && t + (i + g) * NT >= sp.vecs) u = no_entries<T>();
+                L::unpack(u, x + g * kVec);
+            }
+            float most = x[0];
+#pragma unroll
+            for (int j = 1; j < N; ++j) most = fmaxf(most, x[j]);
+            stat_add<N, false>(r, x, most, a.c);
+            __builtin_amdgcn_sched_barrier(0);       // group by group: several at once spill
+        }
+        if constexpr (FAR) {
+            for (int32_t at = NV * NT; at < sp.vecs; at += kGroup * NT) {
+                float x[kGroup * kVec];
+                u32x4 u[kGroup];
+#pragma unroll
+                for (int g = 0; g < kGroup; ++g) u[g] = in.load(16u * uint32_t(at + t + g * NT));
+#pragma unroll
+                for (int g = 0; g < kGroup; ++g) L::unpack(at + t + g * NT < sp.vecs ? u[g] : no_entries<T>(), x + g * kVec);
+                float most = x[0];
+#pragma unroll
+                for (int j = 1; j < kGroup * kVec; ++j) most = fmaxf(most, x[j]);
+                stat_add<kGroup * kVec, false>(r, x, most, a.c);
             }
         }
-        const RowOut o = row_out(group_stat<NT>(r, a.c, stats));
-        const float loss = teacher_loss<T, NT>(row, a.k, id, p, logs, o, a.inv_t, part);
-        if (t == 0) a.loss[m] = any ? loss : 0.f;
-        if (t == 0 && a.stats) {
-            a.stats[2 * m] = o.mx;
-            a.stats[2 * m + 1] = o.b;
+        r = stat_wave(r, a.c);
+        if (lane == 0) stats[wave] = r;
+        __syncthreads();
+        const RowOut o = row_out(stat_group<NW>(stats, a.c));
+        const bool any = some != 0;
+        if (wave == 0) {
+            float loss = 0.f;
+            for (int j = lane; j < a.k; j += 64)
+                // an entry without weight adds nothing, whatever the student says of it
+                if (id[j] >= 0 && p[j] != 0.f) loss += p[j] * (logs[j] * kLn2 - logp_of(o, given[j], a.inv_t));
+            loss = wave_sum(loss);
+            if (lane == 0) {
+                a.loss[m] = any ? loss : 0.f;
+                if (a.stats) {
+                    a.stats[2 * m] = o.mx;
+                    a.stats[2 * m + 1] = o.b;
+                }
+            }
         }
         d.mx = o.mx;
         d.b = o.b;
         d.c = a.c;
-        d.G = 1.f;
-        d.scale = -w * a.inv_t;
+        d.f = w * a.inv_t;
+        d.scale = -d.f;
         d.zero = !any || o.kind == 1;
-    } else if (t == 0) {
-        a.loss[m] = 0.f;
-        if (a.stats) a.stats[2 * m] = a.stats[2 * m + 1] = 0.f;
-    }
-    // the row's logits are in registers, or are read before they are written: dx may be the logits
-    const bool whole = a.same != 0;
-    if (single) L::put(dx + at1, d.zero ? 0.f : dense_of(d, x1, false));
-    if constexpr (NV > 0) {
-        if (d.zero) {
-#pragma unroll
-            for (int i = 0; i < NV; ++i)
-                if (t + i * NT < sp.vecs) put_piece<T>(dx + sp.head + int64_t(t + i * NT) * kVec, u32x4{0, 0, 0, 0}, whole);
-            return;
-        }
-#pragma unroll
-        for (int i = 0; i < NV; ++i)
-            if (t + i * NT < sp.vecs)
-                put_piece<T>(dx + sp.head + int64_t(t + i * NT) * kVec, dense_piece<T, NT, false>(d, held[i]), whole);
     } else {
-        for (int32_t i = t; i < sp.vecs; i += NT) {
-            const u32x4 u = d.zero ? u32x4{0, 0, 0, 0} : dense_piece<T, NT, false>(d, v[i]);
-            put_piece<T>(dx + sp.head + int64_t(i) * kVec, u, whole);
+        if (t == 0) {
+            a.loss[m] = 0.f;
+            if (a.stats) a.stats[2 * m] = a.stats[2 * m + 1] = 0.f;
         }
-        if (d.zero) return;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) held[i] = u32x4{0, 0, 0, 0};
     }
+    // the row's logits are in registers or read by now: dx may be the logits
+    if (single) L::put(dx + at1, d.zero ? 0.f : dense_of<false>(d, x1));
+    const Pieces out(dx + sp.head, sp.vecs);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        u32x4 u = dense_piece<T, false>(d, held[i]);
+        if (d.zero) u = u32x4{0, 0, 0, 0};
+        if constexpr (SAME) {
+            out.store<ONCE ? 2 : 0>(16u * uint32_t(t + i * NT), u);
+        } else {
+            if (t + i * NT < sp.vecs) put_piece<T>(dx + sp.head + (t + i * NT) * kVec, u);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+    }
+    if constexpr (FAR) {
+        for (int32_t at = NV * NT; at < sp.vecs; at += kGroup * NT) {
+            u32x4 u[kGroup];
+#pragma unroll
+            for (int g = 0; g < kGroup; ++g) u[g] = d.zero ? u32x4{0, 0, 0, 0} : in.load(16u * uint32_t(at + t + g * NT));
+#pragma unroll
+            for (int g = 0; g < kGroup; ++g) {
+                if (!d.zero) u[g] = dense_piece<T, false>(d, u[g]);
+                if constexpr (SAME) {
+                    out.store<ONCE ? 2 : 0>(16u * uint32_t(at + t + g * NT), u[g]);
+                } else {
+                    if (at + t + g * NT < sp.vecs) put_piece<T>(dx + sp.head + int64_t(at + t + g * NT) * kVec, u[g]);
+                }
+            }
+        }
+    }
+    if (d.zero) return;
     __syncthreads();                                 // the given entries after the dense ones
     for (int j = t; j < a.k; j += NT)
-        if (id[j] >= 0) put_given<T>(dx, d, given[j], id[j], id, p, a.k, false);
+        if (id[j] >= 0) put_given<T, false>(dx, d, given[j], id[j], id, p, a.k);
 }
 
 // Gradient from kept statistics: of the distillation's loss (DIST: weight is the
 // loss's gradient) or of log probabilities and entropy.  A workgroup takes a
-// part of a row.
-template <typename T, int NT, bool DIST>
+// part of a row of up to NV pieces per thread, all loaded before it looks at the
+// given entries.
+template <typename T, int NT, int NV, bool DIST, bool SAME, bool ONCE>
 __global__ __launch_bounds__(NT) void logits_grad_kernel(GradArgs a) {
     using L = LogitType<T>;
-    constexpr int kVec = L::kVec, U = 16 / kVec;
-    extern __shared__ float lds[];                   // ids, g, logits of the ids
-    __shared__ float part[NT / 64];
+    constexpr int kVec = L::kVec;
+    extern __shared__ float lds[];                   // ids, g, logits of the ids, (DIST) log p
+    __shared__ int some;
     int32_t *id = reinterpret_cast<int32_t *>(lds);
     float *g = lds + a.k, *given = lds + 2 * a.k;
     const int64_t m = int64_t(blockIdx.x) / a.S, c0 = (int64_t(blockIdx.x) - m * a.S) * a.part;
     const int64_t n = min(a.V - c0, a.part);
     const T *row = static_cast<const T *>(a.x) + m * a.ld;
     T *dx = static_cast<T *>(a.dx) + m * a.ldd;
-    const int32_t t = threadIdx.x;
+    const int32_t t = threadIdx.x, lane = t & 63, wave = __builtin_amdgcn_readfirstlane(t >> 6);
+    const Span sp = span_of(row + c0, n);
+    const bool single = t < sp.head + sp.tail;
+    const int64_t at1 = c0 + (t < sp.head ? int64_t(t) : n - sp.tail + (t - sp.head));
+    const Pieces in(row + c0 + sp.head, sp.vecs), out(dx + c0 + sp.head, sp.vecs);
     Dense d{};
     d.mx = a.row_stats[2 * m];
     d.b = a.row_stats[2 * m + 1];
     d.c = a.c;
-    d.zero = d.mx == -__builtin_inff();              // a row that allows nothing
-    if constexpr (DIST) {
-        const float w = a.weight[m];
-        if (w == 0.f) d.zero = true;
-        if (!d.zero) d.zero = !teacher_row<NT>(a.ids + m * a.k, a.teacher + m * a.k, a.k, a.V, a.c, id, g, nullptr, part);
-        d.G = 1.f;
-        d.scale = -w * a.inv_t;
-    } else {
-        float sum = 0.f, some = 0.f;
-        for (int j = t; j < a.k; j += NT) {
+    const float w = DIST ? a.weight[m] : 0.f, e = !DIST && a.g_entropy ? a.g_entropy[m] : 0.f;
+    bool any = DIST ? w != 0.f : e != 0.f;
+    if constexpr (!DIST)
+        for (int j = 0; j < a.k && !any; ++j) {
             const int32_t v = a.ids[m * a.k + j];
-            const bool in = v >= 0 && v < a.V;
-            id[j] = in ? v : -1;
-            g[j] = in ? a.g[m * a.k + j] : 0.f;
-            sum += g[j];
-            some += g[j] != 0.f ? 1.f : 0.f;
+            any = v >= 0 && v < a.V && a.g[m * a.k + j] != 0.f;
         }
-        d.G = group_total<NT>(sum, part);
-        some = group_total<NT>(some, part);
-        d.E = a.g_entropy ? a.g_entropy[m] : 0.f;
-        d.H = a.g_entropy ? a.entropy[m] : 0.f;
-        d.scale = a.inv_t;
-        if (some == 0.f && d.E == 0.f) d.zero = true;
-    }
+    d.zero = !any || d.mx == -__builtin_inff();      // no gradient, or a row that allows nothing: not read
+    u32x4 held[NV];
+    float x1 = 0.f;
     if (!d.zero) {
-        for (int j = t; j < a.k; j += NT) given[j] = id[j] >= c0 && id[j] < c0 + n ? L::get(row + id[j]) : 0.f;
-    }
-    const Span sp = span_of(row + c0, n);
-    const bool ent = !DIST && d.E != 0.f;
-    const bool whole = a.same != 0, single = t < sp.head + sp.tail;
-    const int64_t at1 = c0 + (t < sp.head ? int64_t(t) : n - sp.tail + (t - sp.head));
-    __syncthreads();                                 // the given logits are read: dx may be the logits
-    if (single) L::put(dx + at1, d.zero ? 0.f : dense_of(d, L::get(row + at1), ent));
-    const u32x4 *v = reinterpret_cast<const u32x4 *>(row + c0 + sp.head);
-    T *y = dx + c0 + sp.head;
-    if (d.zero) {
-        for (int32_t i = t; i < sp.vecs; i += NT) put_piece<T>(y + int64_t(i) * kVec, u32x4{0, 0, 0, 0}, whole);
-        return;
-    }
-    for (int32_t at = 0; at < sp.vecs; at += U * NT) {
-        u32x4 u[U];
 #pragma unroll
-        for (int j = 0; j < U; ++j) {
-            const int32_t i = at + j * NT + t;
-            if (i < sp.vecs) u[j] = __builtin_nontemporal_load(v + i);
-        }
-#pragma unroll
-        for (int j = 0; j < U; ++j) {
-            const int32_t i = at + j * NT + t;
-            if (i < sp.vecs) {
-                const u32x4 o = ent ? dense_piece<T, NT, true>(d, u[j]) : dense_piece<T, NT, false>(d, u[j]);
-                put_piece<T>(y + int64_t(i) * kVec, o, whole);
+        for (int i = 0; i < NV; ++i) held[i] = in.load<ONCE ? 2 : 0>(16u * uint32_t(t + i * NT));
+        if (single) x1 = L::get(row + at1);
+        if constexpr (DIST) {
+            if (wave == 0) {
+                const bool kept = teacher_wave<T>(a.ids + m * a.k, a.teacher + m * a.k, row, c0, c0 + n, a.k, a.V, a.c, id, g,
+                                                  lds + 3 * a.k, given);
+                if (lane == 0) some = kept;
             }
+            d.f = w * a.inv_t;
+            d.scale = -d.f;
+        } else {
+            float sum = 0.f;                         // every wavefront its own, in the same order
+            for (int j = lane; j < a.k; j += 64) {
+                const int32_t v = a.ids[m * a.k + j];
+                const float gj = v >= 0 && v < a.V ? a.g[m * a.k + j] : 0.f;
+                sum += gj;
+                if (wave == 0) {
+                    id[j] = v >= 0 && v < a.V ? v : -1;
+                    g[j] = gj;
+                    given[j] = v >= c0 && v < c0 + n ? L::get(row + v) : 0.f;
+                }
+            }
+            sum = wave_sum(sum);
+            d.f = -a.inv_t * (sum + (e != 0.f ? e * a.entropy[m] : 0.f));
+            d.e = -a.inv_t * e * kLn2;
+            d.scale = a.inv_t;
         }
+    } else {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) held[i] = u32x4{0, 0, 0, 0};
     }
-    __syncthreads();                                 // the given entries after the dense ones
-    for (int j = t; j < a.k; j += NT)
-        if (id[j] >= c0 && id[j] < c0 + n) put_given<T>(dx, d, given[j], id[j], id, g, a.k, ent);
+    __syncthreads();                                 // the given logits are read: dx may be the logits
+    if (DIST && !d.zero) d.zero = some == 0;
+    const auto put = [&](auto entropy) {
+        constexpr bool kEnt = decltype(entropy)::value;
+        if (single) L::put(dx + at1, d.zero ? 0.f : dense_of<kEnt>(d, x1));
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            u32x4 u = dense_piece<T, kEnt>(d, held[i]);
+            if (d.zero) u = u32x4{0, 0, 0, 0};
+            if constexpr (SAME) {
+                out.store<ONCE ? 2 : 0>(16u * uint32_t(t + i * NT), u);
+            } else {
+                if (t + i * NT < sp.vecs) put_piece<T>(dx + c0 + sp.head + (t + i * NT) * kVec, u);
+            }
+            __builtin_amdgcn_sched_barrier(0);       // piece by piece: several at once spill
+        }
+        if (d.zero) return;
+        __syncthreads();                             // the given entries after the dense ones
+        for (int j = t; j < a.k; j += NT)
+            if (id[j] >= c0 && id[j] < c0 + n) put_given<T, kEnt>(dx, d, given[j], id[j], id, g, a.k);
+    };
+    if (!DIST && e != 0.f) put(std::true_type{});
+    else put(std::false_type{});
 }
 
 // dx's rows lie as x's do within 16 bytes: whole pieces of one are whole pieces of the other.
@@ -414,45 +506,53 @@ bool same_alignment(const void *x, int64_t ld, const void *dx, int64_t ldd, int6
            (M <= 1 || ((ld - ldd) * size) % 16 == 0);
 }
 
-template <typename T>
-ht_status launch_step(const GradArgs &a, int64_t M, hipStream_t s) {
-    constexpr int kVec = LogitType<T>::kVec;
+bool once(const GradArgs &a, int64_t M, int size) { return M * a.V * size > (int64_t(256) << 20); }
+
+template <typename T, int NT, int NV, bool FAR = false>
+void step_kernel(const GradArgs &a, int64_t M, hipStream_t s) {
     const uint32_t grid = uint32_t(M);
     const size_t lds = size_t(4) * size_t(a.k) * 4;
-    const int64_t pieces = a.V / kVec;               // at most: the head takes some
-#define HT_STEP(NT, NV) distill_step_kernel<T, NT, NV><<<grid, NT, lds, s>>>(a)
-    if (pieces <= 256) HT_STEP(256, 1);
-    else if (pieces <= 1024) HT_STEP(256, 4);
-    else if (pieces <= 4096) HT_STEP(1024, 4);
-    else if (pieces <= 8192) HT_STEP(1024, 8);
-    else if (pieces <= 16384) HT_STEP(1024, 16);
-    else HT_STEP(1024, 0);
-#undef HT_STEP
+    if (!a.same) distill_step_kernel<T, NT, NV, false, false, FAR><<<grid, NT, lds, s>>>(a);
+    else if (once(a, M, int(sizeof(T)))) distill_step_kernel<T, NT, NV, true, true, FAR><<<grid, NT, lds, s>>>(a);
+    else distill_step_kernel<T, NT, NV, true, false, FAR><<<grid, NT, lds, s>>>(a);
+}
+
+template <typename T>
+ht_status launch_step(const GradArgs &a, int64_t M, hipStream_t s) {
+    const int64_t pieces = a.V / LogitType<T>::kVec;   // at most: the head takes some
+    if (pieces <= 256) step_kernel<T, 256, 1>(a, M, s);
+    else if (pieces <= 1024) step_kernel<T, 256, 4>(a, M, s);
+    else if (pieces <= 4096) step_kernel<T, 1024, 4>(a, M, s);
+    else if (pieces <= 8192) step_kernel<T, 1024, 8>(a, M, s);
+    else if (pieces <= 16384) step_kernel<T, 1024, 16>(a, M, s);
+    else if (pieces <= 20480) step_kernel<T, 1024, 20>(a, M, s);
+    else step_kernel<T, 1024, 20, true>(a, M, s);
     HT_LAUNCH_CHECK();
     return HT_OK;
 }
 
-// Parts of a row in the gradient kernel: pieces of about 16384 entries, so
-// that the teacher's distribution is computed a few times per row.
-void grad_shape(GradArgs &a, int64_t M) {
-    int64_t S = (a.V + 16383) / 16384;
-    if (M * S < 512) {
-        S = (512 + M - 1) / M;
-        const int64_t most = (a.V + 4095) / 4096;
-        if (S > most) S = most;
-    }
-    while (M * S >= (int64_t(1) << 23)) S = (S + 1) / 2;   // the launch's limit on threads
-    a.part = ((a.V + S - 1) / S + 7) / 8 * 8;
-    a.S = int32_t((a.V + a.part - 1) / a.part);
+template <typename T, int NV, bool DIST>
+void grad_kernel(const GradArgs &a, int64_t M, hipStream_t s) {
+    const uint32_t grid = uint32_t(M * a.S);
+    const size_t lds = size_t(4) * size_t(a.k) * 4;
+    if (!a.same) logits_grad_kernel<T, 256, NV, DIST, false, false><<<grid, 256, lds, s>>>(a);
+    else if (once(a, M, int(sizeof(T)))) logits_grad_kernel<T, 256, NV, DIST, true, true><<<grid, 256, lds, s>>>(a);
+    else logits_grad_kernel<T, 256, NV, DIST, true, false><<<grid, 256, lds, s>>>(a);
 }
 
-template <bool DIST>
-ht_status launch_grad(GradArgs &a, int64_t M, int32_t type, hipStream_t s) {
-    grad_shape(a, M);
-    const uint32_t grid = uint32_t(M * a.S);
-    const size_t lds = size_t(3) * size_t(a.k) * 4;
-    if (type == HT_BF16) logits_grad_kernel<uint16_t, 256, DIST><<<grid, 256, lds, s>>>(a);
-    else logits_grad_kernel<float, 256, DIST><<<grid, 256, lds, s>>>(a);
+// Equal parts of a row of at most 16 pieces per thread, or of 4 where those
+// give too few workgroups to fill the card.
+template <typename T, bool DIST>
+ht_status launch_grad(GradArgs &a, int64_t M, hipStream_t s) {
+    const int64_t piece = LogitType<T>::kVec, pieces = (a.V + piece - 1) / piece;
+    int nv = 16;
+    if (M * ((pieces + 4095) / 4096) < 1024 || pieces <= 1024) nv = 4;
+    const int64_t S = (pieces + 256 * nv - 1) / (256 * nv);
+    if (M * S >= (int64_t(1) << 24)) return HT_ESHAPE;    // the launch's limit on threads
+    a.part = ((pieces + S - 1) / S) * piece;
+    a.S = int32_t((a.V + a.part - 1) / a.part);
+    if (nv == 16) grad_kernel<T, 16, DIST>(a, M, s);
+    else grad_kernel<T, 4, DIST>(a, M, s);
     HT_LAUNCH_CHECK();
     return HT_OK;
 }
@@ -508,7 +608,8 @@ extern "C" ht_status ht_token_logprobs_backward(const float *d_logp, const float
     a.g_entropy = d_entropy;
     a.row_stats = stats;
     a.entropy = entropy;
-    return launch_grad<false>(a, M, type, hipStream_t(stream));
+    return type == HT_BF16 ? launch_grad<uint16_t, false>(a, M, hipStream_t(stream))
+                           : launch_grad<float, false>(a, M, hipStream_t(stream));
 }
 
 extern "C" ht_status ht_distill_loss(const void *logits, int64_t ld, int32_t type, int64_t M, int64_t V,
@@ -546,7 +647,8 @@ extern "C" ht_status ht_distill_backward(const float *d_loss, const void *logits
     a.teacher = teacher;
     a.weight = d_loss;
     a.row_stats = stats;
-    return launch_grad<true>(a, M, type, hipStream_t(stream));
+    return type == HT_BF16 ? launch_grad<uint16_t, true>(a, M, hipStream_t(stream))
+                           : launch_grad<float, true>(a, M, hipStream_t(stream));
 }
 
 extern "C" ht_status ht_distill_step(const void *logits, int64_t ld, int32_t type, int64_t M, int64_t V,

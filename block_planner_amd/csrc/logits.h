@@ -44,7 +44,7 @@ struct LogitType<uint16_t> {
         return u32x4{pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7])};
     }
     static __device__ __forceinline__ float get(const uint16_t *p) { return __uint_as_float(uint32_t(*p) << 16); }
-    static __device__ __forceinline__ void put(uint16_t *p, float v) { *p = f32_to_bf16_rne(v); }
+    static __device__ __forceinline__ void put(uint16_t *p, float v) { *p = round_bf16(v); }
 };
 
 // n elements from p on as `head` single ones, up to the next 16-byte boundary,
@@ -62,6 +62,32 @@ __device__ __forceinline__ Span span_of(const T *p, int64_t n) {
     s.vecs = int32_t((n - s.head) / kVec);
     s.tail = int(n - s.head - int64_t(s.vecs) * kVec);
     return s;
+}
+
+// The whole pieces of a row as a buffer: a piece takes one 32-bit offset, and
+// those past the end read zeros and store nothing.  Its address is the same in
+// every lane.
+struct Pieces {
+    __amdgpu_buffer_rsrc_t r;
+    int32_t vecs;
+
+    __device__ __forceinline__ Pieces(const void *p, int32_t n)
+        : r(__builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(p), 0, int(16u * uint32_t(n)), 0x00020000)), vecs(n) {}
+    template <int AUX = 0>
+    __device__ __forceinline__ u32x4 load(uint32_t byte) const {
+        return __builtin_amdgcn_raw_buffer_load_b128(r, byte, 0, AUX);
+    }
+    template <int AUX = 0>
+    __device__ __forceinline__ void store(uint32_t byte, u32x4 v) const {
+        __builtin_amdgcn_raw_buffer_store_b128(v, r, byte, 0, AUX);
+    }
+};
+
+// -Inf entries: what the pieces past a row's end stand for.
+template <typename T>
+__device__ __forceinline__ u32x4 no_entries() {
+    return sizeof(T) == 4 ? u32x4{0xFF800000u, 0xFF800000u, 0xFF800000u, 0xFF800000u}
+                          : u32x4{0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u};
 }
 
 __device__ __forceinline__ float exp2_fast(float d) { return __builtin_amdgcn_exp2f(d); }
@@ -98,11 +124,40 @@ __device__ __forceinline__ void stat_add(RowStat &r, const float *x, float top, 
     r.mx = m;
 }
 
+// Largest over a wavefront, the same on all lanes.
+__device__ __forceinline__ float wave_top(float v) {
+    v = fmaxf(v, dpp_f32<kDppXor1>(v));
+    v = fmaxf(v, dpp_f32<kDppXor2>(v));
+    v = fmaxf(v, dpp_f32<kDppHalfMirror>(v));
+    v = fmaxf(v, dpp_f32<kDppMirror>(v));
+    v = fmaxf(v, __shfl_xor(v, 16));
+    return fmaxf(v, __shfl_xor(v, 32));
+}
+
+// Statistics relative to a larger or equal maximum.
+__device__ __forceinline__ RowStat stat_under(RowStat r, float m, float c) {
+    const float d = fmaxf((r.mx - m) * c, kFar), f = exp2_fast(d);
+    return RowStat{m, f * r.s, f * (r.t + d * r.s)};
+}
+
+// Over a wavefront: the maximum first, then sums relative to it.
 __device__ __forceinline__ RowStat stat_wave(RowStat r, float c) {
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1)
-        r = stat_join(r, RowStat{__shfl_xor(r.mx, d), __shfl_xor(r.s, d), __shfl_xor(r.t, d)}, c);
-    return r;
+    r = stat_under(r, wave_top(r.mx), c);
+    return RowStat{r.mx, wave_sum(r.s), wave_sum(r.t)};
+}
+
+// Over the NW <= 16 wavefronts' results in LDS, lane by lane of 16.
+template <int NW>
+__device__ __forceinline__ RowStat stat_group(const RowStat *stats, float c) {
+    RowStat r = stat_none();
+    if (int(threadIdx.x & 15) < NW) r = stats[threadIdx.x & 15];
+    float m = r.mx;
+    m = fmaxf(m, dpp_f32<kDppXor1>(m));
+    m = fmaxf(m, dpp_f32<kDppXor2>(m));
+    m = fmaxf(m, dpp_f32<kDppHalfMirror>(m));
+    m = fmaxf(m, dpp_f32<kDppMirror>(m));
+    r = stat_under(r, m, c);
+    return RowStat{m, group_sum<16>(r.s), group_sum<16>(r.t)};
 }
 
 // log2 of a sum s >= 1 (its largest entry adds 1): exact near 1, where the
@@ -154,89 +209,172 @@ __device__ __forceinline__ float key_value(uint32_t k) {
 __device__ __forceinline__ uint64_t entry_of(float x, uint32_t i) { return (uint64_t(order_key(x)) << 32) | (0xFFFFFFFFu - i); }
 __device__ __forceinline__ uint32_t entry_index(uint64_t e) { return 0xFFFFFFFFu - uint32_t(e); }
 
-__device__ __forceinline__ uint64_t lane_xor(uint64_t v, int j) {
-    return (uint64_t(uint32_t(__shfl_xor(int(v >> 32), j))) << 32) | uint32_t(__shfl_xor(int(v), j));
+// The value of lane ^ J.  Within 16 lanes by lane permutations of one or two
+// moves, across them by the swaps of halves and of rows of 16.
+template <int J>
+__device__ __forceinline__ uint32_t lane_xor32(uint32_t v) {
+    if constexpr (J == 1) return dpp_u32<kDppXor1>(v);
+    else if constexpr (J == 2) return dpp_u32<kDppXor2>(v);
+    else if constexpr (J == 4) return dpp_u32<0x1B>(dpp_u32<kDppHalfMirror>(v));   // ^ 7, then ^ 3
+    else if constexpr (J == 8) return dpp_u32<0x128>(v);                             // rotated by 8 of 16
+    else if constexpr (J == 16) {
+        const auto r = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+        return threadIdx.x & 16 ? r[0] : r[1];
+    } else {
+        const auto r = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+        return threadIdx.x & 32 ? r[0] : r[1];
+    }
+}
+
+template <int J>
+__device__ __forceinline__ uint64_t lane_xor(uint64_t v) {
+    return (uint64_t(lane_xor32<J>(uint32_t(v >> 32))) << 32) | lane_xor32<J>(uint32_t(v));
 }
 
 __device__ __forceinline__ uint64_t keep(uint64_t a, uint64_t b, bool larger) { return (a > b) == larger ? a : b; }
 
+// One step of a merge within groups of 2 J lanes: K is the direction's bit.
+template <int K, int J>
+__device__ __forceinline__ uint64_t sort_steps(uint64_t v, int lane) {
+    v = keep(v, lane_xor<J>(v), ((lane & J) == 0) != ((lane & K) == 0));
+    if constexpr (J > 1) return sort_steps<K, J / 2>(v, lane);
+    else return v;
+}
+
 // One entry per lane in ascending order of lanes.
 __device__ __forceinline__ uint64_t sort_up(uint64_t v, int lane) {
-#pragma unroll
-    for (int k = 2; k <= 64; k <<= 1)
-#pragma unroll
-        for (int j = k >> 1; j > 0; j >>= 1) v = keep(v, lane_xor(v, j), ((lane & j) == 0) != ((lane & k) == 0));
-    return v;
+    v = sort_steps<2, 1>(v, lane);
+    v = sort_steps<4, 2>(v, lane);
+    v = sort_steps<8, 4>(v, lane);
+    v = sort_steps<16, 8>(v, lane);
+    v = sort_steps<32, 16>(v, lane);
+    return sort_steps<64, 32>(v, lane);
 }
 
-// The 64 largest of a descending list and an ascending one, descending.
+// The 64 largest of a descending list and an ascending one, descending: K = 0
+// keeps the larger in the lower lane everywhere.
 __device__ __forceinline__ uint64_t join_lists(uint64_t down, uint64_t up, int lane) {
-    uint64_t v = down > up ? down : up;
-#pragma unroll
-    for (int j = 32; j > 0; j >>= 1) v = keep(v, lane_xor(v, j), (lane & j) == 0);
-    return v;
+    return sort_steps<128, 32>(down > up ? down : up, lane ^ 63);
 }
 
-// A wavefront's k largest so far.  Entries at least `thr` are collected in LDS
-// and join the list 64 at a time, so that a sort and a merge serve many; a row
-// in no order passes about k log(n / k) of them.  thr is the smallest value
-// above the k-th of the list, whose entries all come before those still to be
-// read: an equal one has a higher index and stays out.
+// A wavefront's k largest so far.  Where a lane's entries reach `thr`, its two
+// 16-byte pieces are put aside in LDS, which costs the pass over the row a vote and
+// a few stores; 64 lanes' pieces at a time join the list.  thr is the larger of
+// two bounds:
+//   - the smallest value above the k-th of the list, whose entries all come
+//     before those still to be read: an equal one has a higher index;
+//   - the least, over the workgroup's W wavefronts, of the ceil(k / W)-th largest
+//     of their lanes' maxima: k entries of the row reach it.  It costs 16 votes
+//     and no sort, so it is renewed often (raise): a row of n entries in no
+//     order puts about k log(n / k) pairs of pieces aside.  The wavefronts publish
+//     theirs without waiting: an older one is a lower bound, and what is put aside
+//     in vain changes nothing in the result.
+template <typename T>
 struct TopList {
-    uint64_t list;       // this lane's
-    float thr;
-    int pending;
-    uint64_t *buf;       // [128] of the wavefront
+    static constexpr int kVec = LogitType<T>::kVec, kMost = 128;
+    struct Aside {
+        u32x4 piece[2][kMost];
+        int32_t first[kMost];    // the first one's number in the row; the second's is `apart` further
+    };
+    uint64_t list, kth;  // this lane's entry; the k-th, 0: none yet
+    float thr;           // never NaN
+    int pending, k, lane;
+    int waves, part;     // part: ceil(k / waves)
+    Aside *aside;        // the wavefront's, in LDS
+    float *bounds;       // [waves] of the workgroup, in LDS, -Inf at first
 
-    __device__ __forceinline__ void init(uint64_t *b) {
-        list = 0;
+    __device__ __forceinline__ void init(Aside *a, float *s, int w, int top) {
+        list = kth = 0;
         thr = -__builtin_inff();
         pending = 0;
-        buf = b;
+        k = top;
+        lane = threadIdx.x & 63;
+        waves = w;
+        part = (k + w - 1) / w;
+        aside = a;
+        bounds = s;
     }
 
-    __device__ __forceinline__ void flush(int k, int lane) {
+    // Publishes the wavefront's bound; top: the lane's largest entry, -Inf without one.
+    __device__ __forceinline__ void raise(float top) {
+        // to 16 bits, from below; -Inf's are those of no number
+        const uint32_t key = order_key(top);
+        uint32_t p = 0;
+#pragma unroll
+        for (int bit = 31; bit >= 16; --bit) {
+            const uint32_t q = p | (1u << bit);
+            if (__popcll(__ballot(key >= q)) >= part) p = q;
+        }
+        const float v = key_value(p);
+        if (lane == 0 && v > -__builtin_inff())
+            __hip_atomic_store(&bounds[threadIdx.x >> 6], v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+    }
+
+    __device__ __forceinline__ void refresh() {
+        float least = __builtin_inff();
+        for (int w = 0; w < waves; ++w)
+            least = fminf(least, __hip_atomic_load(&bounds[w], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP));
+        thr = fmaxf(thr, least);
+    }
+
+    // One entry per lane (0: none) joins the list.
+    __device__ __forceinline__ void take(uint64_t e) {
+        list = join_lists(list, sort_up(e, lane), lane);
+        kth = (uint64_t(uint32_t(__builtin_amdgcn_readlane(uint32_t(list >> 32), k - 1))) << 32) |
+              uint32_t(__builtin_amdgcn_readlane(uint32_t(list), k - 1));
+    }
+
+    // Puts the lane's two pieces aside where their largest entry reaches thr.
+    __device__ __forceinline__ void put(float top, u32x4 a, u32x4 b, int32_t first) {
+        const bool in = top >= thr;
+        const uint64_t who = __ballot(in);
+        if (who == 0) return;
+        const int at = pending + int(__builtin_amdgcn_mbcnt_hi(uint32_t(who >> 32), __builtin_amdgcn_mbcnt_lo(uint32_t(who), 0)));
+        if (in) {
+            aside->piece[0][at] = a;
+            aside->piece[1][at] = b;
+            aside->first[at] = first;
+        }
+        pending += __popcll(who);
+    }
+
+    // Up to 64 pairs put aside join the list; vecs: pieces of the row, i0: index of the first one's first entry.
+    __device__ __forceinline__ void flush(int32_t apart, int32_t vecs, uint32_t i0) {
         asm volatile("" ::: "memory");                        // other lanes' stores come before these loads
-        const uint64_t in = lane < pending ? buf[lane] : 0;
-        const uint64_t rest = 64 + lane < pending ? buf[64 + lane] : 0;
+        const bool mine = lane < pending;
+        const u32x4 a = aside->piece[0][lane], b = aside->piece[1][lane];
+        const int32_t first = mine ? aside->first[lane] : vecs;
+        const int32_t left = pending - 64;
+        if (lane < left) {
+            aside->piece[0][lane] = aside->piece[0][64 + lane];
+            aside->piece[1][lane] = aside->piece[1][64 + lane];
+            aside->first[lane] = aside->first[64 + lane];
+        }
         asm volatile("" ::: "memory");
-        list = join_lists(list, sort_up(in, lane), lane);
-        pending = pending > 64 ? pending - 64 : 0;
-        if (lane < pending) buf[lane] = rest;
-        const uint32_t kth = uint32_t(__shfl(int(list >> 32), k - 1));
-        if (kth) thr = key_value(kth + 1);                    // the next float up (-0 for 0 above the negative ones)
-    }
-
-    // N entries of each lane, the j-th at index i0 + j; live: whether they exist.  top: their largest.
-    template <int N>
-    __device__ __forceinline__ void add(const float *x, float top, uint32_t i0, bool live, int k, int lane) {
-        const uint64_t some = __ballot(live && top >= thr);
-        if (some == 0) return;
-        float t = thr;
-        const bool crowded = __popcll(some) >= k;
-        if (crowded) {
-            // the k-th largest of the lanes' maxima, to 16 bits from below: at least k entries reach it
-            const uint32_t key = live && top >= thr ? order_key(top) : 0;
-            uint32_t p = 0;
+        pending = left > 0 ? left : 0;
+        float x[2 * kVec];
+        uint32_t key[2 * kVec];
+        LogitType<T>::unpack(a, x);
+        LogitType<T>::unpack(b, x + kVec);
 #pragma unroll
-            for (int bit = 31; bit >= 16; --bit) {
-                const uint32_t q = p | (1u << bit);
-                if (__popcll(__ballot(key >= q)) >= k) p = q;
-            }
-            const float raised = key_value(p);
-            if (raised > t) t = raised;
-        }
+        for (int j = 0; j < 2 * kVec; ++j) key[j] = first + j / kVec * apart < vecs ? order_key(x[j]) : 0;
+        // each lane's largest in turn, while any belongs to the k
+        for (;;) {
+            uint32_t top = key[0];
 #pragma unroll
-        for (int j = 0; j < N; ++j) {
-            const bool in = live && x[j] >= t;
-            const uint64_t who = __ballot(in);
-            if (who == 0) continue;
-            const int at = pending + int(__builtin_amdgcn_mbcnt_hi(uint32_t(who >> 32), __builtin_amdgcn_mbcnt_lo(uint32_t(who), 0)));
-            if (in) buf[at] = entry_of(x[j], i0 + uint32_t(j));
-            pending += __popcll(who);
-            if (pending >= 64) flush(k, lane);
+            for (int j = 1; j < 2 * kVec; ++j) top = max(top, key[j]);
+            int which = 0;
+#pragma unroll
+            for (int j = 2 * kVec - 1; j >= 0; --j) which = key[j] == top ? j : which;
+            const uint32_t i = i0 + uint32_t(first + (which >= kVec ? apart : 0)) * kVec + uint32_t(which & (kVec - 1));
+            const uint64_t e = top ? (uint64_t(top) << 32) | (0xFFFFFFFFu - i) : 0;
+            const bool in = e > kth;
+            if (__ballot(in) == 0) break;
+            take(in ? e : 0);
+#pragma unroll
+            for (int j = 0; j < 2 * kVec; ++j) key[j] = j == which ? 0 : key[j];
         }
-        if (crowded && pending >= k) flush(k, lane);
+        if (kth) thr = fmaxf(thr, key_value(uint32_t(kth >> 32) + 1));   // the next float up (-0 for 0 above the negative ones)
     }
 };
 
@@ -250,7 +388,7 @@ inline ht_status check_logits(const void *p, int64_t ld, int64_t M, int64_t V, i
 
 // Temperatures whose inverse times log2(e) is a normal number.
 inline ht_status check_logit_shape(int64_t M, int64_t V, int32_t type, float temperature) {
-    if (M < 0 || M > kMaxLogitRows || V <= 0 || V >= (int64_t(1) << 31) - 64) return HT_ESHAPE;
+    if (M < 0 || M > kMaxLogitRows || V <= 0 || V > (int64_t(1) << 29)) return HT_ESHAPE;   // a row's bytes as 32-bit offsets
     if (!act_size(type) || !(temperature >= 1e-30f) || !(temperature <= 1e30f)) return HT_EINVAL;
     return HT_OK;
 }

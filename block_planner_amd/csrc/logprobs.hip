@@ -28,59 +28,62 @@ struct LogprobArgs {
 
 // Statistics and largest entries of n entries from p on, whose first has index
 // i0; every wavefront's result in its lanes.
-template <typename T, int NT, int U, bool ENT, bool TOP>
-__device__ __forceinline__ RowStat scan_row(const T *p, int64_t n, uint32_t i0, float c, int k, TopList &list) {
+template <typename T, int NT, bool ENT, bool TOP>
+__device__ __forceinline__ RowStat scan_row(const T *p, int64_t n, uint32_t i0, float c, TopList<T> &list) {
     using L = LogitType<T>;
-    constexpr int kVec = L::kVec;
-    const int lane = threadIdx.x & 63;
+    constexpr int kVec = L::kVec, U = 16 / kVec;     // 16 entries per thread and step
     const Span sp = span_of(p, n);
+    const int32_t t = threadIdx.x;
     RowStat r = stat_none();
-    const auto single = [&](const T *q, int count, uint32_t i) {
-        if (threadIdx.x >= 64 || count == 0) return;          // the first wavefront's
-        const bool live = lane < count;
-        const float x = live ? L::get(q + lane) : -__builtin_inff();
-        stat_add<1, ENT>(r, &x, x, c);
-        if constexpr (TOP) list.add<1>(&x, x, i + uint32_t(lane), live, k, lane);
-    };
-    single(p, sp.head, i0);
-    const u32x4 *v = reinterpret_cast<const u32x4 *>(p + sp.head);
-    const u32x4 none = sizeof(T) == 4 ? u32x4{0xFF800000u, 0xFF800000u, 0xFF800000u, 0xFF800000u}
-                                      : u32x4{0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u};   // -Inf
+    const Pieces in(p + sp.head, sp.vecs);
     u32x4 next[U];
     const auto load = [&](int32_t at) {
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int32_t i = at + u * NT + int32_t(threadIdx.x);
-            next[u] = i < sp.vecs ? __builtin_nontemporal_load(v + i) : none;
-        }
+        for (int u = 0; u < U; ++u) next[u] = in.load<2>(16u * uint32_t(at + u * NT + t));   // not kept in the caches
     };
     load(0);
+    float lane_top = -__builtin_inff();
+    int step = 0, renew = 1;                         // bounds are published after steps 1, 2, 3, 4, 6, 9, ...
     for (int32_t at = 0; at < sp.vecs; at += U * NT) {
-        float x[U * kVec], top[U], most;
-#pragma unroll
-        for (int u = 0; u < U; ++u) L::unpack(next[u], x + u * kVec);
-        if (at + U * NT < sp.vecs) load(at + U * NT);
+        u32x4 cur[U];
+        float x[U * kVec], top[U / 2];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            top[u] = x[u * kVec];
-#pragma unroll
-            for (int j = 1; j < kVec; ++j) top[u] = fmaxf(top[u], x[u * kVec + j]);
-            most = u ? fmaxf(most, top[u]) : top[u];
+            cur[u] = at + (u + 1) * NT <= sp.vecs || at + u * NT + t < sp.vecs ? next[u] : no_entries<T>();
+            L::unpack(cur[u], x + u * kVec);
         }
+        load(at + U * NT);
+#pragma unroll
+        for (int h = 0; h < U / 2; ++h) {
+            top[h] = x[2 * h * kVec];
+#pragma unroll
+            for (int j = 1; j < 2 * kVec; ++j) top[h] = fmaxf(top[h], x[2 * h * kVec + j]);
+        }
+        const float most = U > 2 ? fmaxf(top[0], top[U / 2 - 1]) : top[0];
         stat_add<U * kVec, ENT>(r, x, most, c);
         if constexpr (TOP) {
-            if (__any(most >= list.thr)) {
+            lane_top = fmaxf(lane_top, most);
+            if (++step == renew) {
+                list.raise(lane_top);
+                if (step == 1) __syncthreads();      // no wavefront collects without a bound
+                list.refresh();
+                renew += (step + 1) / 2;
+            }
+            const bool last = at + U * NT >= sp.vecs;
 #pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    const int32_t i = at + u * NT + int32_t(threadIdx.x);
-                    list.add<kVec>(x + u * kVec, top[u], i0 + uint32_t(sp.head) + uint32_t(i) * kVec, i < sp.vecs, k, lane);
-                }
+            for (int h = 0; h < U / 2; ++h) {
+                list.put(top[h], cur[2 * h], cur[2 * h + 1], at + 2 * h * NT + t);
+                while (list.pending >= 64 || (last && h == U / 2 - 1 && list.pending > 0))
+                    list.flush(NT, sp.vecs, i0 + uint32_t(sp.head));
             }
         }
     }
-    single(p + sp.head + int64_t(sp.vecs) * kVec, sp.tail, i0 + uint32_t(n - sp.tail));
-    if constexpr (TOP) {
-        if (list.pending) list.flush(k, lane);
+    if (t < 64 && sp.head + sp.tail) {               // the single ones before and after, by the first wavefront
+        const bool live = t < sp.head + sp.tail;
+        const int64_t i = t < sp.head ? int64_t(t) : n - sp.tail + (t - sp.head);
+        const float x = live ? L::get(p + i) : -__builtin_inff();
+        stat_add<1, ENT>(r, &x, x, c);
+        if constexpr (TOP) list.take(live ? entry_of(x, i0 + uint32_t(i)) : 0);
     }
     return stat_wave(r, c);
 }
@@ -89,14 +92,12 @@ __device__ __forceinline__ RowStat scan_row(const T *p, int64_t n, uint32_t i0, 
 // (statistics in all).
 template <int NW, bool TOP>
 __device__ __forceinline__ RowStat meet(RowStat r, float c, uint64_t &list, uint64_t *lists, RowStat *stats) {
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     __syncthreads();
     if (lane == 0) stats[wave] = r;
     if constexpr (TOP) lists[wave * 64 + lane] = list;
     __syncthreads();
-    r = stats[0];
-#pragma unroll
-    for (int w = 1; w < NW; ++w) r = stat_join(r, stats[w], c);
+    r = stat_group<NW>(stats, c);
     if constexpr (TOP) {
         for (int w = NW / 2; w > 0; w >>= 1) {
             if (wave < w) {
@@ -131,19 +132,25 @@ __device__ __forceinline__ void write_row(const LogprobArgs &a, int64_t m, RowSt
 }
 
 template <typename T, int NT, bool TOP, bool PARTS>
-__global__ __launch_bounds__(NT) void logprob_kernel(LogprobArgs a) {
+__global__ __launch_bounds__(NT, TOP ? 6 : 8) void logprob_kernel(LogprobArgs a) {
     constexpr int NW = NT / 64;
-    __shared__ uint64_t buf[TOP ? NW * 128 : 1];
+    __shared__ typename TopList<T>::Aside aside[TOP ? NW : 1];
+    uint64_t *lists = reinterpret_cast<uint64_t *>(aside);   // [NW][64], once nothing is put aside any more
     __shared__ RowStat stats[NW];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    __shared__ float bounds[NW];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    if constexpr (TOP) {
+        if (threadIdx.x < NW) bounds[threadIdx.x] = -__builtin_inff();
+        __syncthreads();
+    }
     const int64_t m = PARTS ? int64_t(blockIdx.x) / a.S : int64_t(blockIdx.x);
     const int64_t sl = PARTS ? int64_t(blockIdx.x) - m * a.S : 0;
     const int64_t c0 = sl * a.part, n = min(a.V - c0, a.part);
     const T *p = static_cast<const T *>(a.x) + m * a.ld + c0;
-    TopList list;
-    if constexpr (TOP) list.init(buf + wave * 128);
-    RowStat r = scan_row<T, NT, 16 / LogitType<T>::kVec, true, TOP>(p, n, uint32_t(c0), a.c, a.k, list);
-    r = meet<NW, TOP>(r, a.c, list.list, buf, stats);
+    TopList<T> list;
+    if constexpr (TOP) list.init(aside + wave, bounds, NW, a.k);
+    RowStat r = scan_row<T, NT, true, TOP>(p, n, uint32_t(c0), a.c, list);
+    r = meet<NW, TOP>(r, a.c, list.list, lists, stats);
     if constexpr (PARTS) {
         const int64_t rec = m * a.S + sl;
         if (threadIdx.x == 0) a.ws_stats[rec] = r;
@@ -159,7 +166,7 @@ __global__ __launch_bounds__(256) void logprob_join_kernel(LogprobArgs a) {
     __shared__ uint64_t lists[TOP ? 256 : 1];
     __shared__ RowStat stats[4];
     const int64_t m = blockIdx.x;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     RowStat r = stat_none();
     for (int i = threadIdx.x; i < a.S; i += 256) r = stat_join(r, a.ws_stats[m * a.S + i], a.c);
     r = stat_wave(r, a.c);

@@ -107,7 +107,7 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void norm_kernel(NormArgs a)
             const int c = 8 * (t + TPR * g);
             if constexpr (sizeof(R) == 2) {
 #pragma unroll
-                for (int j = 0; j < 8; ++j) v[g].v[j] = __uint_as_float(uint32_t(f32_to_bf16_rne(v[g].v[j])) << 16);
+                for (int j = 0; j < 8; ++j) v[g].v[j] = __uint_as_float(uint32_t(round_bf16(v[g].v[j])) << 16);
             }
             if (a.h && c < a.K) store8(static_cast<R *>(a.h) + m * a.ldh + c, v[g]);
         }

@@ -678,7 +678,7 @@ ht_status ht_add_rms_norm_backward(const void *dy, int64_t lddy, int32_t yt, con
                                    void *dres, int64_t lddres, void *dx, int64_t lddx, float *dw, void *ws,
                                    size_t ws_bytes, ht_stream stream);
 
-/* Rows of logits: x [M][ld] of dtype `type`, V < 2^31 - 64 columns, M <= 2^22,
+/* Rows of logits: x [M][ld] of dtype `type`, V <= 2^29 columns, M <= 2^22,
  * temperature in [1e-30, 1e30];  z = x / temperature.  Entries of -Inf are not
  * allowed (probability 0); a row of nothing else has no distribution: log
  * probabilities of -Inf, entropy 0, gradients of 0.  Entries of the type's
@@ -739,7 +739,7 @@ ht_status ht_distill_backward(const float *d_loss, const void *logits, int64_t l
                               float temperature, void *dx, int64_t ldd, ht_stream stream);
 
 /* ht_distill_step -- loss and gradient in one call, each logit read once where a
- * row fits a compute unit's registers (65536 fp32 or 131072 bf16 columns), with
+ * row fits a compute unit's registers (81920 fp32 or 163840 bf16 columns), with
  * the loss's gradient known beforehand.
  *   weight      fp32 [M], d_loss of ht_distill_backward, or NULL (1); a row of
  *               weight 0 is not read: loss 0, gradient 0 (stats 0). */
