@@ -260,7 +260,8 @@ __device__ __forceinline__ uint64_t join_lists(uint64_t down, uint64_t up, int l
 // A wavefront's k largest so far.  Where a lane's entries reach `thr`, its two
 // 16-byte pieces are put aside in LDS, which costs the pass over the row a vote and
 // a few stores; 64 lanes' pieces at a time join the list.  thr is the larger of
-// two bounds:
+// two bounds (and the lowest finite value: entries of -Inf are not collected; the
+// first of them fill a row that allows fewer than k, at the end):
 //   - the smallest value above the k-th of the list, whose entries all come
 //     before those still to be read: an equal one has a higher index;
 //   - the least, over the workgroup's W wavefronts, of the ceil(k / W)-th largest
@@ -271,7 +272,7 @@ __device__ __forceinline__ uint64_t join_lists(uint64_t down, uint64_t up, int l
 //     in vain changes nothing in the result.
 template <typename T>
 struct TopList {
-    static constexpr int kVec = LogitType<T>::kVec, kMost = 128;
+    static constexpr int kVec = LogitType<T>::kVec, kMost = 128, kFew = 8;
     struct Aside {
         u32x4 piece[2][kMost];
         int32_t first[kMost];    // the first one's number in the row; the second's is `apart` further
@@ -285,7 +286,7 @@ struct TopList {
 
     __device__ __forceinline__ void init(Aside *a, float *s, int w, int top) {
         list = kth = 0;
-        thr = -__builtin_inff();
+        thr = kLowest;
         pending = 0;
         k = top;
         lane = threadIdx.x & 63;
@@ -317,9 +318,21 @@ struct TopList {
         thr = fmaxf(thr, least);
     }
 
-    // One entry per lane (0: none) joins the list.
-    __device__ __forceinline__ void take(uint64_t e) {
-        list = join_lists(list, sort_up(e, lane), lane);
+    // The entries of the lanes in `who` join the list: few one by one, each moving
+    // those below it one lane on, many by a sort and a merge.
+    __device__ __forceinline__ void take(uint64_t e, uint64_t who) {
+        if (__popcll(who) <= kFew) {
+            for (; who; who &= who - 1) {
+                const int from = __builtin_ctzll(who);
+                const uint64_t v = (uint64_t(uint32_t(__builtin_amdgcn_readlane(uint32_t(e >> 32), from))) << 32) |
+                                   uint32_t(__builtin_amdgcn_readlane(uint32_t(e), from));
+                const int at = __popcll(__ballot(list > v));
+                const uint64_t up = (uint64_t(dpp_u32<0x138>(uint32_t(list >> 32))) << 32) | dpp_u32<0x138>(uint32_t(list));
+                list = lane < at ? list : lane == at ? v : up;
+            }
+        } else {
+            list = join_lists(list, sort_up((who >> lane) & 1 ? e : 0, lane), lane);
+        }
         kth = (uint64_t(uint32_t(__builtin_amdgcn_readlane(uint32_t(list >> 32), k - 1))) << 32) |
               uint32_t(__builtin_amdgcn_readlane(uint32_t(list), k - 1));
     }
@@ -357,7 +370,7 @@ struct TopList {
         LogitType<T>::unpack(a, x);
         LogitType<T>::unpack(b, x + kVec);
 #pragma unroll
-        for (int j = 0; j < 2 * kVec; ++j) key[j] = first + j / kVec * apart < vecs ? order_key(x[j]) : 0;
+        for (int j = 0; j < 2 * kVec; ++j) key[j] = x[j] >= kLowest && first + j / kVec * apart < vecs ? order_key(x[j]) : 0;
         // each lane's largest in turn, while any belongs to the k
         for (;;) {
             uint32_t top = key[0];
@@ -368,9 +381,9 @@ struct TopList {
             for (int j = 2 * kVec - 1; j >= 0; --j) which = key[j] == top ? j : which;
             const uint32_t i = i0 + uint32_t(first + (which >= kVec ? apart : 0)) * kVec + uint32_t(which & (kVec - 1));
             const uint64_t e = top ? (uint64_t(top) << 32) | (0xFFFFFFFFu - i) : 0;
-            const bool in = e > kth;
-            if (__ballot(in) == 0) break;
-            take(in ? e : 0);
+            const uint64_t who = __ballot(e > kth);
+            if (who == 0) break;
+            take(e, who);
 #pragma unroll
             for (int j = 0; j < 2 * kVec; ++j) key[j] = j == which ? 0 : key[j];
         }

@@ -83,7 +83,7 @@ __device__ __forceinline__ RowStat scan_row(const T *p, int64_t n, uint32_t i0, 
         const int64_t i = t < sp.head ? int64_t(t) : n - sp.tail + (t - sp.head);
         const float x = live ? L::get(p + i) : -__builtin_inff();
         stat_add<1, ENT>(r, &x, x, c);
-        if constexpr (TOP) list.take(live ? entry_of(x, i0 + uint32_t(i)) : 0);
+        if constexpr (TOP) list.take(entry_of(x, i0 + uint32_t(i)), __ballot(live && x >= kLowest));
     }
     return stat_wave(r, c);
 }
@@ -125,9 +125,25 @@ __device__ __forceinline__ void write_row(const LogprobArgs &a, int64_t m, RowSt
             a.stats[2 * m + 1] = o.b;
         }
     }
-    if (tops && int(threadIdx.x) < a.k) {
-        a.top[m * a.k + threadIdx.x] = logp_of(o, key_value(uint32_t(list >> 32)), a.inv_t);
-        a.top_tokens[m * a.k + threadIdx.x] = o.kind == 2 ? -1 : int32_t(entry_index(list));
+    if (!tops || threadIdx.x >= 64) return;
+    const int lane = threadIdx.x;
+    int32_t token = int32_t(entry_index(list));
+    float logp = logp_of(o, key_value(uint32_t(list >> 32)), a.inv_t);
+    const int found = __popcll(__ballot(list != 0));
+    if (found < a.k) {
+        // fewer than k are allowed: the first of the others (the rest is -Inf: 128 entries hold 64 of them)
+        if (list == 0) logp = o.kind == 2 ? __builtin_nanf("") : -__builtin_inff();
+        int have = found;
+        for (int64_t i0 = 0; i0 < a.V && have < a.k && o.kind != 2; i0 += 64) {
+            const bool in = i0 + lane < a.V && LogitType<T>::get(row + i0 + lane) == -__builtin_inff();
+            uint64_t who = __ballot(in);
+            for (; who && have < a.k; ++have, who &= who - 1)
+                if (lane == have) token = int32_t(i0) + __builtin_ctzll(who);
+        }
+    }
+    if (lane < a.k) {
+        a.top[m * a.k + lane] = logp;
+        a.top_tokens[m * a.k + lane] = o.kind == 2 ? -1 : token;
     }
 }
 
@@ -187,13 +203,15 @@ struct LogprobShape {
     int64_t part;
 };
 
-// Parts of a row: enough workgroups for the card, each of at least 4096
-// entries (one step of its 256 threads).
+// Parts of a row: two workgroups for each compute unit, of at least 16384 entries
+// each: parts cost a second launch (4 us) and its joins.  With 20 alternatives,
+// fp32, whole and in parts: 64 x 32000 13.5 us and 15.0 (parts of 4000), 4 x 128000
+// 25.2 and 15.4, 64 x 128000 28.7 and 18.0, 256 x 128000 31.2 and 29.1.  Whole
+// rows by 1024 threads: 16.1 us for 64 x 32000 and 35 against 17.7 for 512 x 32000.
 LogprobShape logprob_shape(int64_t M, int64_t V) {
     LogprobShape s{1, V};
-    if (M >= 256) return s;
-    int64_t S = (1024 + M - 1) / M;
-    const int64_t most = (V + 4095) / 4096;
+    int64_t S = (512 + M - 1) / M;
+    const int64_t most = V / 16384;
     if (S > most) S = most;
     if (S > 256) S = 256;
     if (S <= 1) return s;
