@@ -496,6 +496,10 @@ class Q8Rows(NamedTuple):
 def q8_rows(M: int, K: int, device) -> Q8Rows:
     """Buffers for 8-bit rows [M, K]."""
     B.ht_q8_bytes(M, K)       # refuses what the kernels do not take
+    return _new_q8(M, K, device)
+
+
+def _new_q8(M: int, K: int, device) -> Q8Rows:
     G = -(-M // 16)
     return Q8Rows(torch.empty(G, K // 64, 64, 16, dtype=torch.int8, device=device),
                   torch.empty(K // 64, 16 * G, dtype=torch.float32, device=device), int(M))
@@ -590,8 +594,8 @@ def add_rms_norm(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor |
     if dt not in (torch.float32, torch.bfloat16):
         raise ValueError(f"out_dtype: expected fp32 or bf16, got {dt}")
     if out is None:
-        y = torch.empty(x.shape, dtype=dt, device=x.device)
-        h = torch.empty(x.shape, dtype=residual.dtype, device=x.device) if residual is not None else None
+        y = torch.empty_like(x, dtype=dt, memory_format=torch.contiguous_format)
+        h = torch.empty_like(residual, memory_format=torch.contiguous_format) if residual is not None else None
     else:
         y = _out_matrix(out[0], "out[0]", x.shape, dt)
         h = _out_matrix(out[1], "out[1]", x.shape, residual.dtype) if residual is not None else None
@@ -609,8 +613,8 @@ def add_rms_norm_q8(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tenso
             return add_rms_norm_q8(x, weight, residual, eps, out)
     x, residual = _norm_args(x, weight, residual)
     if out is None:
-        q = q8_rows(*x.shape, x.device)
-        h = torch.empty(x.shape, dtype=residual.dtype, device=x.device) if residual is not None else None
+        q = _new_q8(*x.shape, x.device)
+        h = torch.empty_like(residual, memory_format=torch.contiguous_format) if residual is not None else None
     else:
         q, h = out[0], _out_matrix(out[1], "out[1]", x.shape, residual.dtype) if residual is not None else None
     desc = _q8_desc(q)
@@ -698,9 +702,13 @@ def token_logprobs(logits: torch.Tensor, tokens: torch.Tensor | None = None, top
     if not 0 <= top <= min(64, V):
         raise ValueError(f"top: expected 0 to {min(64, V)}, got {top}")
     _on_gpu(logits, tokens, ws)
-    new = lambda shape, dt=torch.float32: torch.empty(shape, dtype=dt, device=logits.device)  # noqa: E731
-    r = TokenLogprobs(None if tokens is None else new(tokens.shape), new((M,)), new((M, top)),
-                      new((M, top), torch.int32), new((M, 2)))
+    # one allocation for the fp32 results
+    n = B._count(tokens) * M
+    buf = torch.empty(n + (3 + top) * M, dtype=torch.float32, device=logits.device)
+    r = TokenLogprobs(None if tokens is None else buf.as_strided(tokens.shape, tokens.stride()),
+                      buf.as_strided((M,), (1,), n), buf.as_strided((M, top), (top, 1), n + 3 * M),
+                      torch.empty((M, top), dtype=torch.int32, device=logits.device),
+                      buf.as_strided((M, 2), (2, 1), n + M))
     if ws is None:
         ws = _scratch(B.ht_token_logprobs_workspace(M, V, top), logits.device)
     B.ht_token_logprobs(logits, tokens, temperature, *r, ws=ws)
@@ -802,3 +810,17 @@ def distill_step(logits: torch.Tensor, ids: torch.Tensor, teacher: torch.Tensor,
     _on_gpu(x, ids, teacher, weight, out, stats)
     B.ht_distill_step(x, ids, teacher, weight, temperature, loss, stats, out)
     return loss, out
+
+
+def scale_rows(x: torch.Tensor, factor: torch.Tensor, stream=None) -> None:
+    """x [M, V] (fp32 or bf16, dense rows) times factor fp32 [1] in place;
+    nothing moves where it is 1 (ht_scale_rows)."""
+    if stream is not None:
+        with _using(stream):
+            return scale_rows(x, factor)
+    if x.dim() != 2:
+        raise ValueError(f"x: expected [rows, columns], got {tuple(x.shape)}")
+    _out_matrix(x, "x", x.shape, x.dtype)
+    _need(factor, "factor", torch.float32, (1,))
+    _on_gpu(x, factor)
+    B.ht_scale_rows(x, factor)

@@ -39,7 +39,7 @@ EXPORTS = ("ht_status_string", "ht_plan_params_default", "ht_plan", "ht_plan_cou
            "ht_q8_bytes", "ht_q8_values", "ht_linear_q8_workspace", "ht_linear_forward_q8",
            "ht_add_rms_norm", "ht_add_rms_norm_workspace", "ht_add_rms_norm_backward",
            "ht_token_logprobs_workspace", "ht_token_logprobs", "ht_token_logprobs_backward",
-           "ht_distill_loss", "ht_distill_backward", "ht_distill_step")
+           "ht_distill_loss", "ht_distill_backward", "ht_distill_step", "ht_scale_rows")
 
 
 class HTError(RuntimeError):
@@ -194,6 +194,8 @@ def load() -> ctypes.CDLL:
     lib.ht_distill_backward.argtypes = [P, P, I64, I32, I64, I64, P, P, I32, P, F, P, I64, P]
     lib.ht_distill_step.restype = St
     lib.ht_distill_step.argtypes = [P, I64, I32, I64, I64, P, P, I32, P, F, P, P, P, I64, P]
+    lib.ht_scale_rows.restype = St
+    lib.ht_scale_rows.argtypes = [P, I64, I32, I64, I64, P, P]
     _lib = lib
     return lib
 
@@ -586,3 +588,7 @@ def ht_distill_step(logits, ids, teacher, weight, temperature: float, loss, stat
     _check("ht_distill_step", load().ht_distill_step(
         *_mat(logits), _act(logits), *logits.shape, ids.data_ptr(), teacher.data_ptr(), ids.shape[1], _ptr(weight),
         temperature, loss.data_ptr(), _ptr(stats), *_mat(dx), _stream(stream)))
+
+
+def ht_scale_rows(dx, g, stream=None) -> None:
+    _check("ht_scale_rows", load().ht_scale_rows(*_mat(dx), _act(dx), *dx.shape, g.data_ptr(), _stream(stream)))

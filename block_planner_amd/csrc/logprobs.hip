@@ -26,68 +26,6 @@ struct LogprobArgs {
     uint64_t *ws_top;           // [M][S][k]
 };
 
-// Statistics and largest entries of n entries from p on, whose first has index
-// i0; every wavefront's result in its lanes.
-template <typename T, int NT, bool ENT, bool TOP>
-__device__ __forceinline__ RowStat scan_row(const T *p, int64_t n, uint32_t i0, float c, TopList<T> &list) {
-    using L = LogitType<T>;
-    constexpr int kVec = L::kVec, U = 16 / kVec;     // 16 entries per thread and step
-    const Span sp = span_of(p, n);
-    const int32_t t = threadIdx.x;
-    RowStat r = stat_none();
-    const Pieces in(p + sp.head, sp.vecs);
-    u32x4 next[U];
-    const auto load = [&](int32_t at) {
-#pragma unroll
-        for (int u = 0; u < U; ++u) next[u] = in.load<2>(16u * uint32_t(at + u * NT + t));   // not kept in the caches
-    };
-    load(0);
-    float lane_top = -__builtin_inff();
-    int step = 0, renew = 1;                         // bounds are published after steps 1, 2, 3, 4, 6, 9, ...
-    for (int32_t at = 0; at < sp.vecs; at += U * NT) {
-        u32x4 cur[U];
-        float x[U * kVec], top[U / 2];
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            cur[u] = at + (u + 1) * NT <= sp.vecs || at + u * NT + t < sp.vecs ? next[u] : no_entries<T>();
-            L::unpack(cur[u], x + u * kVec);
-        }
-        load(at + U * NT);
-#pragma unroll
-        for (int h = 0; h < U / 2; ++h) {
-            top[h] = x[2 * h * kVec];
-#pragma unroll
-            for (int j = 1; j < 2 * kVec; ++j) top[h] = fmaxf(top[h], x[2 * h * kVec + j]);
-        }
-        const float most = U > 2 ? fmaxf(top[0], top[U / 2 - 1]) : top[0];
-        stat_add<U * kVec, ENT>(r, x, most, c);
-        if constexpr (TOP) {
-            lane_top = fmaxf(lane_top, most);
-            if (++step == renew) {
-                list.raise(lane_top);
-                if (step == 1) __syncthreads();      // no wavefront collects without a bound
-                list.refresh();
-                renew += (step + 1) / 2;
-            }
-            const bool last = at + U * NT >= sp.vecs;
-#pragma unroll
-            for (int h = 0; h < U / 2; ++h) {
-                list.put(top[h], cur[2 * h], cur[2 * h + 1], at + 2 * h * NT + t);
-                while (list.pending >= 64 || (last && h == U / 2 - 1 && list.pending > 0))
-                    list.flush(NT, sp.vecs, i0 + uint32_t(sp.head));
-            }
-        }
-    }
-    if (t < 64 && sp.head + sp.tail) {               // the single ones before and after, by the first wavefront
-        const bool live = t < sp.head + sp.tail;
-        const int64_t i = t < sp.head ? int64_t(t) : n - sp.tail + (t - sp.head);
-        const float x = live ? L::get(p + i) : -__builtin_inff();
-        stat_add<1, ENT>(r, &x, x, c);
-        if constexpr (TOP) list.take(entry_of(x, i0 + uint32_t(i)), __ballot(live && x >= kLowest));
-    }
-    return stat_wave(r, c);
-}
-
 // The wavefronts' lists and statistics as one, valid in the first wavefront
 // (statistics in all).
 template <int NW, bool TOP>

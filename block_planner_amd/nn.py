@@ -1,6 +1,8 @@
 """PyTorch modules over the C ABI: HyperLinear, scan_model,
 wrap_model_with_hypertensor and save/load of packed models; HyperAttention
-over a paged 8-bit cache (KVPool); qk_norm_rope with its gradient.
+over a paged 8-bit cache (KVPool); qk_norm_rope with its gradient; AddRMSNorm,
+token_logprobs and distill_loss, differentiable, for what stands between two
+layers and around the last linear.
 
 Follows the user calls of the HyperTensor 1.0.1 page ("Usage Example":
 HyperLinear layers with ReLU; "Convert model": scan_model, then
@@ -173,6 +175,8 @@ class HyperLinear(torch.nn.Module):
                                    and self._calls % self.refresh_every == 0):
             self.pack()
         self._calls += 1
+        if isinstance(x, api.Q8Rows):
+            return self._forward_q8(x)
         if x.shape[-1] != self.in_features:
             raise ValueError(f"expected {self.in_features} input features, got {x.shape[-1]}")
         lead = x.shape[:-1]
@@ -185,6 +189,15 @@ class HyperLinear(torch.nn.Module):
         else:
             y = api.linear(self.packed, x2.to(torch.bfloat16).contiguous())
         return y.reshape(*lead, self.out_features)
+
+    def _forward_q8(self, x: api.Q8Rows) -> torch.Tensor:
+        """8-bit rows (AddRMSNorm with bits8): fp32 [rows, out_features]."""
+        if torch.is_grad_enabled() and self.weight is not None and self.weight.requires_grad:
+            raise RuntimeError("HyperLinear has no backward pass through 8-bit rows: call it under torch.no_grad() "
+                               "(its weight requires a gradient)")
+        if 64 * x.codes.shape[1] != self.in_features:
+            raise ValueError(f"expected {self.in_features} input features, got {64 * x.codes.shape[1]}")
+        return api.linear(self.packed, x)
 
     def extra_repr(self) -> str:
         mix = ""
@@ -344,6 +357,175 @@ class HyperAttention(torch.nn.Module):
 
     def extra_repr(self) -> str:
         return f"heads={self.n_heads}, kv_heads={self.n_kv_heads}, head_dim={self.head_dim}, window={self.window}"
+
+
+# -----------------------------------------------------------------------------
+# Between two layers, and around the last linear
+# -----------------------------------------------------------------------------
+class _AddRMSNormFn(torch.autograd.Function):
+    """api.add_rms_norm with ht_add_rms_norm_backward."""
+
+    @staticmethod
+    def forward(ctx, x, weight, residual, eps, out_dtype):
+        y, h = api.add_rms_norm(x, weight, residual, eps, out_dtype)
+        ctx.eps, ctx.x_dtype, ctx.res = eps, x.dtype, residual is not None
+        ctx.save_for_backward(x if h is None else h, weight)
+        ctx.set_materialize_grads(False)
+        return y, h
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dy, dh):
+        h, weight = ctx.saved_tensors
+        if dy is None:                       # the norm's output is not used: the sum's gradient alone
+            return None if dh is None else dh.to(ctx.x_dtype), None, dh, None, None
+        dx, dres, dw = api.add_rms_norm_backward(dy, h, weight, dh, ctx.eps, ctx.x_dtype)
+        return dx, dw, dres if ctx.res else None, None, None
+
+
+def add_rms_norm(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor | None = None, eps: float = 1e-6,
+                 out_dtype=None) -> tuple:
+    """Differentiable api.add_rms_norm over any leading dims: (y, h), h = x +
+    residual (None without one) and y its norm times weight, bf16 by default.
+    Gradients for x, weight and residual."""
+    shape = x.shape
+    if residual is not None and residual.shape != shape:
+        raise ValueError(f"residual: expected {tuple(shape)}, got {tuple(residual.shape)}")
+    y, h = _AddRMSNormFn.apply(x.reshape(-1, shape[-1]), weight,
+                               None if residual is None else residual.reshape(-1, shape[-1]), float(eps), out_dtype)
+    return y.view(shape), None if h is None else h.view(shape)
+
+
+class AddRMSNorm(torch.nn.Module):
+    """The norm between two layers: forward(x, residual) gives (y, h), the norm
+    of h = x + residual for the next linear and h, the next residual (of x
+    itself and None without one).
+
+        y, h = norm(attention(...), h)
+        y, h = next_norm(linear(y), h)
+
+    x and residual fp32 or bf16 [..., hidden]; y in out_dtype (bf16, what
+    HyperLinear takes).  With bits8 y is api.Q8Rows of the flattened rows, the
+    input of a HyperLinear in 8 bits, for serving (no backward pass)."""
+
+    def __init__(self, hidden: int, eps: float = 1e-6, out_dtype=None, bits8: bool = False, device=None):
+        super().__init__()
+        if hidden % (64 if bits8 else 8):
+            raise ValueError(f"hidden must be a multiple of {64 if bits8 else 8}")
+        dev = torch.device(device) if device is not None else torch.device("cuda", torch.cuda.current_device())
+        self.hidden, self.eps, self.out_dtype, self.bits8 = int(hidden), float(eps), out_dtype, bool(bits8)
+        self.weight = torch.nn.Parameter(torch.ones(hidden, dtype=torch.float32, device=dev))
+
+    def forward(self, x: torch.Tensor, residual: torch.Tensor | None = None) -> tuple:
+        w = self.weight.float()              # the kernels read it in fp32, whatever the module was cast to
+        if not self.bits8:
+            return add_rms_norm(x, w, residual, self.eps, self.out_dtype)
+        if torch.is_grad_enabled() and (x.requires_grad or w.requires_grad or (residual is not None and residual.requires_grad)):
+            raise RuntimeError("AddRMSNorm has no backward pass through 8-bit rows: call it under torch.no_grad()")
+        flat = lambda t: None if t is None else t.reshape(-1, self.hidden)  # noqa: E731
+        q, h = api.add_rms_norm_q8(flat(x), w, flat(residual), self.eps)
+        return q, None if h is None else h.view(x.shape)
+
+    def extra_repr(self) -> str:
+        return f"{self.hidden}, eps={self.eps}, bits8={self.bits8}"
+
+
+def _int32(t: torch.Tensor, V: int) -> torch.Tensor:
+    """Tokens as the kernels read them; one outside [0, V) stays outside."""
+    if t.dtype != torch.int32:
+        if t.is_floating_point() or t.dtype == torch.bool:
+            raise ValueError(f"tokens: expected whole numbers, got {t.dtype}")
+        t = t.clamp(-1, V).to(torch.int32)
+    return t.contiguous()
+
+
+class _TokenLogprobsFn(torch.autograd.Function):
+    """api.token_logprobs with ht_token_logprobs_backward."""
+
+    @staticmethod
+    def forward(ctx, logits, tokens, temperature):
+        r = api.token_logprobs(logits, tokens, temperature=temperature)
+        ctx.temperature = temperature
+        # the results share one allocation: copies leave the saved ones out of the reach of in-place changes
+        ctx.save_for_backward(logits, tokens, r.stats, r.entropy)
+        ctx.set_materialize_grads(False)
+        return r.logprobs.clone(), r.entropy.clone()
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, d_logprobs, d_entropy):
+        if d_logprobs is None and d_entropy is None:
+            return None, None, None
+        logits, tokens, stats, entropy = ctx.saved_tensors
+        cont = lambda t: None if t is None else t.contiguous()  # noqa: E731
+        return api.token_logprobs_backward(cont(d_logprobs), cont(d_entropy), logits,
+                                           None if d_logprobs is None else tokens, stats, entropy, ctx.temperature), None, None
+
+
+def token_logprobs(logits: torch.Tensor, tokens: torch.Tensor, temperature: float = 1.0) -> tuple:
+    """Differentiable log probabilities: (logprobs, entropy) of logits [..., V]
+    (fp32 or bf16), tokens [...] or [..., n] of any whole type; logprobs fp32 in
+    tokens' shape, 0 for a token outside [0, V); entropy fp32 [...]."""
+    lead, V = logits.shape[:-1], logits.shape[-1]
+    if tokens.shape != lead and tokens.shape[:-1] != lead:
+        raise ValueError(f"tokens: expected {tuple(lead)} or {tuple(lead)} + (n,), got {tuple(tokens.shape)}")
+    flat = tokens.reshape(-1) if tokens.shape == lead else tokens.reshape(-1, tokens.shape[-1])
+    logp, entropy = _TokenLogprobsFn.apply(logits.reshape(-1, V), _int32(flat, V), float(temperature))
+    return logp.view(tokens.shape), entropy.view(lead)
+
+
+class _DistillFn(torch.autograd.Function):
+    """sum(weight * loss) by api.distill_step, whose gradient is kept for the
+    first backward call; another one starts from the kept statistics."""
+
+    @staticmethod
+    def forward(ctx, logits, ids, teacher, weight, temperature):
+        stats = torch.empty(logits.shape[0], 2, dtype=torch.float32, device=logits.device)
+        loss, ctx.d = api.distill_step(logits, ids, teacher, weight, temperature, stats=stats)
+        ctx.temperature = temperature
+        ctx.save_for_backward(logits, ids, teacher, weight, stats)
+        return (weight * loss).sum()
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, g):
+        logits, ids, teacher, weight, stats = ctx.saved_tensors
+        d, ctx.d = ctx.d, None
+        if d is not None:
+            api.scale_rows(d, g.reshape(1))
+        else:
+            d = api.distill_backward(weight * g, logits, ids, teacher, stats, ctx.temperature)
+        return d, None, None, None, None
+
+
+def distill_loss(logits: torch.Tensor, ids: torch.Tensor, teacher: torch.Tensor, weight: torch.Tensor | None = None,
+                 temperature: float = 1.0) -> torch.Tensor:
+    """Distillation from a teacher's top entries: sum(weight * loss) over the
+    rows of the student's logits [..., V] (fp32 or bf16), differentiable in
+    them.  ids [..., k] (whole numbers; outside [0, V): not kept) and teacher fp32
+    [..., k], its logits or log probabilities there (api.token_logprobs'
+    top_tokens and top_logprobs); weight [...] fp32, by default 1 / rows (the
+    mean); rows of weight 0 are not read.  loss is the divergence of the
+    teacher's softmax over its kept entries from the student's over all, both
+    at the temperature; its gradient shrinks with the temperature's square,
+    which belongs into weight where it is mixed with another loss."""
+    lead, V = logits.shape[:-1], logits.shape[-1]
+    if ids.shape[:-1] != lead or teacher.shape != ids.shape:
+        raise ValueError(f"ids, teacher: expected {tuple(lead)} + (k,), got {tuple(ids.shape)} and {tuple(teacher.shape)}")
+    x = logits.reshape(-1, V)
+    M, k = x.shape[0], ids.shape[-1]
+    ids = _int32(ids.reshape(M, k), V)
+    teacher = teacher.reshape(M, k).float().contiguous()
+    if weight is None:
+        weight = torch.full((M,), 1.0 / max(M, 1), dtype=torch.float32, device=x.device)
+    else:
+        if weight.shape != lead:
+            raise ValueError(f"weight: expected {tuple(lead)}, got {tuple(weight.shape)}")
+        weight = weight.detach().reshape(M).float().contiguous()
+    if torch.is_grad_enabled() and x.requires_grad:
+        return _DistillFn.apply(x, ids, teacher.detach(), weight, float(temperature))
+    loss, _ = api.distill_loss(x, ids, teacher, temperature)
+    return torch.where(weight != 0, weight * loss, 0.0).sum()
 
 
 # -----------------------------------------------------------------------------

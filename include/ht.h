@@ -747,6 +747,11 @@ ht_status ht_distill_step(const void *logits, int64_t ld, int32_t type, int64_t 
                           const float *teacher, int32_t k, const float *weight, float temperature, float *loss,
                           float *stats, void *dx, int64_t ldd, ht_stream stream);
 
+/* ht_scale_rows -- rows [M][V] times *g (fp32, device) in place; nothing is read or
+ * written where it is 1: the step's gradient under the gradient of what was made
+ * of its loss, which is rarely anything else. */
+ht_status ht_scale_rows(void *dx, int64_t ldd, int32_t type, int64_t M, int64_t V, const float *g, ht_stream stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -139,3 +139,24 @@ def test_gradient_against_differences():
         u = rng.normal(size=h.shape)
         num = (f(h + step * u) - f(h - step * u)) / (2 * step)
         assert abs(num - (d * u).sum()) <= 1e-4 * np.linalg.norm(d) * np.linalg.norm(u)
+
+
+def test_a_row_of_more_than_a_gigabyte():
+    """Offsets within a row past 2^30 bytes: zeros with a few others."""
+    V = 300_000_007
+    x = torch.zeros(1, V, device=dev())
+    x[0, 5], x[0, V - 2], x[0, V - 1] = 12.0, 14.0, 13.0
+    s = np.exp(12.0) + np.exp(14.0) + np.exp(13.0) + V - 3
+    ids = torch.tensor([[V - 2, 5, 1 << 28]], dtype=torch.int32, device=dev())
+    r = api.token_logprobs(x, ids, top=5)
+    assert r.top_tokens[0].tolist() == [V - 2, V - 1, 5, 0, 1]
+    want = np.array([14.0, 12.0, 0.0]) - np.log(s)
+    assert np.abs(r.logprobs[0].double().cpu().numpy() - want).max() < 1e-5
+    t = torch.zeros(1, 3, device=dev())
+    loss, d = api.distill_step(x, ids, t)
+    assert abs(loss.item() - (-np.log(3) - want.mean())) < 1e-4
+    g = api.distill_backward(torch.ones(1, device=dev()), x, ids, t, api.distill_loss(x, ids, t)[1])
+    for grad in (d, g):
+        assert abs(grad[0, V - 2].item() - (np.exp(14.0) / s - 1 / 3)) < 1e-6 and abs(grad[0, 5].item() - (np.exp(12.0) / s - 1 / 3)) < 1e-6
+        assert abs(grad[0, V - 1].item() * s / np.exp(13.0) - 1) < 1e-4 and abs(grad[0, 1 << 27].item() * s - 1) < 1e-4
+        assert abs(grad[0, 1 << 28].item() - (1 / s - 1 / 3)) < 1e-6
