@@ -10,6 +10,8 @@
 // registers (8 consecutive values per thread and group), so its sum of squares
 // costs no second read: by one wavefront up to 2048 columns (four rows per
 // workgroup, no barrier), by 256 threads up to 8192, by 1024 above.
+#include <type_traits>
+
 #include "rows.h"
 
 namespace ht {
@@ -17,6 +19,7 @@ namespace ht {
 namespace {
 
 constexpr int64_t kNormMaxK = 32768;
+constexpr int kQ8MinExp = -119;   // a block's scale, 2^(E-7), stays a normal number
 
 struct NormArgs {
     const void *x, *res;
@@ -30,61 +33,130 @@ struct NormArgs {
     float eps, inv_k;
 };
 
+__device__ __forceinline__ double wave_sum(double v) {
+    v += dpp_f64<kDppXor1>(v);
+    v += dpp_f64<kDppXor2>(v);
+    v += dpp_f64<kDppHalfMirror>(v);
+    v += dpp_f64<kDppMirror>(v);
+    v += __shfl_xor(v, 16);
+    v += __shfl_xor(v, 32);
+    return v;
+}
+
 // Sum over the row's TPR threads (a wavefront, or the workgroup).
-template <int TPR>
-__device__ __forceinline__ float row_total(float v, float *part) {
+template <int TPR, typename F>
+__device__ __forceinline__ F row_total(F v, F *part) {
     v = wave_sum(v);
     if constexpr (TPR > 64) {
         if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = v;
         __syncthreads();
-        v = 0.f;
+        v = 0;
 #pragma unroll
         for (int i = 0; i < TPR / 64; ++i) v += part[i];
     }
     return v;
 }
 
-// The row's 8 values of one lane as codes; the 64-wide block's 8 lanes share
-// the scale.  The largest magnitude's bits, compared as whole numbers, tell a
-// block that holds Inf or NaN too.
-__device__ __forceinline__ void encode8(const Row8 &y, const NormArgs &a, int64_t m, int col, bool live) {
-    uint32_t top = 0;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) top = max(top, __float_as_uint(y.v[j]) & 0x7FFFFFFFu);
-    top = max(top, dpp_u32<kDppXor1>(top));
-    top = max(top, dpp_u32<kDppXor2>(top));
-    top = max(top, dpp_u32<kDppHalfMirror>(top));
-    const bool bad = top >= 0x7F800000u;
-    int E = 7;
-    if (top > 0 && !bad) (void)frexpf(__uint_as_float(top), &E);
-    uint32_t c[2] = {0, 0};
+// Largest over the 64-wide block's 8 lanes.
+__device__ __forceinline__ uint32_t block_top(uint32_t v) {
+    v = max(v, dpp_u32<kDppXor1>(v));
+    v = max(v, dpp_u32<kDppXor2>(v));
+    return max(v, dpp_u32<kDppHalfMirror>(v));
+}
+__device__ __forceinline__ uint64_t block_top(uint64_t v) {
+    const auto other = [&](auto ctrl) {
+        constexpr int kCtrl = decltype(ctrl)::value;
+        return (uint64_t(dpp_u32<kCtrl>(uint32_t(v >> 32))) << 32) | dpp_u32<kCtrl>(uint32_t(v));
+    };
+    v = max(v, other(std::integral_constant<int, kDppXor1>{}));
+    v = max(v, other(std::integral_constant<int, kDppXor2>{}));
+    return max(v, other(std::integral_constant<int, kDppHalfMirror>{}));
+}
+
+// The row's 8 values h r w of one lane as codes; the 64-wide block's 8 lanes share
+// the scale.  The codes are those of 64 bits (r is in 64 bits; in 32 the norm's
+// rounding moves about one code in 10^5 across a border, by a whole step), worked
+// out in 32 where that is certain (3001 x 2048 of fp32 + bf16: 13.8 us; all in 64
+// bits 16.8; 32 alone 12.4).  A scaled value, of at most 128, is off by 4 steps of
+// 2^-24, under 2^-14, so those within 2^-13 of a half are worked out again, and so are
+// blocks whose largest value is within 16 steps of a power of two or far from 1, or
+// whose r or w would make h r lose digits below fp32's normal numbers that the result
+// still shows (2^-150 2^20 of a largest value of 2^-100: 2^-23 of a step).  The
+// largest magnitude's bits, compared as whole numbers, tell a block that holds Inf or
+// NaN too.
+__device__ __forceinline__ void encode8(const Row8 &h, const Row8 &w, double r, const NormArgs &a, int64_t m, int col, bool live) {
+    float y[8];
+    const float rn = float(r);
+    uint32_t top = 0, wtop = 0;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-        const float v = fminf(127.0f, fmaxf(-127.0f, rintf(ldexpf(y.v[j], 7 - E))));
-        c[j >> 2] |= (uint32_t(int32_t(bad ? 0.0f : v)) & 0xFFu) << (8 * (j & 3));
+        y[j] = h.v[j] * rn * w.v[j];
+        top = max(top, __float_as_uint(y[j]) & 0x7FFFFFFFu);
+        wtop = max(wtop, __float_as_uint(w.v[j]) & 0x7FFFFFFFu);
+    }
+    top = block_top(top);
+    const uint32_t digits = top & 0x7FFFFFu;
+    bool bad = false;
+    int E = 7, q[8];
+    // from 2^-100 to 2^100, not at a power of two: 32 bits give the exponent
+    const bool sure = top >= 0x0D800000u && top < 0x71800000u && digits >= 16 && digits <= 0x7FFFEFu &&
+                      wtop < 0x49800000u && rn >= 0x1p-100f;
+    if (__all(!live || sure)) {
+        if (live) E = int(top >> 23) - 126;                        // 2^(E-1) <= top < 2^E
+        bool near = false;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float v = ldexpf(y[j], 7 - E), n = rintf(v);
+            near = near || fabsf(v - n) > 0.5f - 0x1p-13f;
+            q[j] = int(n);
+        }
+        if (__any(near)) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float v = ldexpf(y[j], 7 - E);
+                if (fabsf(v - rintf(v)) > 0.5f - 0x1p-13f) q[j] = int(rint(ldexp(double(h.v[j]) * r * double(w.v[j]), 7 - E)));
+            }
+        }
+    } else {
+        double z[8];
+        uint64_t most = 0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            z[j] = double(h.v[j]) * r * double(w.v[j]);
+            most = max(most, uint64_t(__double_as_longlong(z[j])) & 0x7FFFFFFFFFFFFFFFull);
+        }
+        most = block_top(most);
+        bad = !(float(__longlong_as_double((long long)most)) <= 3.402823466e+38f);
+        if (most > 0 && !bad) E = max(int(most >> 52) - 1022, kQ8MinExp);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) q[j] = bad ? 0 : int(rint(ldexp(z[j], 7 - E)));
     }
     if (!live) return;
+    uint32_t c[2] = {0, 0};
+#pragma unroll
+    for (int j = 0; j < 8; ++j) c[j >> 2] |= (uint32_t(min(max(q[j], -127), 127)) & 0xFFu) << (8 * (j & 3));
     const int64_t g = m >> 4;
-    const uint32_t r = uint32_t(m) & 15u, kb = uint32_t(col) >> 6, e = uint32_t(col) & 63u;
-    uint8_t *dst = a.codes + (g * (a.K / 64) + kb) * 1024 + 16u * (r + 16u * (e >> 4)) + (e & 15u);
+    const uint32_t i = uint32_t(m) & 15u, kb = uint32_t(col) >> 6, e = uint32_t(col) & 63u;
+    uint8_t *dst = a.codes + (g * (a.K / 64) + kb) * 1024 + 16u * (i + 16u * (e >> 4)) + (e & 15u);
     *reinterpret_cast<u32x2 *>(dst) = u32x2{c[0], c[1]};
     if (e == 0) a.scales[int64_t(kb) * a.Mp + m] = bad ? __builtin_nanf("") : ldexpf(1.0f, E - 7);
 }
 
-template <int TPR, int NV, typename X, typename R, bool RES>
+template <int TPR, int NV, typename X, typename R, bool RES, bool Q8>
 __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void norm_kernel(NormArgs a) {
+    using F = std::conditional_t<Q8, double, float>;
     constexpr int kRows = TPR >= 256 ? 1 : 256 / TPR;
-    __shared__ float part[16];
+    __shared__ F part[16];
     const int t = threadIdx.x & (TPR - 1);
     uint32_t b = blockIdx.x;
     // 8-bit rows: the 16 rows of a group share cache lines, so neighbouring
     // workgroups are placed on one XCD (workgroups go to the 8 XCDs in turn)
-    if (a.codes && (gridDim.x & 7u) == 0) b = (b & 7u) * (gridDim.x >> 3) + (b >> 3);
+    if (Q8 && (gridDim.x & 7u) == 0) b = (b & 7u) * (gridDim.x >> 3) + (b >> 3);
     const int64_t m = int64_t(b) * kRows + (threadIdx.x / TPR);
     if (m >= a.M) return;    // whole wavefronts (TPR = 64), never part of a workgroup that meets at a barrier
     const X *x = static_cast<const X *>(a.x) + m * a.ldx;
     Row8 v[NV];
-    float ss = 0.f;
+    F ss = 0;
 #pragma unroll
     for (int g = 0; g < NV; ++g) {
         const int c = 8 * (t + TPR * g);
@@ -115,22 +187,39 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void norm_kernel(NormArgs a)
 #pragma unroll
     for (int g = 0; g < NV; ++g)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) ss += v[g].v[j] * v[g].v[j];
-    const float rn = 1.0f / sqrtf(row_total<TPR>(ss, part) * a.inv_k + a.eps);
+        for (int j = 0; j < 8; ++j) ss += F(v[g].v[j]) * F(v[g].v[j]);
+    ss = row_total<TPR>(ss, part);
+    if constexpr (Q8) {
+        const double rn = 1.0 / sqrt(ss / a.K + double(a.eps));
 #pragma unroll
-    for (int g = 0; g < NV; ++g) {
-        const int c = 8 * (t + TPR * g);
-        const bool live = c < a.K;
-        if (live) {
+        for (int g = 0; g < NV; ++g) {
+            const int c = 8 * (t + TPR * g);
+            const bool live = c < a.K;
+            Row8 w{};
+            if (live) {
+                w = load8(a.w + c);
+                if (a.y) {
+                    Row8 o;
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) o.v[j] = v[g].v[j] * float(rn) * w.v[j];
+                    if (a.y_bf16) store8(static_cast<uint16_t *>(a.y) + m * a.ldy + c, o);
+                    else store8(static_cast<float *>(a.y) + m * a.ldy + c, o);
+                }
+            }
+            encode8(v[g], w, rn, a, m, c, live);
+        }
+    } else {
+        const float rn = 1.0f / sqrtf(ss * a.inv_k + a.eps);
+#pragma unroll
+        for (int g = 0; g < NV; ++g) {
+            const int c = 8 * (t + TPR * g);
+            if (c >= a.K) continue;
             const Row8 w = load8(a.w + c);
 #pragma unroll
             for (int j = 0; j < 8; ++j) v[g].v[j] = v[g].v[j] * rn * w.v[j];
-            if (a.y) {
-                if (a.y_bf16) store8(static_cast<uint16_t *>(a.y) + m * a.ldy + c, v[g]);
-                else store8(static_cast<float *>(a.y) + m * a.ldy + c, v[g]);
-            }
+            if (a.y_bf16) store8(static_cast<uint16_t *>(a.y) + m * a.ldy + c, v[g]);
+            else store8(static_cast<float *>(a.y) + m * a.ldy + c, v[g]);
         }
-        if (a.codes) encode8(v[g], a, m, c, live);
     }
 }
 
@@ -297,21 +386,27 @@ __global__ __launch_bounds__(256) void q8_values_kernel(const uint8_t *codes, co
     store8(p + 8, b);
 }
 
-template <int TPR, int NV>
-void launch_norm(const NormArgs &a, int32_t xt, int32_t rt, hipStream_t s) {
+template <int TPR, int NV, bool Q8>
+void launch_norm_as(const NormArgs &a, int32_t xt, int32_t rt, hipStream_t s) {
     constexpr int kThreads = TPR > 256 ? TPR : 256, kRows = TPR >= 256 ? 1 : 256 / TPR;
     const uint32_t grid = uint32_t((a.M + kRows - 1) / kRows);
     const bool xb = xt == HT_BF16, rb = rt == HT_BF16;
     if (!a.res) {
-        if (xb) norm_kernel<TPR, NV, uint16_t, float, false><<<grid, kThreads, 0, s>>>(a);
-        else norm_kernel<TPR, NV, float, float, false><<<grid, kThreads, 0, s>>>(a);
+        if (xb) norm_kernel<TPR, NV, uint16_t, float, false, Q8><<<grid, kThreads, 0, s>>>(a);
+        else norm_kernel<TPR, NV, float, float, false, Q8><<<grid, kThreads, 0, s>>>(a);
     } else if (xb) {
-        if (rb) norm_kernel<TPR, NV, uint16_t, uint16_t, true><<<grid, kThreads, 0, s>>>(a);
-        else norm_kernel<TPR, NV, uint16_t, float, true><<<grid, kThreads, 0, s>>>(a);
+        if (rb) norm_kernel<TPR, NV, uint16_t, uint16_t, true, Q8><<<grid, kThreads, 0, s>>>(a);
+        else norm_kernel<TPR, NV, uint16_t, float, true, Q8><<<grid, kThreads, 0, s>>>(a);
     } else {
-        if (rb) norm_kernel<TPR, NV, float, uint16_t, true><<<grid, kThreads, 0, s>>>(a);
-        else norm_kernel<TPR, NV, float, float, true><<<grid, kThreads, 0, s>>>(a);
+        if (rb) norm_kernel<TPR, NV, float, uint16_t, true, Q8><<<grid, kThreads, 0, s>>>(a);
+        else norm_kernel<TPR, NV, float, float, true, Q8><<<grid, kThreads, 0, s>>>(a);
     }
+}
+
+template <int TPR, int NV>
+void launch_norm(const NormArgs &a, int32_t xt, int32_t rt, hipStream_t s) {
+    if (a.codes) launch_norm_as<TPR, NV, true>(a, xt, rt, s);
+    else launch_norm_as<TPR, NV, false>(a, xt, rt, s);
 }
 
 template <int TPR, int NV>

@@ -616,8 +616,9 @@ ht_status ht_kv_attention_kernels(const ht_kv_cache *cache, int64_t T, int64_t R
 
 /* 8-bit rows [M][K]: the encoding HT_PATH_W8A8 makes of x, in the order in which
  * its kernel takes it.  Per row and 64 columns one scale: 2^(E-1) <= max |v| <
- * 2^E, code = clamp(rne(v 2^(7-E)), -127, 127), value = code 2^(E-7); an all-zero
- * block has scale 1, one that holds Inf or NaN a NaN scale and codes 0.
+ * 2^E, code = clamp(rne(v 2^(7-E)), -127, 127), value = code 2^(E-7), with E at
+ * least -119 here; an all-zero block has scale 1, one that holds Inf or NaN (past
+ * fp32's range) a NaN scale and codes 0.
  *   codes   int8 [ceil(M/16)][K/64][64][16]: row m, column 64 kb + e at
  *           [m / 16][kb][m % 16 + 16 (e / 16)][e % 16];
  *   scales  fp32 [K/64][16 ceil(M/16)]: row m's at [kb][m].
@@ -654,9 +655,10 @@ ht_status ht_linear_forward_q8(const ht_packed_weight *w, const ht_q8_rows *x, f
  *   h          out, dtype rt, or NULL (always without res);
  *   y          out, dtype yt, or NULL;
  *   q          (host) out: y as 8-bit rows (K % 64 == 0, q->M == M), or NULL;
- *              y or q or both.  The codes are of the fp32 values.
+ *              y or q or both.  The codes are of y in 64 bits, sums and all: fp32
+ *              would move some across a border, by a whole step.
  * h and y may be x or res themselves where dtype and stride are the same.  Sums
- * and products in fp32, one rounding at the end. */
+ * and products in fp32 (with q in 64 bits), one rounding at the end. */
 ht_status ht_add_rms_norm(const void *x, int64_t ldx, int32_t xt, const void *res, int64_t ldr, int32_t rt, int64_t M,
                           int64_t K, const float *w, float eps, void *h, int64_t ldh, void *y, int64_t ldy, int32_t yt,
                           const ht_q8_rows *q, ht_stream stream);

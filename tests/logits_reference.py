@@ -53,7 +53,7 @@ def q8_encode(y):
             top = np.abs(v).max()
             if top == 0:
                 continue
-            e = math.frexp(top)[1]
+            e = max(math.frexp(top)[1], -119)
             scales[m, b] = 2.0 ** (e - 7)
             codes[m, 64 * b:64 * b + 64] = np.clip(np.rint(v / 2.0 ** (e - 7)), -127, 127)
     return codes, scales

@@ -103,26 +103,55 @@ def test_zero_and_non_finite_rows():
 @pytest.mark.parametrize("M,K", [(1, 64), (15, 128), (16, 512), (17, 1024), (33, 2048), (128, 4096), (5, 8192), (3, 16384)])
 @pytest.mark.parametrize("x,r", [("fp32", "fp32"), ("bf16", "bf16"), ("fp32", None)])
 def test_q8(M, K, x, r):
-    """The codes are those of the kernel's own fp32 values (add_rms_norm's),
-    bit for bit, in the documented places; their values are exact."""
+    """The codes are those of the norm in 64 bits, in the documented places, their
+    values exact.  The host's 64 bits differ from the kernel's by some 2^-50: a code
+    may differ only where the scaled value lies within 2^-40 of a border, and a
+    scale only where the largest value lies that near a power of two (no case
+    here has either: the count is asserted)."""
     print(M, K, x, r, flush=True)
     rng = np.random.default_rng(M + K)
-    xg, _ = rows(rng, M, K, x, 3.0)
-    rg = rows(rng, M, K, r)[0] if r else None
+    xg, xh = rows(rng, M, K, x, 3.0)
+    rg, rh = rows(rng, M, K, r) if r else (None, 0.0)
     w = torch.rand(K, device=dev()) * 4
     w[:64] = 0 if K > 64 else w[:64]          # a block of zeros
-    y, h = api.add_rms_norm(xg, w, rg, out_dtype=torch.float32)
-    q, h8 = api.add_rms_norm_q8(xg, w, rg)
+    q, h = api.add_rms_norm_q8(xg, w, rg, eps=1e-6)
     values = api.q8_values(q), api.q8_values(q, torch.float32)
     torch.cuda.synchronize()
-    codes, scales = ref.q8_encode(y.cpu().numpy())
+    hw = ref.rounded((xh + rh).astype(np.float32), r) if r else xh
+    assert h is None if r is None else np.array_equal(host(h), hw)
+    codes, scales = ref.q8_encode(ref.norm(hw, host(w), float(np.float32(1e-6))))
     ci, si = ref.q8_index(M, K)
     assert np.array_equal(q.codes.cpu().numpy().reshape(-1)[ci], codes)
     assert np.array_equal(q.scales.cpu().numpy().reshape(-1)[si[:, ::64]], scales)
     want = codes * np.repeat(scales, 64, 1)
     for v in values:
         assert np.array_equal(host(v), want)
-    assert (h is None and h8 is None) or torch.equal(h, h8)
+
+
+def test_q8_of_tiny_and_huge_values():
+    """Blocks around the smallest scale, and past fp32's range."""
+    x = torch.ones(4, 256, device=dev())
+    w = torch.ones(256, device=dev())
+    w[:64], w[64:128], w[128:192], w[192:] = 2.0 ** -126, 2.0 ** -149, 3e38, 1.0
+    q, _ = api.add_rms_norm_q8(x, w, eps=0.0)
+    v = api.q8_values(q, torch.float32)
+    assert torch.all(v[:, :64] == 2.0 ** -126) and torch.all(v[:, 64:128] == 0) and torch.all(v[:, 192:] == 1)
+    assert torch.isfinite(v[:, 128:192]).all() and torch.all((v[:, 128:192] / 3e38 - 1).abs() <= 2.0 ** -7)
+    # h r below fp32's normal numbers, brought back by the weight: 64-bit values of
+    # this row, which 32 bits lose, and zeros beside them
+    y = torch.zeros(1, 256, device=dev())
+    y[0, :64], y[0, 64:128], y[0, 128] = torch.arange(1, 65, device=dev()) * 3e-14, 3e-14, 3e30
+    w[:64], w[64:128] = 3e38, 1e37
+    q, _ = api.add_rms_norm_q8(y, w, eps=0.0)
+    v = host(api.q8_values(q, torch.float32))
+    h = host(y)
+    want = h / np.sqrt(np.mean(h * h)) * host(w)
+    for b in range(2):
+        blk = want[:, 64 * b:64 * b + 64]
+        E = np.frexp(np.abs(blk).max())[1]
+        assert np.array_equal(v[:, 64 * b:64 * b + 64], np.rint(np.ldexp(blk, 7 - E)).clip(-127, 127) * 2.0 ** (E - 7))
+    x[:, 128:192] = 4.0
+    assert torch.isnan(api.q8_values(api.add_rms_norm_q8(x, w, eps=0.0)[0])[:, 128:192]).all()
 
 
 def weight(rng, N, K, int8):
