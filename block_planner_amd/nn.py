@@ -469,9 +469,18 @@ def token_logprobs(logits: torch.Tensor, tokens: torch.Tensor, temperature: floa
     lead, V = logits.shape[:-1], logits.shape[-1]
     if tokens.shape != lead and tokens.shape[:-1] != lead:
         raise ValueError(f"tokens: expected {tuple(lead)} or {tuple(lead)} + (n,), got {tuple(tokens.shape)}")
-    flat = tokens.reshape(-1) if tokens.shape == lead else tokens.reshape(-1, tokens.shape[-1])
+    flat = tokens.reshape(-1) if tokens.shape == lead else tokens.reshape(lead.numel(), tokens.shape[-1])
     logp, entropy = _TokenLogprobsFn.apply(logits.reshape(-1, V), _int32(flat, V), float(temperature))
     return logp.view(tokens.shape), entropy.view(lead)
+
+
+def _total(t: torch.Tensor) -> torch.Tensor:
+    """Sum of [M] in stages that no row of 256 leaves its workgroup in: one sum
+    over many workgroups clears its counters by a memset, which a captured
+    graph is not to hold."""
+    while t.numel() > 1024:
+        t = torch.nn.functional.pad(t, (0, -t.numel() % 256)).view(-1, 256).sum(1)
+    return t.sum()
 
 
 class _DistillFn(torch.autograd.Function):
@@ -484,7 +493,7 @@ class _DistillFn(torch.autograd.Function):
         loss, ctx.d = api.distill_step(logits, ids, teacher, weight, temperature, stats=stats)
         ctx.temperature = temperature
         ctx.save_for_backward(logits, ids, teacher, weight, stats)
-        return (weight * loss).sum()
+        return _total(weight * loss)
 
     @staticmethod
     @torch.autograd.function.once_differentiable
@@ -525,7 +534,7 @@ def distill_loss(logits: torch.Tensor, ids: torch.Tensor, teacher: torch.Tensor,
     if torch.is_grad_enabled() and x.requires_grad:
         return _DistillFn.apply(x, ids, teacher.detach(), weight, float(temperature))
     loss, _ = api.distill_loss(x, ids, teacher, temperature)
-    return torch.where(weight != 0, weight * loss, 0.0).sum()
+    return _total(torch.where(weight != 0, weight * loss, 0.0))
 
 
 # -----------------------------------------------------------------------------

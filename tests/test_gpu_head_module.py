@@ -290,6 +290,36 @@ def test_operators_in_graphs():
     captured(train, lambda i: (lg.normal_(), t2.normal_(), i2.random_(0, V), wt.uniform_(), dy.normal_(), h.normal_()))
 
 
+def test_training_loss_in_a_graph():
+    """Loss and gradient of the module, forward and backward captured, over more
+    rows than one workgroup adds; the loss within its sum's rounding (four
+    stages of at most 256 entries, 1024 in the last, and the product)."""
+    torch.manual_seed(7)
+    M, V, k = 70001, 40, 5
+    x = torch.randn(M, V, device=dev()).requires_grad_()
+    t, ids = torch.randn(M, k, device=dev()), torch.randint(0, V, (M, k), device=dev())
+    w = torch.rand(M, device=dev())
+    with torch.no_grad():
+        eager = htnn.distill_loss(x, ids, t, w)
+
+    def call():
+        loss = htnn.distill_loss(x, ids, t, w)
+        return loss.detach(), torch.autograd.grad(loss, x)[0]
+
+    captured(call, lambda i: (x.detach().normal_(), t.normal_(), ids.random_(0, V), w.uniform_()))
+    got, _ = call()
+    terms = host(w) * host(api.distill_loss(x.detach(), ids.int(), t)[0])
+    assert abs(got.item() - terms.sum()) <= (3 * 256 + 1024 + 1) * U * np.abs(terms).sum() and got != eager
+
+
+def test_no_tokens_a_row():
+    x = torch.randn(3, 2, 50, device=dev()).requires_grad_()
+    lp, ent = htnn.token_logprobs(x, torch.empty(3, 2, 0, dtype=torch.long, device=dev()))
+    assert lp.shape == (3, 2, 0) and ent.shape == (3, 2)
+    ent.sum().backward()
+    assert torch.isfinite(x.grad).all()
+
+
 def test_two_streams_at_once():
     """Calls of the same kind on two streams, each with its own temporaries."""
     torch.manual_seed(6)
