@@ -159,7 +159,7 @@ __global__ __launch_bounds__(NT, 8) void distill_loss_kernel(GradArgs a) {
     const int64_t m = blockIdx.x;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const T *row = static_cast<const T *>(a.x) + m * a.ld;
-    TopList<T> none;
+    TopList<T, NT / 64> none;
     const RowStat r = scan_row<T, NT, false, false>(row, a.V, 0, a.c, none);
     if (lane == 0) stats[wave] = r;
     bool any = false;

@@ -130,8 +130,8 @@ __device__ __forceinline__ float wave_top(float v) {
     v = fmaxf(v, dpp_f32<kDppXor2>(v));
     v = fmaxf(v, dpp_f32<kDppHalfMirror>(v));
     v = fmaxf(v, dpp_f32<kDppMirror>(v));
-    v = fmaxf(v, __shfl_xor(v, 16));
-    return fmaxf(v, __shfl_xor(v, 32));
+    v = fmaxf(v, row_xor16(v));
+    return fmaxf(v, row_xor32(v));
 }
 
 // Statistics relative to a larger or equal maximum.
@@ -257,65 +257,98 @@ __device__ __forceinline__ uint64_t join_lists(uint64_t down, uint64_t up, int l
     return sort_steps<128, 32>(down > up ? down : up, lane ^ 63);
 }
 
-// A wavefront's k largest so far.  Where a lane's entries reach `thr`, its two
-// 16-byte pieces are put aside in LDS, which costs the pass over the row a vote and
-// a few stores; 64 lanes' pieces at a time join the list.  thr is the larger of
-// two bounds (and the lowest finite value: entries of -Inf are not collected; the
-// first of them fill a row that allows fewer than k, at the end):
-//   - the smallest value above the k-th of the list, whose entries all come
-//     before those still to be read: an equal one has a higher index;
-//   - the least, over the workgroup's W wavefronts, of the ceil(k / W)-th largest
-//     of their lanes' maxima: k entries of the row reach it.  It costs 16 votes
-//     and no sort, so it is renewed often (raise): a row of n entries in no
-//     order puts about k log(n / k) pairs of pieces aside.  The wavefronts publish
-//     theirs without waiting: an older one is a lower bound, and what is put aside
-//     in vain changes nothing in the result.
-template <typename T>
-struct TopList {
-    static constexpr int kVec = LogitType<T>::kVec, kMost = 128, kFew = 8;
+// The k largest of what a workgroup of NW wavefronts reads.  Where a lane's entries
+// reach `thr`, its two 16-byte pieces are put aside in LDS, which costs the pass over
+// the row a vote and a few stores.  thr is never past the k-th largest (and at
+// least the lowest finite value: entries of -Inf are not collected; the first of them
+// fill a row that allows fewer than k, at the end).  It comes from the least, over
+// the wavefronts, of the ceil(k / NW)-th largest of their lanes' maxima: k entries of the
+// row reach that.  A wavefront's costs 24 votes (0.4 us) and no sort, so it is renewed
+// after 1, 2, 4, 8 ... steps (every half as often again: the same times): a row of n
+// entries in no order puts about k log2(n / 4096) pairs of pieces aside.  The wavefronts
+// publish theirs without waiting: an older one is a lower bound, and what is put
+// aside in vain changes nothing in the result.
+// At the end what reaches the last bound, 1.5 to 2 k entries, goes into one array,
+// and each entry's rank there is counted (1.3 us; 4 x 128000 with 20: 13.8 us a call,
+// with a list per wavefront, sorted and merged, 14.9).  Places in that array depend on who comes first;
+// ranks do not.  A wavefront that has put too much aside meanwhile moves 64 pairs into
+// a list of its own, sorted; so does one at the end where the array is too small (rows
+// of equal entries).  Rows in ascending order cost that all the time: 4096 x 128000
+// bf16, k = 20, 1.5 ms.
+template <typename T, int NW>
+struct TopShared {
+    static constexpr int kMost = NW > 4 ? 128 : 160, kCands = 256;
     struct Aside {
         u32x4 piece[2][kMost];
         int32_t first[kMost];    // the first one's number in the row; the second's is `apart` further
     };
+    union {
+        Aside aside[NW];
+        uint64_t lists[NW * 64]; // once nothing is put aside any more
+    };
+    uint64_t cand[kCands], best[64];
+    float bounds[NW];
+    int rank[kCands], count;
+
+    __device__ __forceinline__ void init() {
+        if (threadIdx.x < NW) bounds[threadIdx.x] = -__builtin_inff();
+        if (threadIdx.x < kCands) rank[threadIdx.x] = 0;
+        if (threadIdx.x == 0) count = 0;
+    }
+};
+
+template <typename T, int NW>
+struct TopList {
+    using Shared = TopShared<T, NW>;
+    static constexpr int kVec = LogitType<T>::kVec, kFew = 8;
     uint64_t list, kth;  // this lane's entry; the k-th, 0: none yet
     float thr;           // never NaN
-    int pending, k, lane;
-    int waves, part;     // part: ceil(k / waves)
-    Aside *aside;        // the wavefront's, in LDS
-    float *bounds;       // [waves] of the workgroup, in LDS, -Inf at first
+    float lane_top;      // the lane's largest entry, -Inf without one
+    int pending, k, lane, wave;
+    int part;            // ceil(k / NW)
+    Shared *sh;          // the workgroup's, in LDS
+    typename Shared::Aside *aside;
 
-    __device__ __forceinline__ void init(Aside *a, float *s, int w, int top) {
+    __device__ __forceinline__ void init(Shared *s, int top) {
         list = kth = 0;
         thr = kLowest;
+        lane_top = -__builtin_inff();
         pending = 0;
         k = top;
         lane = threadIdx.x & 63;
-        waves = w;
-        part = (k + w - 1) / w;
-        aside = a;
-        bounds = s;
+        wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+        part = (k + NW - 1) / NW;
+        sh = s;
+        aside = s->aside + wave;
     }
 
-    // Publishes the wavefront's bound; top: the lane's largest entry, -Inf without one.
-    __device__ __forceinline__ void raise(float top) {
-        // to 16 bits, from below; -Inf's are those of no number
-        const uint32_t key = order_key(top);
+    // Publishes the wavefront's bound.
+    __device__ __forceinline__ void raise() {
+        // to 16 bits, two at a time, from below; -Inf's are those of no number
+        const uint32_t key = order_key(lane_top);
         uint32_t p = 0;
 #pragma unroll
-        for (int bit = 31; bit >= 16; --bit) {
-            const uint32_t q = p | (1u << bit);
-            if (__popcll(__ballot(key >= q)) >= part) p = q;
+        for (int bit = 30; bit >= 16; bit -= 2) {
+            const uint32_t q1 = p | (1u << bit), q2 = p | (2u << bit), q3 = p | (3u << bit);
+            const int n1 = __popcll(__ballot(key >= q1)), n2 = __popcll(__ballot(key >= q2)), n3 = __popcll(__ballot(key >= q3));
+            p = n3 >= part ? q3 : n2 >= part ? q2 : n1 >= part ? q1 : p;
         }
         const float v = key_value(p);
         if (lane == 0 && v > -__builtin_inff())
-            __hip_atomic_store(&bounds[threadIdx.x >> 6], v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+            __hip_atomic_store(&sh->bounds[wave], v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
     }
 
-    __device__ __forceinline__ void refresh() {
-        float least = __builtin_inff();
-        for (int w = 0; w < waves; ++w)
-            least = fminf(least, __hip_atomic_load(&bounds[w], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP));
+    // The workgroup's bound, which thr takes over.
+    __device__ __forceinline__ float refresh() {
+        static_assert(NW <= 16 && (NW & (NW - 1)) == 0, "");
+        float least = __hip_atomic_load(&sh->bounds[lane & (NW - 1)], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+        if constexpr (NW > 1) least = fminf(least, dpp_f32<kDppXor1>(least));
+        if constexpr (NW > 2) least = fminf(least, dpp_f32<kDppXor2>(least));
+        if constexpr (NW > 4) least = fminf(least, dpp_f32<kDppHalfMirror>(least));
+        if constexpr (NW > 8) least = fminf(least, dpp_f32<kDppMirror>(least));
+        least = __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(least)));
         thr = fmaxf(thr, least);
+        return least;
     }
 
     // The entries of the lanes in `who` join the list: few one by one, each moving
@@ -358,10 +391,10 @@ struct TopList {
         const u32x4 a = aside->piece[0][lane], b = aside->piece[1][lane];
         const int32_t first = mine ? aside->first[lane] : vecs;
         const int32_t left = pending - 64;
-        if (lane < left) {
-            aside->piece[0][lane] = aside->piece[0][64 + lane];
-            aside->piece[1][lane] = aside->piece[1][64 + lane];
-            aside->first[lane] = aside->first[64 + lane];
+        for (int i = lane; i < left; i += 64) {
+            aside->piece[0][i] = aside->piece[0][64 + i];
+            aside->piece[1][i] = aside->piece[1][64 + i];
+            aside->first[i] = aside->first[64 + i];
         }
         asm volatile("" ::: "memory");
         pending = left > 0 ? left : 0;
@@ -389,12 +422,81 @@ struct TopList {
         }
         if (kth) thr = fmaxf(thr, key_value(uint32_t(kth >> 32) + 1));   // the next float up (-0 for 0 above the negative ones)
     }
+
+    // All that reach the last bound, of the whole workgroup, into sh->cand; between
+    // two barriers.  Their number, sh->count, may be more than it holds.  thr is past
+    // the k-th of a list already, whose own entries go by the workgroup's bound.
+    __device__ __forceinline__ void gather(int32_t apart, int32_t vecs, uint32_t i0) {
+        const float least = refresh();
+        bool old = lane < k && list != 0 && uint32_t(list >> 32) >= order_key(least);
+        for (int from = 0; from == 0 || from < pending; from += 64) {
+            const int i = from + lane;
+            const u32x4 a = aside->piece[0][i], b = aside->piece[1][i];
+            const int32_t first = i < pending ? aside->first[i] : vecs;
+            float x[2 * kVec];
+            LogitType<T>::unpack(a, x);
+            LogitType<T>::unpack(b, x + kVec);
+            if (first >= vecs) {
+#pragma unroll
+                for (int j = 0; j < kVec; ++j) x[j] = __builtin_nanf("");
+            }
+            if (first + apart >= vecs) {
+#pragma unroll
+                for (int j = kVec; j < 2 * kVec; ++j) x[j] = __builtin_nanf("");
+            }
+            uint32_t n = old ? 1 : 0;
+#pragma unroll
+            for (int j = 0; j < 2 * kVec; ++j) n += x[j] >= thr ? 1 : 0;
+            // places: the lanes' counts bit by bit
+            uint32_t at = 0, all = 0;
+#pragma unroll
+            for (int bit = 0; bit < 5; ++bit) {
+                const uint64_t who = __ballot((n >> bit) & 1);
+                at += uint32_t(__builtin_amdgcn_mbcnt_hi(uint32_t(who >> 32), __builtin_amdgcn_mbcnt_lo(uint32_t(who), 0))) << bit;
+                all += uint32_t(__popcll(who)) << bit;
+            }
+            if (all == 0) continue;
+            uint32_t base = 0;
+            if (lane == 0) base = uint32_t(atomicAdd(&sh->count, int(all)));
+            base = uint32_t(__builtin_amdgcn_readfirstlane(int(base)));
+            if (base + all > uint32_t(Shared::kCands)) return;      // too many: the count says so
+            at += base;
+            if (old) sh->cand[at++] = list;
+            old = false;
+#pragma unroll
+            for (int j = 0; j < 2 * kVec; ++j)
+                if (x[j] >= thr)
+                    sh->cand[at++] = entry_of(x[j], i0 + uint32_t(first + (j >= kVec ? apart : 0)) * kVec + uint32_t(j & (kVec - 1)));
+        }
+    }
+
+    // The 64 largest candidates in order, in the first wavefront: each goes to the
+    // place that the number of larger ones gives it, counted by as many threads per
+    // candidate as there are.
+    __device__ __forceinline__ void order() {
+        constexpr int NT = 64 * NW;
+        const int n = sh->count, t = threadIdx.x;
+        int wide = 32;                               // candidates' places: a power of two
+        while (wide < n) wide *= 2;
+        const int c = t & (wide - 1), slice = t / wide, slices = NT / wide < 16 ? NT / wide : 16;
+        if (c < n && slice < slices) {
+            const uint64_t mine = sh->cand[c];
+            int rank = 0;
+#pragma unroll 4
+            for (int i = slice; i < n; i += slices) rank += sh->cand[i] > mine ? 1 : 0;
+            if (rank) atomicAdd(&sh->rank[c], rank);
+        }
+        __syncthreads();
+        if (t < n && sh->rank[t] < 64) sh->best[sh->rank[t]] = sh->cand[t];
+        __syncthreads();
+        list = wave == 0 && lane < n ? sh->best[lane] : 0;
+    }
 };
 
 // Statistics and largest entries of n entries from p on, whose first has index
 // i0; every wavefront's result in its lanes.
 template <typename T, int NT, bool ENT, bool TOP>
-__device__ __forceinline__ RowStat scan_row(const T *p, int64_t n, uint32_t i0, float c, TopList<T> &list) {
+__device__ __forceinline__ RowStat scan_row(const T *p, int64_t n, uint32_t i0, float c, TopList<T, NT / 64> &list) {
     using L = LogitType<T>;
     constexpr int kVec = L::kVec, U = 16 / kVec;     // 16 entries per thread and step
     const Span sp = span_of(p, n);
@@ -407,7 +509,6 @@ __device__ __forceinline__ RowStat scan_row(const T *p, int64_t n, uint32_t i0, 
         for (int u = 0; u < U; ++u) next[u] = in.load<2>(16u * uint32_t(at + u * NT + t));   // not kept in the caches
     };
     load(0);
-    float lane_top = -__builtin_inff();
     int step = 0, renew = 1;                         // bounds are published after steps 1, 2, 3, 4, 6, 9, ...
     for (int32_t at = 0; at < sp.vecs; at += U * NT) {
         u32x4 cur[U];
@@ -427,19 +528,17 @@ __device__ __forceinline__ RowStat scan_row(const T *p, int64_t n, uint32_t i0, 
         const float most = U > 2 ? fmaxf(top[0], top[U / 2 - 1]) : top[0];
         stat_add<U * kVec, ENT>(r, x, most, c);
         if constexpr (TOP) {
-            lane_top = fmaxf(lane_top, most);
-            if (++step == renew) {
-                list.raise(lane_top);
+            list.lane_top = fmaxf(list.lane_top, most);
+            if (++step == renew && (step == 1 || at + U * NT < sp.vecs)) {   // the last bound comes after the row
+                list.raise();
                 if (step == 1) __syncthreads();      // no wavefront collects without a bound
                 list.refresh();
-                renew += (step + 1) / 2;
+                renew = 2 * step;
             }
-            const bool last = at + U * NT >= sp.vecs;
 #pragma unroll
             for (int h = 0; h < U / 2; ++h) {
                 list.put(top[h], cur[2 * h], cur[2 * h + 1], at + 2 * h * NT + t);
-                while (list.pending >= 64 || (last && h == U / 2 - 1 && list.pending > 0))
-                    list.flush(NT, sp.vecs, i0 + uint32_t(sp.head));
+                if (list.pending > TopShared<T, NT / 64>::kMost - 64) list.flush(NT, sp.vecs, i0 + uint32_t(sp.head));
             }
         }
     }

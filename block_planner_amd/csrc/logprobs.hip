@@ -6,8 +6,12 @@
 //
 // Bound by HBM: every logit is read once.  A workgroup takes a row, or one of
 // S parts of it where rows are few; each lane keeps (mx, s, t) of its entries,
-// each wavefront its k largest; they meet in LDS, and for parts in a second
-// kernel over the workspace.
+// its wavefronts put aside what may be among the k largest; they meet in LDS,
+// and for parts in a second kernel over the workspace.  4096 x 128000 bf16: 174 us without
+// alternatives, 6.0 TB/s, 191 with 20 and 219 with 64; a row of 32000 fp32 4.6 us, 9.3
+// with 20.
+#include <type_traits>
+
 #include "logits.h"
 
 namespace ht {
@@ -26,26 +30,20 @@ struct LogprobArgs {
     uint64_t *ws_top;           // [M][S][k]
 };
 
-// The wavefronts' lists and statistics as one, valid in the first wavefront
-// (statistics in all).
-template <int NW, bool TOP>
-__device__ __forceinline__ RowStat meet(RowStat r, float c, uint64_t &list, uint64_t *lists, RowStat *stats) {
+// The wavefronts' lists as one, in the first wavefront.
+template <int NW>
+__device__ __forceinline__ void meet_lists(uint64_t &list, uint64_t *lists) {
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     __syncthreads();
-    if (lane == 0) stats[wave] = r;
-    if constexpr (TOP) lists[wave * 64 + lane] = list;
+    lists[wave * 64 + lane] = list;
     __syncthreads();
-    r = stat_group<NW>(stats, c);
-    if constexpr (TOP) {
-        for (int w = NW / 2; w > 0; w >>= 1) {
-            if (wave < w) {
-                list = join_lists(list, lists[(wave + w) * 64 + 63 - lane], lane);
-                lists[wave * 64 + lane] = list;
-            }
-            __syncthreads();
+    for (int w = NW / 2; w > 0; w >>= 1) {
+        if (wave < w) {
+            list = join_lists(list, lists[(wave + w) * 64 + 63 - lane], lane);
+            lists[wave * 64 + lane] = list;
         }
+        __syncthreads();
     }
-    return r;
 }
 
 template <typename T>
@@ -88,23 +86,36 @@ __device__ __forceinline__ void write_row(const LogprobArgs &a, int64_t m, RowSt
 template <typename T, int NT, bool TOP, bool PARTS>
 __global__ __launch_bounds__(NT, TOP ? 6 : 8) void logprob_kernel(LogprobArgs a) {
     constexpr int NW = NT / 64;
-    __shared__ typename TopList<T>::Aside aside[TOP ? NW : 1];
-    uint64_t *lists = reinterpret_cast<uint64_t *>(aside);   // [NW][64], once nothing is put aside any more
+    __shared__ std::conditional_t<TOP, TopShared<T, NW>, int> sh;
     __shared__ RowStat stats[NW];
-    __shared__ float bounds[NW];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     if constexpr (TOP) {
-        if (threadIdx.x < NW) bounds[threadIdx.x] = -__builtin_inff();
+        sh.init();
         __syncthreads();
     }
     const int64_t m = PARTS ? int64_t(blockIdx.x) / a.S : int64_t(blockIdx.x);
     const int64_t sl = PARTS ? int64_t(blockIdx.x) - m * a.S : 0;
     const int64_t c0 = sl * a.part, n = min(a.V - c0, a.part);
     const T *p = static_cast<const T *>(a.x) + m * a.ld + c0;
-    TopList<T> list;
-    if constexpr (TOP) list.init(aside + wave, bounds, NW, a.k);
+    TopList<T, NW> list;
+    if constexpr (TOP) list.init(&sh, a.k);
     RowStat r = scan_row<T, NT, true, TOP>(p, n, uint32_t(c0), a.c, list);
-    r = meet<NW, TOP>(r, a.c, list.list, lists, stats);
+    if (lane == 0) stats[wave] = r;
+    if constexpr (TOP) list.raise();
+    __syncthreads();
+    r = stat_group<NW>(stats, a.c);
+    if constexpr (TOP) {
+        const Span sp = span_of(p, n);
+        const uint32_t i0 = uint32_t(c0) + uint32_t(sp.head);
+        list.gather(NT, sp.vecs, i0);
+        __syncthreads();
+        if (sh.count <= TopShared<T, NW>::kCands) {
+            list.order();
+        } else {                                     // many equal ones
+            while (list.pending > 0) list.flush(NT, sp.vecs, i0);
+            meet_lists<NW>(list.list, sh.lists);
+        }
+    }
     if constexpr (PARTS) {
         const int64_t rec = m * a.S + sl;
         if (threadIdx.x == 0) a.ws_stats[rec] = r;
@@ -124,6 +135,7 @@ __global__ __launch_bounds__(256) void logprob_join_kernel(LogprobArgs a) {
     RowStat r = stat_none();
     for (int i = threadIdx.x; i < a.S; i += 256) r = stat_join(r, a.ws_stats[m * a.S + i], a.c);
     r = stat_wave(r, a.c);
+    if (lane == 0) stats[wave] = r;
     uint64_t list = 0;
     if constexpr (TOP) {
         for (int i = wave; i < a.S; i += 4) {
@@ -132,7 +144,9 @@ __global__ __launch_bounds__(256) void logprob_join_kernel(LogprobArgs a) {
             list = join_lists(list, up, lane);
         }
     }
-    r = meet<4, TOP>(r, a.c, list, lists, stats);
+    if constexpr (TOP) meet_lists<4>(list, lists);
+    else __syncthreads();
+    r = stat_group<4>(stats, a.c);
     write_row<T>(a, m, r, list, TOP);
 }
 
@@ -142,10 +156,10 @@ struct LogprobShape {
 };
 
 // Parts of a row: two workgroups for each compute unit, of at least 16384 entries
-// each: parts cost a second launch (4 us) and its joins.  With 20 alternatives,
-// fp32, whole and in parts: 64 x 32000 13.5 us and 15.0 (parts of 4000), 4 x 128000
-// 25.2 and 15.4, 64 x 128000 28.7 and 18.0, 256 x 128000 31.2 and 29.1.  Whole
-// rows by 1024 threads: 16.1 us for 64 x 32000 and 35 against 17.7 for 512 x 32000.
+// each: parts cost a second launch and its joins.  With 20 alternatives, fp32,
+// without the host's part of a call, in parts of at least 8192, 16384 and 32768:
+// 1 x 128000 11.8, 12.1 and 14.4 us, 1 x 32000 10.3, 9.4 and 9.2, 64 x 32000 11.6,
+// 10.2 and 10.2, 64 x 128000 14.9, 16.1 and 16.7.
 LogprobShape logprob_shape(int64_t M, int64_t V) {
     LogprobShape s{1, V};
     int64_t S = (512 + M - 1) / M;
@@ -158,17 +172,28 @@ LogprobShape logprob_shape(int64_t M, int64_t V) {
     return s;
 }
 
+template <typename T, int NT>
+void launch_rows(const LogprobArgs &a, uint32_t grid, bool top, hipStream_t s) {
+    if (a.S == 1) {
+        if (top) logprob_kernel<T, NT, true, false><<<grid, NT, 0, s>>>(a);
+        else logprob_kernel<T, NT, false, false><<<grid, NT, 0, s>>>(a);
+    } else {
+        if (top) logprob_kernel<T, NT, true, true><<<grid, NT, 0, s>>>(a);
+        else logprob_kernel<T, NT, false, true><<<grid, NT, 0, s>>>(a);
+    }
+}
+
+// 512 threads where workgroups are few, or the list is long: without the host's
+// part of a call, with 20 alternatives, 10.2 us for 64 x 32000 fp32 (256 threads
+// 12.3, 1024 12.0), 11.3 for 256 x 32000 (13.3, 14.2); with 64, 18.8 for 512 x 32000
+// (256 threads 20.7), but 58 against 55 for 2048 x 32000.
 template <typename T>
 ht_status launch_logprobs(LogprobArgs &a, int64_t M, hipStream_t s) {
     const bool top = a.k > 0;
-    if (a.S == 1) {
-        const uint32_t grid = uint32_t(M);
-        if (top) logprob_kernel<T, 256, true, false><<<grid, 256, 0, s>>>(a);
-        else logprob_kernel<T, 256, false, false><<<grid, 256, 0, s>>>(a);
-    } else {
-        const uint32_t grid = uint32_t(M * a.S);
-        if (top) logprob_kernel<T, 256, true, true><<<grid, 256, 0, s>>>(a);
-        else logprob_kernel<T, 256, false, true><<<grid, 256, 0, s>>>(a);
+    const uint32_t grid = uint32_t(M * a.S);
+    if (grid <= 256 || (a.k > 32 && grid <= 1024)) launch_rows<T, 512>(a, grid, top, s);
+    else launch_rows<T, 256>(a, grid, top, s);
+    if (a.S > 1) {
         HT_LAUNCH_CHECK();
         if (top) logprob_join_kernel<T, true><<<uint32_t(M), 256, 0, s>>>(a);
         else logprob_join_kernel<T, false><<<uint32_t(M), 256, 0, s>>>(a);

@@ -41,11 +41,21 @@ __device__ __forceinline__ void store8(uint16_t *p, const Row8 &r) {
                                           pack_bf16(r.v[4], r.v[5]), pack_bf16(r.v[6], r.v[7])};
 }
 
+// The value of lane ^ 16, lane ^ 32, by the swaps of rows of 16 and of halves.
+__device__ __forceinline__ float row_xor16(float v) {
+    const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    return __uint_as_float(threadIdx.x & 16 ? r[0] : r[1]);
+}
+__device__ __forceinline__ float row_xor32(float v) {
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    return __uint_as_float(threadIdx.x & 32 ? r[0] : r[1]);
+}
+
 // Sum over a wavefront, the same on all lanes.
 __device__ __forceinline__ float wave_sum(float v) {
     v = group_sum<16>(v);
-    v += __shfl_xor(v, 16);
-    v += __shfl_xor(v, 32);
+    v += row_xor16(v);
+    v += row_xor32(v);
     return v;
 }
 

@@ -113,6 +113,22 @@ def test_parts_of_rows(M, V):
     check(r.top_logprobs[:few], top, b3, "top")
 
 
+@pytest.mark.parametrize("M,k", [(256, 20), (257, 20), (600, 64), (1025, 64)])
+@pytest.mark.parametrize("t", ["fp32", "bf16"])
+@pytest.mark.parametrize("kind", ["normal", "ties", "zeros", "up", "masked"])
+def test_many_rows(M, k, t, kind):
+    """Either side of the rules on threads per row, with more equal entries than
+    are counted at the end and rows that put everything aside."""
+    print(M, k, t, kind, flush=True)
+    rng = np.random.default_rng(M + k)
+    x, h = put(np.resize(logits(rng, kind, 12, 14001, t), (M, 14001)), t, shift=3)
+    rows = [0, 1, M - 1]
+    run(x[rows], h[rows], np.zeros((3, 1), int), k, 1.0)
+    r = api.token_logprobs(x, top=k)
+    want = ref.token_logprobs(h[:12], np.zeros((12, 1), int), k, 1.0)[3]
+    assert np.array_equal(r.top_tokens.cpu().numpy(), np.resize(want, (M, k)))
+
+
 def test_no_tokens_no_top_no_rows_other_stream():
     rng = np.random.default_rng(0)
     x, h = put(logits(rng, "normal", 5, 999), "fp32")
