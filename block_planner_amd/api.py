@@ -673,7 +673,7 @@ def _tokens(t: torch.Tensor, M: int) -> None:
 
 def _dlogits(logits: torch.Tensor, out: torch.Tensor | None) -> torch.Tensor:
     if out is None:
-        return torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
+        return torch.empty_like(logits, memory_format=torch.contiguous_format)
     return _out_matrix(out, "out", logits.shape, logits.dtype)
 
 

@@ -86,12 +86,19 @@ __device__ __forceinline__ void put_piece(T *y, u32x4 u) {
 }
 
 // Entry j's place written whole: the dense part and every g of that place, in
-// order, so that equal places write equal values.
+// order.  The first entry of a place writes it: two threads' equal sums may still be
+// rounded otherwise, by where the compiler fuses a product in each wavefront's code.
 template <typename T, bool ENT>
-__device__ __forceinline__ void put_given(T *dx, const Dense &d, float x, int32_t v, const int32_t *id, const float *g, int k) {
+__device__ __forceinline__ void put_given(T *dx, const Dense &d, float x, int j, const int32_t *id, const float *g, int k) {
+    const int32_t v = id[j];
     float sum = 0.f;
-    for (int i = 0; i < k; ++i) sum += id[i] == v ? g[i] : 0.f;
-    LogitType<T>::put(dx + v, d.scale * sum + dense_of<ENT>(d, x));
+    bool first = true;
+    for (int i = 0; i < k; ++i) {
+        const bool same = id[i] == v;
+        sum += same ? g[i] : 0.f;
+        first = first && !(same && i < j);
+    }
+    if (first) LogitType<T>::put(dx + v, __builtin_fmaf(d.scale, sum, dense_of<ENT>(d, x)));
 }
 
 // The teacher's distribution of a row by one wavefront: ids (-1: not kept), p, log2 p
@@ -149,7 +156,8 @@ __device__ __forceinline__ void put_loss(const GradArgs &a, int64_t m, const Row
 
 // Loss alone: the logits are read once, 2048 x 32000 fp32 in 44 us, 6.0 TB/s.  A
 // workgroup of 1024 threads for each of few long rows: 11 us for one of 128000,
-// 256 threads 15.
+// 256 threads 15; of 64 for each of many short ones: 16384 x 1000 fp32 20 us (256
+// threads 37), 16384 x 4000 bf16 32 (39), but 2000 x 12001 fp32 19.3 (18.8).
 template <typename T, int NT>
 __global__ __launch_bounds__(NT, 8) void distill_loss_kernel(GradArgs a) {
     extern __shared__ float lds[];                   // ids, p, log p, logits of the ids
@@ -293,13 +301,13 @@ __global__ __launch_bounds__(NT, NV == 4 ? 6 : 4) void distill_step_kernel(GradA
     if (d.zero) return;
     __syncthreads();                                 // the given entries after the dense ones
     for (int j = t; j < a.k; j += NT)
-        if (id[j] >= 0) put_given<T, false>(dx, d, given[j], id[j], id, p, a.k);
+        if (id[j] >= 0) put_given<T, false>(dx, d, given[j], j, id, p, a.k);
 }
 
 // Gradient from kept statistics: of the distillation's loss (DIST: weight is the
 // loss's gradient) or of log probabilities and entropy.  A workgroup takes a
 // part of a row of up to NV pieces per thread, all loaded before it looks at the
-// given entries.
+// given entries.  2000 x 50001 fp32: 143 us, 5.6 TB/s.
 template <typename T, int NT, int NV, bool DIST, bool SAME, bool ONCE>
 __global__ __launch_bounds__(NT) void logits_grad_kernel(GradArgs a) {
     using L = LogitType<T>;
@@ -383,7 +391,7 @@ __global__ __launch_bounds__(NT) void logits_grad_kernel(GradArgs a) {
         if (d.zero) return;
         __syncthreads();                             // the given entries after the dense ones
         for (int j = t; j < a.k; j += NT)
-            if (id[j] >= c0 && id[j] < c0 + n) put_given<T, kEnt>(dx, d, given[j], id[j], id, g, a.k);
+            if (id[j] >= c0 && id[j] < c0 + n) put_given<T, kEnt>(dx, d, given[j], j, id, g, a.k);
     };
     if (!DIST && e != 0.f) put(std::true_type{});
     else put(std::false_type{});
@@ -396,6 +404,11 @@ bool same_alignment(const void *x, int64_t ld, const void *dx, int64_t ldd, int6
 }
 
 bool once(const GradArgs &a, int64_t M, int size) { return M * a.V * size > (int64_t(256) << 20); }
+
+template <typename T, int NT>
+void loss_kernel(const GradArgs &a, int64_t M, hipStream_t s) {
+    distill_loss_kernel<T, NT><<<uint32_t(M), NT, size_t(4) * size_t(a.k) * 4, s>>>(a);
+}
 
 template <typename T, int NT, int NV, bool FAR = false>
 void step_kernel(const GradArgs &a, int64_t M, hipStream_t s) {
@@ -540,15 +553,17 @@ extern "C" ht_status ht_distill_loss(const void *logits, int64_t ld, int32_t typ
     a.teacher = teacher;
     a.loss = loss;
     a.stats = stats;
-    const size_t lds = size_t(4) * size_t(k) * 4;
     const hipStream_t s = hipStream_t(stream);
-    if (M <= 256 && V > 16384) {                     // a long row by a whole compute unit where there are few
-        if (type == HT_BF16) distill_loss_kernel<uint16_t, 1024><<<uint32_t(M), 1024, lds, s>>>(a);
-        else distill_loss_kernel<float, 1024><<<uint32_t(M), 1024, lds, s>>>(a);
-    } else if (type == HT_BF16) {
-        distill_loss_kernel<uint16_t, 256><<<uint32_t(M), 256, lds, s>>>(a);
+    // a long row by a whole compute unit where there are few, a short one by a
+    // wavefront where there are many
+    if (type == HT_BF16) {
+        if (M <= 256 && V > 16384) loss_kernel<uint16_t, 1024>(a, M, s);
+        else if (M > 1024 && V <= 8192) loss_kernel<uint16_t, 64>(a, M, s);
+        else loss_kernel<uint16_t, 256>(a, M, s);
     } else {
-        distill_loss_kernel<float, 256><<<uint32_t(M), 256, lds, s>>>(a);
+        if (M <= 256 && V > 16384) loss_kernel<float, 1024>(a, M, s);
+        else if (M > 1024 && V <= 8192) loss_kernel<float, 64>(a, M, s);
+        else loss_kernel<float, 256>(a, M, s);
     }
     HT_LAUNCH_CHECK();
     return HT_OK;

@@ -277,7 +277,7 @@ __device__ __forceinline__ uint64_t join_lists(uint64_t down, uint64_t up, int l
 // bf16, k = 20, 1.5 ms.
 template <typename T, int NW>
 struct TopShared {
-    static constexpr int kMost = NW > 4 ? 128 : 160, kCands = 256;
+    static constexpr int kMost = NW > 4 ? 128 : 160, kCands = NW == 1 ? 64 : 256;
     struct Aside {
         u32x4 piece[2][kMost];
         int32_t first[kMost];    // the first one's number in the row; the second's is `apart` further
@@ -292,7 +292,7 @@ struct TopShared {
 
     __device__ __forceinline__ void init() {
         if (threadIdx.x < NW) bounds[threadIdx.x] = -__builtin_inff();
-        if (threadIdx.x < kCands) rank[threadIdx.x] = 0;
+        for (int i = threadIdx.x; i < kCands; i += 64 * NW) rank[i] = 0;
         if (threadIdx.x == 0) count = 0;
     }
 };

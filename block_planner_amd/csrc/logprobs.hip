@@ -186,12 +186,16 @@ void launch_rows(const LogprobArgs &a, uint32_t grid, bool top, hipStream_t s) {
 // 512 threads where workgroups are few, or the list is long: without the host's
 // part of a call, with 20 alternatives, 10.2 us for 64 x 32000 fp32 (256 threads
 // 12.3, 1024 12.0), 11.3 for 256 x 32000 (13.3, 14.2); with 64, 18.8 for 512 x 32000
-// (256 threads 20.7), but 58 against 55 for 2048 x 32000.
+// (256 threads 20.7), but 58 against 55 for 2048 x 32000.  A wavefront of its own for
+// each of many short rows, which shares the list's work with no other: with 20, bf16, 44
+// us for 16384 x 4000 (256 threads 84), 60 for 4096 x 32000 (65), fp32 47.5 for
+// 2048 x 32000 (50), but 189 against 186 for 4096 x 128000 bf16.
 template <typename T>
 ht_status launch_logprobs(LogprobArgs &a, int64_t M, hipStream_t s) {
     const bool top = a.k > 0;
     const uint32_t grid = uint32_t(M * a.S);
     if (grid <= 256 || (a.k > 32 && grid <= 1024)) launch_rows<T, 512>(a, grid, top, s);
+    else if (grid > 1024 && a.k <= 32 && a.V <= 32768) launch_rows<T, 64>(a, grid, top, s);
     else launch_rows<T, 256>(a, grid, top, s);
     if (a.S > 1) {
         HT_LAUNCH_CHECK();

@@ -10,6 +10,9 @@
 // registers (8 consecutive values per thread and group), so its sum of squares
 // costs no second read: by one wavefront up to 2048 columns (four rows per
 // workgroup, no barrier), by 256 threads up to 8192, by 1024 above.
+//   8192 x 4096 fp32 + fp32 -> bf16: 85 us, 5.5 TB/s;  one row: 2.5 us;
+//   3001 x 2048 fp32 + bf16 -> 8 bits: 13.8 us (256 threads a row: the same);
+//   backward, 8192 x 2048 fp32: 50 us, 5.4 TB/s, and 4.6 us for dw's parts.
 #include <type_traits>
 
 #include "rows.h"
@@ -362,7 +365,7 @@ __global__ __launch_bounds__(1024) void norm_dw_kernel(const float *part, int n,
 }
 
 // 8-bit rows as the values they stand for: a wavefront turns one 1 KiB record
-// (16 rows x 64 columns) round, each lane 16 codes of one row.
+// (16 rows x 64 columns) round, each lane 16 codes of one row.  3001 x 2048: 5 us.
 template <typename Y>
 __global__ __launch_bounds__(256) void q8_values_kernel(const uint8_t *codes, const float *scales, int64_t M, int64_t Mp,
                                                         uint32_t KB, int64_t records, Y *y, int64_t ldy) {

@@ -113,7 +113,7 @@ def test_parts_of_rows(M, V):
     check(r.top_logprobs[:few], top, b3, "top")
 
 
-@pytest.mark.parametrize("M,k", [(256, 20), (257, 20), (600, 64), (1025, 64)])
+@pytest.mark.parametrize("M,k", [(256, 20), (257, 20), (600, 64), (1025, 64), (1025, 32), (1100, 3)])
 @pytest.mark.parametrize("t", ["fp32", "bf16"])
 @pytest.mark.parametrize("kind", ["normal", "ties", "zeros", "up", "masked"])
 def test_many_rows(M, k, t, kind):
