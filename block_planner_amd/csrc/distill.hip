@@ -93,10 +93,12 @@ __device__ __forceinline__ void put_given(T *dx, const Dense &d, float x, int j,
     const int32_t v = id[j];
     float sum = 0.f;
     bool first = true;
+#pragma unroll 8
     for (int i = 0; i < k; ++i) {
-        const bool same = id[i] == v;
-        sum += same ? g[i] : 0.f;
-        first = first && !(same && i < j);
+        const int32_t w = id[i];
+        const float gi = g[i];                       // read in any case: 64 entries 2.3 us less than under the condition
+        sum += w == v ? gi : 0.f;
+        first = first && (w != v || i >= j);
     }
     if (first) LogitType<T>::put(dx + v, __builtin_fmaf(d.scale, sum, dense_of<ENT>(d, x)));
 }
@@ -419,10 +421,17 @@ void step_kernel(const GradArgs &a, int64_t M, hipStream_t s) {
     else distill_step_kernel<T, NT, NV, true, false, FAR><<<grid, NT, lds, s>>>(a);
 }
 
+// Short rows by a wavefront where there are many: with 8 entries, 16384 x 1000 fp32 28
+// us (256 threads 39), bf16 28 (44), 16384 x 4000 bf16 52 (79), but in 16 pieces per
+// thread 108 against 103 for 16384 x 4000 fp32, and 5.4 against 4.9 for 33 x 1003 bf16.
 template <typename T>
 ht_status launch_step(const GradArgs &a, int64_t M, hipStream_t s) {
     const int64_t pieces = a.V / LogitType<T>::kVec;   // at most: the head takes some
-    if (pieces <= 256) step_kernel<T, 256, 1>(a, M, s);
+    const bool many = M > 1024;
+    if (pieces <= 64) step_kernel<T, 64, 1>(a, M, s);
+    else if (many && pieces <= 256) step_kernel<T, 64, 4>(a, M, s);
+    else if (many && pieces <= 512) step_kernel<T, 64, 8>(a, M, s);
+    else if (pieces <= 256) step_kernel<T, 256, 1>(a, M, s);
     else if (pieces <= 1024) step_kernel<T, 256, 4>(a, M, s);
     else if (pieces <= 4096) step_kernel<T, 1024, 4>(a, M, s);
     else if (pieces <= 8192) step_kernel<T, 1024, 8>(a, M, s);

@@ -35,7 +35,7 @@ CASES = [  # M, V, k, T
     (1, 1, 1, 1.0), (2, 3, 2, 2.0), (6, 7, 3, 1.0), (5, 64, 8, 1.0), (33, 1003, 8, 1.0), (7, 1024, 64, 4.0), (6, 4096, 65, 1.0),
     (5, 4100, 5, 0.5), (300, 515, 20, 1.0), (5, 16385, 20, 2.0), (2, 32000, 1024, 1.0), (2, 32771, 31, 1.0),
     (5, 65536, 20, 1.0), (3, 70001, 20, 1.0), (2, 131072, 20, 1.0), (2, 140003, 20, 1.0), (1030, 77, 5, 1.0),
-    (1030, 1003, 70, 2.0)]
+    (1030, 1003, 70, 2.0), (1027, 1900, 9, 1.0)]
 
 
 @pytest.mark.parametrize("M,V,k,T", CASES)
