@@ -208,12 +208,26 @@ def _ptr(t) -> int | None:
     return t.data_ptr()
 
 
+_current = None
+
+
+def _current_stream():
+    """The function that gives the current stream's handle, found once."""
+    import torch
+    # without building the stream's Python object (2 us a call), where torch has that private lookup
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    if raw is None:
+        return lambda: torch.cuda.current_stream().cuda_stream
+    device = torch.cuda.current_device
+    return lambda: raw(device())
+
+
 def _stream(stream) -> int | None:
     if stream is None:
-        import torch
-        # the handle without building the stream's Python object (2 us a call), where torch has that private lookup
-        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-        return torch.cuda.current_stream().cuda_stream if raw is None else raw(torch.cuda.current_device())
+        global _current
+        if _current is None:
+            _current = _current_stream()
+        return _current()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -389,14 +403,19 @@ def ht_mlp_forward(descs, x, y, act_dump=None, path: int = HT_PATH_AUTO, ws=None
 # -----------------------------------------------------------------------------
 # Attention beside the linears
 # -----------------------------------------------------------------------------
+_ACTS: dict = {}
+
+
 def _act(t) -> int:
     """HT_FP32 or HT_BF16 of a tensor."""
-    import torch
-    if t.dtype is torch.bfloat16:
-        return HT_BF16
-    if t.dtype is not torch.float32:
-        raise ValueError(f"expected fp32 or bf16, got {t.dtype}")
-    return HT_FP32
+    code = _ACTS.get(t.dtype)
+    if code is None:
+        import torch
+        _ACTS.update({torch.float32: HT_FP32, torch.bfloat16: HT_BF16})
+        code = _ACTS.get(t.dtype)
+        if code is None:
+            raise ValueError(f"expected fp32 or bf16, got {t.dtype}")
+    return code
 
 
 def _ld(t) -> int:
