@@ -10,9 +10,11 @@
 // registers (8 consecutive values per thread and group), so its sum of squares
 // costs no second read: by one wavefront up to 2048 columns (four rows per
 // workgroup, no barrier), by 256 threads up to 8192, by 1024 above.
-//   8192 x 4096 fp32 + fp32 -> bf16: 85 us, 5.5 TB/s;  one row: 2.5 us;
-//   3001 x 2048 fp32 + bf16 -> 8 bits: 13.8 us (256 threads a row: the same);
-//   backward, 8192 x 2048 fp32: 50 us, 5.4 TB/s, and 4.6 us for dw's parts.
+//   8192 x 4096 fp32 + fp32 -> bf16: 73 us, 6.5 TB/s;  one row: 2.5 us;
+//   3001 x 2048 fp32 + bf16 -> 8 bits: 14.0 us (256 threads a row: the same);
+//   backward, 8192 x 2048 fp32: 49 us, 4.6 of them for dw's parts.
+// Loads and stores are the buffer's, which need no branch at a row's end: all of a
+// row's are in flight at once (16384 x 4096 bf16 backward: 130 -> 111 us).
 #include <type_traits>
 
 #include "rows.h"
@@ -79,7 +81,7 @@ __device__ __forceinline__ uint64_t block_top(uint64_t v) {
 // The row's 8 values h r w of one lane as codes; the 64-wide block's 8 lanes share
 // the scale.  The codes are those of 64 bits (r is in 64 bits; in 32 the norm's
 // rounding moves about one code in 10^5 across a border, by a whole step), worked
-// out in 32 where that is certain (3001 x 2048 of fp32 + bf16: 13.8 us; all in 64
+// out in 32 where that is certain (3001 x 2048 of fp32 + bf16: 14.0 us; all in 64
 // bits 16.8; 32 alone 12.4).  A scaled value, of at most 128, is off by 4 steps of
 // 2^-24, under 2^-14, so those within 2^-13 of a half are worked out again, and so are
 // blocks whose largest value is within 16 steps of a power of two or far from 1, or
@@ -145,9 +147,33 @@ __device__ __forceinline__ void encode8(const Row8 &h, const Row8 &w, double r, 
     if (e == 0) a.scales[int64_t(kb) * a.Mp + m] = bad ? __builtin_nanf("") : ldexpf(1.0f, E - 7);
 }
 
-template <int TPR, int NV, typename X, typename R, bool RES, bool Q8>
+// The columns of a thread's group g of 8 in a row of TPR threads: 8 consecutive
+// ones, or (QUAD, where an operand is fp32) 4 and 4 half the row's group further, so
+// that a wavefront's 16-byte loads lie side by side: 8192 x 4096 fp32 -> bf16 88 ->
+// 83 us.  ONCE: where the matrices are more than the 256 MB Infinity Cache they are
+// not read with a view to the caches: 83 -> 73 (6.5 TB/s), 16384 x 4096 bf16 95 -> 83, but
+// 49 -> 52 for a backward pass of 268 MB (stores with the same hint: slower).
+template <int TPR, bool QUAD, bool ONCE>
+struct Cols {
+    static __device__ __forceinline__ int lo(int t, int g) { return QUAD ? 8 * TPR * g + 4 * t : 8 * (t + TPR * g); }
+    static __device__ __forceinline__ int hi(int t, int g) { return lo(t, g) + (QUAD ? 4 * TPR : 4); }
+
+    template <typename T>
+    static __device__ __forceinline__ Row8 load(const RowBuf<T> &p, int t, int g) {
+        return p.template load<!QUAD, ONCE>(lo(t, g), hi(t, g));
+    }
+    template <typename T>
+    static __device__ __forceinline__ void store(const RowBuf<T> &p, const Row8 &r, int t, int g) {
+        p.template store<!QUAD>(lo(t, g), hi(t, g), r);
+    }
+};
+
+template <int TPR, int NV, typename X, typename R, bool RES, bool Q8, bool ONCE>
 __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void norm_kernel(NormArgs a) {
     using F = std::conditional_t<Q8, double, float>;
+    constexpr bool kQuad = !Q8 && (sizeof(X) == 4 || (RES && sizeof(R) == 4));
+    using In = Cols<TPR, kQuad, ONCE>;
+    using Kept = Cols<TPR, kQuad, false>;
     constexpr int kRows = TPR >= 256 ? 1 : 256 / TPR;
     __shared__ F part[16];
     const int t = threadIdx.x & (TPR - 1);
@@ -155,36 +181,31 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void norm_kernel(NormArgs a)
     // 8-bit rows: the 16 rows of a group share cache lines, so neighbouring
     // workgroups are placed on one XCD (workgroups go to the 8 XCDs in turn)
     if (Q8 && (gridDim.x & 7u) == 0) b = (b & 7u) * (gridDim.x >> 3) + (b >> 3);
-    const int64_t m = int64_t(b) * kRows + (threadIdx.x / TPR);
+    const int64_t m = int64_t(b) * kRows + __builtin_amdgcn_readfirstlane(threadIdx.x / TPR);
     if (m >= a.M) return;    // whole wavefronts (TPR = 64), never part of a workgroup that meets at a barrier
-    const X *x = static_cast<const X *>(a.x) + m * a.ldx;
+    const RowBuf<X> x(static_cast<const X *>(a.x) + m * a.ldx, a.K);
+    const RowBuf<R> res(static_cast<const R *>(a.res) + m * a.ldr, a.K);
+    const RowBuf<float> wb(a.w, a.K);
     Row8 v[NV];
     F ss = 0;
 #pragma unroll
     for (int g = 0; g < NV; ++g) {
-        const int c = 8 * (t + TPR * g);
-        if (c < a.K) {
-            v[g] = load8(x + c);
-            if constexpr (RES) {
-                const Row8 r = load8(static_cast<const R *>(a.res) + m * a.ldr + c);
+        v[g] = In::load(x, t, g);
+        if constexpr (RES) {
+            const Row8 r = In::load(res, t, g);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) v[g].v[j] += r.v[j];
-            }
-        } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[g].v[j] = 0.f;
+            for (int j = 0; j < 8; ++j) v[g].v[j] += r.v[j];
         }
     }
     if constexpr (RES) {
         // the norm sees h as it is stored: the backward pass, which has h, differentiates what was computed
 #pragma unroll
         for (int g = 0; g < NV; ++g) {
-            const int c = 8 * (t + TPR * g);
             if constexpr (sizeof(R) == 2) {
 #pragma unroll
                 for (int j = 0; j < 8; ++j) v[g].v[j] = __uint_as_float(uint32_t(round_bf16(v[g].v[j])) << 16);
             }
-            if (a.h && c < a.K) store8(static_cast<R *>(a.h) + m * a.ldh + c, v[g]);
+            if (a.h) Kept::store(RowBuf<R>(static_cast<R *>(a.h) + m * a.ldh, a.K), v[g], t, g);
         }
     }
 #pragma unroll
@@ -192,36 +213,32 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void norm_kernel(NormArgs a)
 #pragma unroll
         for (int j = 0; j < 8; ++j) ss += F(v[g].v[j]) * F(v[g].v[j]);
     ss = row_total<TPR>(ss, part);
+    const auto put = [&](int g, const Row8 &o) {
+        if (a.y_bf16) Kept::store(RowBuf<uint16_t>(static_cast<uint16_t *>(a.y) + m * a.ldy, a.K), o, t, g);
+        else Kept::store(RowBuf<float>(static_cast<float *>(a.y) + m * a.ldy, a.K), o, t, g);
+    };
     if constexpr (Q8) {
         const double rn = 1.0 / sqrt(ss / a.K + double(a.eps));
 #pragma unroll
         for (int g = 0; g < NV; ++g) {
-            const int c = 8 * (t + TPR * g);
-            const bool live = c < a.K;
-            Row8 w{};
-            if (live) {
-                w = load8(a.w + c);
-                if (a.y) {
-                    Row8 o;
+            const int c = Kept::lo(t, g);
+            const Row8 w = Kept::load(wb, t, g);
+            if (a.y) {
+                Row8 o;
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) o.v[j] = v[g].v[j] * float(rn) * w.v[j];
-                    if (a.y_bf16) store8(static_cast<uint16_t *>(a.y) + m * a.ldy + c, o);
-                    else store8(static_cast<float *>(a.y) + m * a.ldy + c, o);
-                }
+                for (int j = 0; j < 8; ++j) o.v[j] = v[g].v[j] * float(rn) * w.v[j];
+                put(g, o);
             }
-            encode8(v[g], w, rn, a, m, c, live);
+            encode8(v[g], w, rn, a, m, c, c < a.K);
         }
     } else {
         const float rn = 1.0f / sqrtf(ss * a.inv_k + a.eps);
 #pragma unroll
         for (int g = 0; g < NV; ++g) {
-            const int c = 8 * (t + TPR * g);
-            if (c >= a.K) continue;
-            const Row8 w = load8(a.w + c);
+            const Row8 w = Kept::load(wb, t, g);
 #pragma unroll
             for (int j = 0; j < 8; ++j) v[g].v[j] = v[g].v[j] * rn * w.v[j];
-            if (a.y_bf16) store8(static_cast<uint16_t *>(a.y) + m * a.ldy + c, v[g]);
-            else store8(static_cast<float *>(a.y) + m * a.ldy + c, v[g]);
+            put(g, v[g]);
         }
     }
 }
@@ -239,39 +256,35 @@ struct NormBwdArgs {
 
 // A workgroup takes every gridDim.x-th set of rows and keeps its part of dw in
 // registers; the parts are added by norm_dw_kernel in a fixed order.
-template <int TPR, int NV, typename Y, typename H>
+template <int TPR, int NV, typename Y, typename H, bool ONCE>
 __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void norm_bwd_kernel(NormBwdArgs a) {
+    constexpr bool kQuad = sizeof(Y) == 4 || sizeof(H) == 4;
+    using In = Cols<TPR, kQuad, ONCE>;
+    using Kept = Cols<TPR, kQuad, false>;
     constexpr int kRows = TPR >= 256 ? 1 : 256 / TPR;
     __shared__ float part[2][32];
     extern __shared__ __align__(16) float acc[];     // TPR = 64: [4][K]
     const int t = threadIdx.x & (TPR - 1);
-    const int sub = threadIdx.x / TPR;
+    const int sub = __builtin_amdgcn_readfirstlane(threadIdx.x / TPR);
+    const RowBuf<float> wb(a.w, a.K);
     Row8 w[NV], dw[NV];
 #pragma unroll
     for (int g = 0; g < NV; ++g) {
-        const int c = 8 * (t + TPR * g);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) w[g].v[j] = dw[g].v[j] = 0.f;
-        if (c < a.K) w[g] = load8(a.w + c);
+        w[g] = Kept::load(wb, t, g);
+        dw[g] = Row8{};
     }
     int at = 0;
     for (int64_t m0 = int64_t(blockIdx.x) * kRows; m0 < a.M; m0 += int64_t(gridDim.x) * kRows) {
         const int64_t m = m0 + sub;
         if (kRows > 1 && m >= a.M) break;            // a wavefront of its own: no barrier inside the loop
-        const H *hp = static_cast<const H *>(a.h) + m * a.ldh;
-        const Y *yp = static_cast<const Y *>(a.dy) + m * a.lddy;
+        const RowBuf<H> hp(static_cast<const H *>(a.h) + m * a.ldh, a.K);
+        const RowBuf<Y> yp(static_cast<const Y *>(a.dy) + m * a.lddy, a.K);
         Row8 h[NV], dy[NV];
         float ss = 0.f, dot = 0.f;
 #pragma unroll
         for (int g = 0; g < NV; ++g) {
-            const int c = 8 * (t + TPR * g);
-            if (c < a.K) {
-                h[g] = load8(hp + c);
-                dy[g] = load8(yp + c);
-            } else {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) h[g].v[j] = dy[g].v[j] = 0.f;
-            }
+            h[g] = In::load(hp, t, g);
+            dy[g] = In::load(yp, t, g);
         }
 #pragma unroll
         for (int g = 0; g < NV; ++g)
@@ -301,8 +314,6 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void norm_bwd_kernel(NormBwd
         const float k = dot * a.inv_k * rn * rn;     // d = dh + r (g - h k)
 #pragma unroll
         for (int g = 0; g < NV; ++g) {
-            const int c = 8 * (t + TPR * g);
-            if (c >= a.K) continue;
             Row8 d;
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
@@ -310,14 +321,14 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void norm_bwd_kernel(NormBwd
                 d.v[j] = rn * (dy[g].v[j] * w[g].v[j] - h[g].v[j] * k);
             }
             if (a.dh) {
-                const Row8 e = load8(static_cast<const H *>(a.dh) + m * a.lddh + c);
+                const Row8 e = In::load(RowBuf<H>(static_cast<const H *>(a.dh) + m * a.lddh, a.K), t, g);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) d.v[j] += e.v[j];
             }
-            store8(static_cast<H *>(a.dres) + m * a.lddres + c, d);
+            Kept::store(RowBuf<H>(static_cast<H *>(a.dres) + m * a.lddres, a.K), d, t, g);
             if (a.dx) {
-                if constexpr (sizeof(H) == 4) store8(static_cast<uint16_t *>(a.dx) + m * a.lddx + c, d);
-                else store8(static_cast<float *>(a.dx) + m * a.lddx + c, d);
+                if constexpr (sizeof(H) == 4) Kept::store(RowBuf<uint16_t>(static_cast<uint16_t *>(a.dx) + m * a.lddx, a.K), d, t, g);
+                else Kept::store(RowBuf<float>(static_cast<float *>(a.dx) + m * a.lddx, a.K), d, t, g);
             }
         }
     }
@@ -325,8 +336,11 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void norm_bwd_kernel(NormBwd
     if constexpr (kRows > 1) {
 #pragma unroll
         for (int g = 0; g < NV; ++g) {
-            const int c = 8 * (t + TPR * g);
-            if (c < a.K) store8(acc + sub * a.K + c, dw[g]);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int c = (j < 4 ? Kept::lo(t, g) : Kept::hi(t, g) - 4) + j;
+                if (c < a.K) acc[sub * a.K + c] = dw[g].v[j];
+            }
         }
         __syncthreads();
         for (int c = threadIdx.x; c < a.K; c += 256) {
@@ -337,10 +351,7 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void norm_bwd_kernel(NormBwd
         }
     } else {
 #pragma unroll
-        for (int g = 0; g < NV; ++g) {
-            const int c = 8 * (t + TPR * g);
-            if (c < a.K) store8(out + c, dw[g]);
-        }
+        for (int g = 0; g < NV; ++g) Kept::store(RowBuf<float>(out, a.K), dw[g], t, g);
     }
 }
 
@@ -389,38 +400,45 @@ __global__ __launch_bounds__(256) void q8_values_kernel(const uint8_t *codes, co
     store8(p + 8, b);
 }
 
-template <int TPR, int NV, bool Q8>
+template <int TPR, int NV, bool Q8, bool ONCE>
 void launch_norm_as(const NormArgs &a, int32_t xt, int32_t rt, hipStream_t s) {
     constexpr int kThreads = TPR > 256 ? TPR : 256, kRows = TPR >= 256 ? 1 : 256 / TPR;
     const uint32_t grid = uint32_t((a.M + kRows - 1) / kRows);
     const bool xb = xt == HT_BF16, rb = rt == HT_BF16;
     if (!a.res) {
-        if (xb) norm_kernel<TPR, NV, uint16_t, float, false, Q8><<<grid, kThreads, 0, s>>>(a);
-        else norm_kernel<TPR, NV, float, float, false, Q8><<<grid, kThreads, 0, s>>>(a);
+        if (xb) norm_kernel<TPR, NV, uint16_t, float, false, Q8, ONCE><<<grid, kThreads, 0, s>>>(a);
+        else norm_kernel<TPR, NV, float, float, false, Q8, ONCE><<<grid, kThreads, 0, s>>>(a);
     } else if (xb) {
-        if (rb) norm_kernel<TPR, NV, uint16_t, uint16_t, true, Q8><<<grid, kThreads, 0, s>>>(a);
-        else norm_kernel<TPR, NV, uint16_t, float, true, Q8><<<grid, kThreads, 0, s>>>(a);
+        if (rb) norm_kernel<TPR, NV, uint16_t, uint16_t, true, Q8, ONCE><<<grid, kThreads, 0, s>>>(a);
+        else norm_kernel<TPR, NV, uint16_t, float, true, Q8, ONCE><<<grid, kThreads, 0, s>>>(a);
     } else {
-        if (rb) norm_kernel<TPR, NV, float, uint16_t, true, Q8><<<grid, kThreads, 0, s>>>(a);
-        else norm_kernel<TPR, NV, float, float, true, Q8><<<grid, kThreads, 0, s>>>(a);
+        if (rb) norm_kernel<TPR, NV, float, uint16_t, true, Q8, ONCE><<<grid, kThreads, 0, s>>>(a);
+        else norm_kernel<TPR, NV, float, float, true, Q8, ONCE><<<grid, kThreads, 0, s>>>(a);
     }
 }
 
 template <int TPR, int NV>
-void launch_norm(const NormArgs &a, int32_t xt, int32_t rt, hipStream_t s) {
-    if (a.codes) launch_norm_as<TPR, NV, true>(a, xt, rt, s);
-    else launch_norm_as<TPR, NV, false>(a, xt, rt, s);
+void launch_norm(const NormArgs &a, bool once, int32_t xt, int32_t rt, hipStream_t s) {
+    if (a.codes) launch_norm_as<TPR, NV, true, false>(a, xt, rt, s);
+    else if (once) launch_norm_as<TPR, NV, false, true>(a, xt, rt, s);
+    else launch_norm_as<TPR, NV, false, false>(a, xt, rt, s);
 }
 
-template <int TPR, int NV>
-void launch_norm_bwd(const NormBwdArgs &a, uint32_t grid, int32_t yt, int32_t ht, hipStream_t s) {
+template <int TPR, int NV, bool ONCE>
+void launch_norm_bwd_as(const NormBwdArgs &a, uint32_t grid, int32_t yt, int32_t ht, hipStream_t s) {
     constexpr int kThreads = TPR > 256 ? TPR : 256, kRows = TPR >= 256 ? 1 : 256 / TPR;
     const size_t lds = kRows > 1 ? size_t(kRows) * size_t(a.K) * 4 : 0;
     const bool yb = yt == HT_BF16, hb = ht == HT_BF16;
-    if (yb && hb) norm_bwd_kernel<TPR, NV, uint16_t, uint16_t><<<grid, kThreads, lds, s>>>(a);
-    else if (yb) norm_bwd_kernel<TPR, NV, uint16_t, float><<<grid, kThreads, lds, s>>>(a);
-    else if (hb) norm_bwd_kernel<TPR, NV, float, uint16_t><<<grid, kThreads, lds, s>>>(a);
-    else norm_bwd_kernel<TPR, NV, float, float><<<grid, kThreads, lds, s>>>(a);
+    if (yb && hb) norm_bwd_kernel<TPR, NV, uint16_t, uint16_t, ONCE><<<grid, kThreads, lds, s>>>(a);
+    else if (yb) norm_bwd_kernel<TPR, NV, uint16_t, float, ONCE><<<grid, kThreads, lds, s>>>(a);
+    else if (hb) norm_bwd_kernel<TPR, NV, float, uint16_t, ONCE><<<grid, kThreads, lds, s>>>(a);
+    else norm_bwd_kernel<TPR, NV, float, float, ONCE><<<grid, kThreads, lds, s>>>(a);
+}
+
+template <int TPR, int NV>
+void launch_norm_bwd(const NormBwdArgs &a, bool once, uint32_t grid, int32_t yt, int32_t ht, hipStream_t s) {
+    if (once) launch_norm_bwd_as<TPR, NV, true>(a, grid, yt, ht, s);
+    else launch_norm_bwd_as<TPR, NV, false>(a, grid, yt, ht, s);
 }
 
 // The instance for K columns: threads per row and groups of 8 per thread.
@@ -435,9 +453,13 @@ void launch_norm_bwd(const NormBwdArgs &a, uint32_t grid, int32_t yt, int32_t ht
         else CALL(1024, 4);               \
     } while (0)
 
-// Workgroups of the backward pass.
-uint32_t norm_bwd_grid(int64_t M, int64_t K) {
-    const int64_t rows = K <= 2048 ? 4 : 1, most = K <= 8192 ? 512 : 256;
+// A call's matrices, `bytes` per entry together, are more than the Infinity Cache holds.
+bool past_caches(int64_t M, int64_t K, int bytes) { return M * K * bytes > (int64_t(256) << 20); }
+
+// Workgroups of the backward pass.  768 where h is bfloat16 and a row takes 256 threads
+// of two groups: 16384 x 4096 bf16 95 us (512: 111, 1024: 99); fp32, 8192 x 4096: 94 (512: 90).
+uint32_t norm_bwd_grid(int64_t M, int64_t K, bool bf16) {
+    const int64_t rows = K <= 2048 ? 4 : 1, most = K > 8192 ? 256 : bf16 && K > 2048 && K <= 4096 ? 768 : 512;
     const int64_t sets = (M + rows - 1) / rows;
     return uint32_t(sets < most ? sets : most);
 }
@@ -522,7 +544,8 @@ extern "C" ht_status ht_add_rms_norm(const void *x, int64_t ldx, int32_t xt, con
     a.eps = eps;
     a.inv_k = 1.0f / float(K);
     const hipStream_t s = hipStream_t(stream);
-#define HT_NORM_CALL(T, V) launch_norm<T, V>(a, xt, rt, s)
+    const bool once = past_caches(M, K, act_size(xt) + (res ? act_size(rt) : 0) + (h ? act_size(rt) : 0) + (y ? act_size(yt) : 1));
+#define HT_NORM_CALL(T, V) launch_norm<T, V>(a, once, xt, rt, s)
     HT_NORM_SHAPES(K, HT_NORM_CALL);
 #undef HT_NORM_CALL
     HT_LAUNCH_CHECK();
@@ -532,7 +555,7 @@ extern "C" ht_status ht_add_rms_norm(const void *x, int64_t ldx, int32_t xt, con
 extern "C" ht_status ht_add_rms_norm_workspace(int64_t M, int64_t K, size_t *bytes) {
     if (!bytes) return HT_EINVAL;
     HT_TRY(check_norm(M, K));
-    const uint32_t grid = norm_bwd_grid(M, K);
+    const uint32_t grid = norm_bwd_grid(M, K, true);     // the larger of both types'
     *bytes = grid > 1 ? size_t(grid) * size_t(K) * sizeof(float) : 0;
     return HT_OK;
 }
@@ -555,7 +578,7 @@ extern "C" ht_status ht_add_rms_norm_backward(const void *dy, int64_t lddy, int3
         size_t need = 0;
         HT_TRY(ht_add_rms_norm_workspace(M, K, &need));
         if (need && (!ws || ws_bytes < need)) return HT_ESMALL;
-        const uint32_t grid = norm_bwd_grid(M, K);
+        const uint32_t grid = norm_bwd_grid(M, K, ht == HT_BF16);
         NormBwdArgs a{};
         a.dy = dy;
         a.h = h;
@@ -573,7 +596,8 @@ extern "C" ht_status ht_add_rms_norm_backward(const void *dy, int64_t lddy, int3
         a.K = int32_t(K);
         a.eps = eps;
         a.inv_k = 1.0f / float(K);
-#define HT_NORM_CALL(T, V) launch_norm_bwd<T, V>(a, grid, yt, ht, s)
+        const bool once = past_caches(M, K, act_size(yt) + (dh ? 3 : 2) * act_size(ht) + (dx ? 6 - act_size(ht) : 0));
+#define HT_NORM_CALL(T, V) launch_norm_bwd<T, V>(a, once, grid, yt, ht, s)
         HT_NORM_SHAPES(K, HT_NORM_CALL);
 #undef HT_NORM_CALL
         HT_LAUNCH_CHECK();
