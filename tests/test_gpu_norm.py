@@ -256,6 +256,33 @@ def test_backward_without_rows_and_in_place():
         assert torch.equal(over, want[1]) and torch.equal(got[2], want[2])
 
 
+@pytest.mark.parametrize("M,K,t,y", [(8300, 4104, "fp32", "bf16"), (16400, 4096, "bf16", "bf16"), (9001, 2040, "fp32", "fp32"),
+                                     (3000, 16392, "bf16", "fp32")])
+def test_more_than_the_caches_hold(M, K, t, y):
+    """Matrices of more than 256 MiB: every row equals that of a small call, and
+    the weight's gradient the formula's (a workgroup adds at most 33 rows here, in
+    turn, then 12 parts and 6 halvings: backward_tol's 96 u hold 40 a term)."""
+    print(M, K, t, y, flush=True)
+    torch.manual_seed(M)
+    x, r = (torch.randn(M, K, device=dev()).to(TYPES[t]) for _ in range(2))
+    w = torch.rand(K, device=dev()) + 0.5
+    out, h = api.add_rms_norm(x, w, r, out_dtype=TYPES[y])
+    dy = torch.randn(M, K, device=dev()).to(TYPES[y])
+    dx, dres, dw = api.add_rms_norm_backward(dy, h, w, r)
+    for i in (0, M // 2 - 7, M - 40):
+        c = slice(i, i + 40)
+        o, s = api.add_rms_norm(x[c], w, r[c], out_dtype=TYPES[y])
+        assert torch.equal(o, out[c]) and torch.equal(s, h[c])
+        assert torch.equal(api.add_rms_norm_backward(dy[c], h[c], w, r[c])[1], dres[c])
+    want, size = torch.zeros(2, K, device=dev(), dtype=torch.float64)
+    for i in range(0, M, 1000):
+        d = h[i:i + 1000].double()
+        d = dy[i:i + 1000].double() * d / (d.square().mean(1, keepdim=True) + 1e-6).sqrt()
+        want += d.sum(0)
+        size += d.abs().sum(0)
+    assert torch.all((dw.double() - want).abs() <= 96 * U * size)
+
+
 def test_gradient_against_differences():
     """Central differences, step 2^-10, of the forward in 64 bits along random
     directions: off by a third derivative times 2^-20 / 6, under 1e-4 of the
