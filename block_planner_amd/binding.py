@@ -208,26 +208,12 @@ def _ptr(t) -> int | None:
     return t.data_ptr()
 
 
-_current = None
-
-
-def _current_stream():
-    """The function that gives the current stream's handle, found once."""
-    import torch
-    # without building the stream's Python object (2 us a call), where torch has that private lookup
-    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-    if raw is None:
-        return lambda: torch.cuda.current_stream().cuda_stream
-    device = torch.cuda.current_device
-    return lambda: raw(device())
-
-
 def _stream(stream) -> int | None:
     if stream is None:
-        global _current
-        if _current is None:
-            _current = _current_stream()
-        return _current()
+        import torch
+        # the handle without building the stream's Python object (2 us a call), where torch has that private lookup
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        return torch.cuda.current_stream().cuda_stream if raw is None else raw(torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
