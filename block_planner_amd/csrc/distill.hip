@@ -54,7 +54,7 @@ struct GradArgs {
 // gradient dx_v = (f + e log2 q_v) q_v.
 struct Dense {
     float mx, b, c, f, e;
-    float scale;         // of the given entries
+    float scale, own;    // of the given entries: f = own - scale sum g
     bool zero;           // the row's gradient is zero whatever its logits are
 };
 
@@ -88,19 +88,27 @@ __device__ __forceinline__ void put_piece(T *y, u32x4 u) {
 // Entry j's place written whole: the dense part and every g of that place, in
 // order.  The first entry of a place writes it: two threads' equal sums may still be
 // rounded otherwise, by where the compiler fuses a product in each wavefront's code.
+// scale (sum g at the place) - q scale (sum of all g) is taken as
+// scale (sum at the place (1 - q) - q sum of the others): with a nearly certain token
+// both terms are small and keep their digits.
 template <typename T, bool ENT>
 __device__ __forceinline__ void put_given(T *dx, const Dense &d, float x, int j, const int32_t *id, const float *g, int k) {
     const int32_t v = id[j];
-    float sum = 0.f;
+    float sum = 0.f, rest = 0.f;
     bool first = true;
 #pragma unroll 8
     for (int i = 0; i < k; ++i) {
         const int32_t w = id[i];
         const float gi = g[i];                       // read in any case: 64 entries 2.3 us less than under the condition
         sum += w == v ? gi : 0.f;
+        rest += w == v ? 0.f : gi;
         first = first && (w != v || i >= j);
     }
-    if (first) LogitType<T>::put(dx + v, __builtin_fmaf(d.scale, sum, dense_of<ENT>(d, x)));
+    if (!first) return;
+    const float l = (x - d.mx) * d.c - d.b, q = exp2_fast(l);
+    float y = d.scale * (sum * one_minus(l, q) - q * rest);
+    if constexpr (ENT) y += q * (d.own + d.e * fmaxf(l, kFar));
+    LogitType<T>::put(dx + v, y);
 }
 
 // The teacher's distribution of a row by one wavefront: ids (-1: not kept), p, log2 p
@@ -110,7 +118,8 @@ template <typename T>
 __device__ __forceinline__ bool teacher_wave(const int32_t *ids, const float *t, const T *row, int64_t lo, int64_t hi, int k,
                                              int64_t V, float c, int32_t *id, float *p, float *logs, float *given) {
     const int lane = threadIdx.x & 63;
-    float top = kLowest;
+    float most = -__builtin_inff();
+    int at = -1;                                     // the lane's first of its largest
     for (int j = lane; j < k; j += 64) {
         const int32_t v = ids[j];
         const bool in = v >= 0 && v < V;
@@ -118,24 +127,27 @@ __device__ __forceinline__ bool teacher_wave(const int32_t *ids, const float *t,
         id[j] = in ? v : -1;
         given[j] = v >= lo && v < hi ? LogitType<T>::get(row + v) : 0.f;
         logs[j] = z;
-        top = fmaxf(top, z);
+        at = z > most ? j : at;
+        most = fmaxf(most, z);
     }
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) top = fmaxf(top, __shfl_xor(top, d));
-    float sum = 0.f;
+    const float top = fmaxf(wave_top(most), kLowest);
+    const uint64_t who = __ballot(at >= 0 && most == top);
+    if (who == 0 || lane != __builtin_ctzll(who)) at = -1;
+    float tail = 0.f;                                // as the student's: one entry of the largest left out
     for (int j = lane; j < k; j += 64) {
         const float d = (logs[j] - top) * c, e = exp2_fast(d);
         logs[j] = d;
         p[j] = e;
-        sum += e;
+        tail += j == at ? 0.f : e;
     }
-    sum = wave_sum(sum);
-    const float inv = 1.0f / sum, b = log2f(sum);
+    tail = wave_sum(tail);
+    const bool any = who != 0 || tail != 0.f;        // NaN too
+    const float inv = 1.0f / (1.0f + tail), b = log2_1p(tail);
     for (int j = lane; j < k; j += 64) {
-        p[j] = sum == 0.f ? 0.f : p[j] * inv;
+        p[j] = any ? p[j] * inv : 0.f;
         logs[j] -= b;
     }
-    return sum != 0.f;
+    return any;
 }
 
 // A row's loss, by one wavefront after the statistics and the teacher's.
@@ -250,7 +262,7 @@ __global__ __launch_bounds__(NT, NV == 4 ? 6 : 4) void distill_step_kernel(GradA
                 stat_add<kGroup * kVec, false>(r, x, most, a.c);
             }
         }
-        r = stat_wave(r, a.c);
+        r = stat_wave<T, NT>(r, a.c, in, single ? x1 : -__builtin_inff());
         if (lane == 0) stats[wave] = r;
         __syncthreads();
         const RowOut o = row_out(stat_group<NW>(stats, a.c));
@@ -366,7 +378,8 @@ __global__ __launch_bounds__(NT) void logits_grad_kernel(GradArgs a) {
                 }
             }
             sum = wave_sum(sum);
-            d.f = -a.inv_t * (sum + (e != 0.f ? e * a.entropy[m] : 0.f));
+            d.own = -a.inv_t * (e != 0.f ? e * a.entropy[m] : 0.f);
+            d.f = d.own - a.inv_t * sum;
             d.e = -a.inv_t * e * kLn2;
             d.scale = a.inv_t;
         }

@@ -132,9 +132,9 @@ __global__ __launch_bounds__(256) void logprob_join_kernel(LogprobArgs a) {
     __shared__ RowStat stats[4];
     const int64_t m = blockIdx.x;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    RowStat r = stat_none();
-    for (int i = threadIdx.x; i < a.S; i += 256) r = stat_join(r, a.ws_stats[m * a.S + i], a.c);
-    r = stat_wave(r, a.c);
+    RowStat r{-__builtin_inff(), 0.f, 0.f};
+    if (int(threadIdx.x) < a.S) r = a.ws_stats[m * a.S + threadIdx.x];   // at most 256 parts
+    r = stat_meet<64>(r, a.c);
     if (lane == 0) stats[wave] = r;
     uint64_t list = 0;
     if constexpr (TOP) {
