@@ -489,10 +489,13 @@ struct TopList {
     }
 
     // All that reach the last bound, of the whole workgroup, into sh->cand; between
-    // two barriers.  Their number, sh->count, may be more than it holds.  thr is past
-    // the k-th of a list already, whose own entries go by the workgroup's bound.
+    // two barriers.  Their number, sh->count, may be more than it holds.  thr, past the
+    // k-th of the wavefront's list, is for pieces that are read after those in it: what
+    // is still put aside may hold the k-th's value at a lower index, so it goes by the
+    // larger of that value and the workgroup's bound, either included.
     __device__ __forceinline__ void gather(int32_t apart, int32_t vecs, uint32_t i0) {
         const float least = refresh();
+        const float bound = fmaxf(least, kth ? key_value(uint32_t(kth >> 32)) : kLowest);
         bool old = lane < k && list != 0 && uint32_t(list >> 32) >= order_key(least);
         for (int from = 0; from == 0 || from < pending; from += 64) {
             const int i = from + lane;
@@ -511,7 +514,7 @@ struct TopList {
             }
             uint32_t n = old ? 1 : 0;
 #pragma unroll
-            for (int j = 0; j < 2 * kVec; ++j) n += x[j] >= thr ? 1 : 0;
+            for (int j = 0; j < 2 * kVec; ++j) n += x[j] >= bound ? 1 : 0;
             // places: the lanes' counts bit by bit
             uint32_t at = 0, all = 0;
 #pragma unroll
@@ -530,7 +533,7 @@ struct TopList {
             old = false;
 #pragma unroll
             for (int j = 0; j < 2 * kVec; ++j)
-                if (x[j] >= thr)
+                if (x[j] >= bound)
                     sh->cand[at++] = entry_of(x[j], i0 + uint32_t(first + (j >= kVec ? apart : 0)) * kVec + uint32_t(j & (kVec - 1)));
         }
     }
