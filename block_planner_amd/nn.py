@@ -433,9 +433,11 @@ class AddRMSNorm(torch.nn.Module):
 def _int32(t: torch.Tensor, V: int) -> torch.Tensor:
     """Tokens as the kernels read them; one outside [0, V) stays outside."""
     if t.dtype != torch.int32:
-        if t.is_floating_point() or t.dtype == torch.bool:
+        if t.is_floating_point() or t.is_complex() or t.dtype == torch.bool:
             raise ValueError(f"tokens: expected whole numbers, got {t.dtype}")
-        t = t.clamp(-1, V).to(torch.int32)
+        if t.dtype.itemsize >= 4:            # narrower ones fit, and hold neither -1 nor V of every vocabulary
+            t = t.to(torch.int64).clamp(-1, V)
+        t = t.to(torch.int32)
     return t.contiguous()
 
 
