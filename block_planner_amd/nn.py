@@ -513,7 +513,8 @@ def distill_loss(logits: torch.Tensor, ids: torch.Tensor, teacher: torch.Tensor,
                  temperature: float = 1.0) -> torch.Tensor:
     """Distillation from a teacher's top entries: sum(weight * loss) over the
     rows of the student's logits [..., V] (fp32 or bf16), differentiable in
-    them.  ids [..., k] (whole numbers; outside [0, V): not kept) and teacher fp32
+    them alone: a teacher or weight that requires a gradient is refused.  ids
+    [..., k] (whole numbers; outside [0, V): not kept) and teacher fp32
     [..., k], its logits or log probabilities there (api.token_logprobs'
     top_tokens and top_logprobs); weight [...] fp32, by default 1 / rows (the
     mean); rows of weight 0 are not read.  loss is the divergence of the
@@ -523,6 +524,9 @@ def distill_loss(logits: torch.Tensor, ids: torch.Tensor, teacher: torch.Tensor,
     lead, V = logits.shape[:-1], logits.shape[-1]
     if ids.shape[:-1] != lead or teacher.shape != ids.shape:
         raise ValueError(f"ids, teacher: expected {tuple(lead)} + (k,), got {tuple(ids.shape)} and {tuple(teacher.shape)}")
+    for name, t in (("teacher", teacher), ("weight", weight)):
+        if torch.is_grad_enabled() and t is not None and t.requires_grad:
+            raise RuntimeError(f"distill_loss has no gradient for {name}: detach it, or call it under torch.no_grad()")
     x = logits.reshape(-1, V)
     M, k = x.shape[0], ids.shape[-1]
     ids = _int32(ids.reshape(M, k), V)
@@ -532,9 +536,9 @@ def distill_loss(logits: torch.Tensor, ids: torch.Tensor, teacher: torch.Tensor,
     else:
         if weight.shape != lead:
             raise ValueError(f"weight: expected {tuple(lead)}, got {tuple(weight.shape)}")
-        weight = weight.detach().reshape(M).float().contiguous()
+        weight = weight.reshape(M).float().contiguous()
     if torch.is_grad_enabled() and x.requires_grad:
-        return _DistillFn.apply(x, ids, teacher.detach(), weight, float(temperature))
+        return _DistillFn.apply(x, ids, teacher, weight, float(temperature))
     loss, _ = api.distill_loss(x, ids, teacher, temperature)
     return _total(torch.where(weight != 0, weight * loss, 0.0))
 
