@@ -363,11 +363,18 @@ class HyperAttention(torch.nn.Module):
 # Between two layers, and around the last linear
 # -----------------------------------------------------------------------------
 class _AddRMSNormFn(torch.autograd.Function):
-    """api.add_rms_norm with ht_add_rms_norm_backward."""
+    """api.add_rms_norm with ht_add_rms_norm_backward, over any leading dims.
+    x and residual get one tensor as their gradient where their types agree, the
+    same object, which autograd copies for a leaf that may not keep it: views of
+    it would both be kept, and added to twice by the next backward call."""
 
     @staticmethod
     def forward(ctx, x, weight, residual, eps, out_dtype):
-        y, h = api.add_rms_norm(x, weight, residual, eps, out_dtype)
+        flat = lambda t: None if t is None else t.reshape(-1, x.shape[-1])  # noqa: E731
+        # tensors of their own, not views, which a caller could not change in place
+        y = torch.empty(x.shape, dtype=out_dtype or torch.bfloat16, device=x.device)
+        h = None if residual is None else torch.empty(x.shape, dtype=residual.dtype, device=x.device)
+        api.add_rms_norm(flat(x), weight, flat(residual), eps, out_dtype, out=(flat(y), flat(h)))
         ctx.eps, ctx.x_dtype, ctx.res = eps, x.dtype, residual is not None
         ctx.save_for_backward(x if h is None else h, weight)
         ctx.set_materialize_grads(False)
@@ -379,8 +386,10 @@ class _AddRMSNormFn(torch.autograd.Function):
         h, weight = ctx.saved_tensors
         if dy is None:                       # the norm's output is not used: the sum's gradient alone
             return None if dh is None else dh.to(ctx.x_dtype), None, dh, None, None
-        dx, dres, dw = api.add_rms_norm_backward(dy, h, weight, dh, ctx.eps, ctx.x_dtype)
-        return dx, dw, dres if ctx.res else None, None, None
+        shape, flat = h.shape, lambda t: None if t is None else t.reshape(-1, h.shape[-1])  # noqa: E731
+        dx, dres, dw = api.add_rms_norm_backward(flat(dy), flat(h), weight, flat(dh), ctx.eps, ctx.x_dtype)
+        same, dres = dx is dres, dres.view(shape)
+        return dres if same else dx.view(shape), dw, dres if ctx.res else None, None, None
 
 
 def add_rms_norm(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor | None = None, eps: float = 1e-6,
@@ -388,12 +397,9 @@ def add_rms_norm(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor |
     """Differentiable api.add_rms_norm over any leading dims: (y, h), h = x +
     residual (None without one) and y its norm times weight, bf16 by default.
     Gradients for x, weight and residual."""
-    shape = x.shape
-    if residual is not None and residual.shape != shape:
-        raise ValueError(f"residual: expected {tuple(shape)}, got {tuple(residual.shape)}")
-    y, h = _AddRMSNormFn.apply(x.reshape(-1, shape[-1]), weight,
-                               None if residual is None else residual.reshape(-1, shape[-1]), float(eps), out_dtype)
-    return y.view(shape), None if h is None else h.view(shape)
+    if residual is not None and residual.shape != x.shape:
+        raise ValueError(f"residual: expected {tuple(x.shape)}, got {tuple(residual.shape)}")
+    return _AddRMSNormFn.apply(x, weight, residual, float(eps), out_dtype)
 
 
 class AddRMSNorm(torch.nn.Module):
